@@ -20,7 +20,8 @@ __all__ = [
     "twell_ffn_bwd_workspace_bytes", "twell_ffn_bwd_noalloc",
     "nm_prune", "ffn_up_relu_nm", "nm_ffn_down", "twell_sync_status", "twell_row_max_histogram",
     "twell_stash_bytes", "twell_choose_slots", "twell_to_row_ell", "twell_row_nnz_histogram",
-    "twell_choose_row_ell_width", "F32", "BF16",
+    "twell_choose_row_ell_width", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+    "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "F32", "BF16",
 ]
 
 F32, BF16 = 0, 1
@@ -33,6 +34,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtwell.so
 
 _c = ctypes
 _P, _I, _F, _Z = _c.c_void_p, _c.c_int32, _c.c_float, _c.c_size_t
+_L = _c.c_int64
 
 
 class TwellError(RuntimeError):
@@ -78,6 +80,12 @@ _SIGS = {
     "twell_row_max_histogram": ([_P, _P, _P], _I),
     "twell_stash_bytes": ([_I, _I, _I, _I, _I, _I], _Z),
     "twell_choose_slots": ([_P, _I, _I, _I, _I, _I, _P], _I),
+    "layer_norm_fwd": ([_P, _L, _P, _L, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _P, _P], _I),
+    "layer_norm_bwd_workspace_bytes": ([_I, _I], _Z),
+    "layer_norm_bwd": ([_P, _L, _I, _P, _L, _I, _P, _P, _P, _P, _L, _I, _I, _P, _I, _P, _P, _P, _Z, _P], _I),
+    "grad_norm_workspace_bytes": ([_I], _Z),
+    "grad_norm": ([_P, _P, _P, _I, _P, _P, _Z, _P], _I),
+    "grad_clip": ([_P, _P, _P, _P, _P, _I, _F, _P, _P, _Z, _P], _I),
 }
 
 _LIB = None
@@ -124,6 +132,30 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t, d: int):
+    """(pointer, row stride) of a [T][d] tensor whose rows are contiguous."""
+    if t is None:
+        return None, d
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    if t.dim() != 2 or t.shape[1] != d:
+        raise ValueError(f"expected [T][{d}], got {tuple(t.shape)}")
+    if t.shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError("the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else d
+
+
+def _vec(t, n: int, name: str, dtype=torch.float32):
+    """Pointer of an optional contiguous [n] vector."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
+    return _ptr(t)
 
 
 def _stream(device=None):
@@ -477,3 +509,99 @@ def twell_to_row_ell(src: TwellMatrix, width: int, ovf_cap: int, val_dtype: torc
     ms, md = src.c(), out.c()
     _check(lib().twell_to_row_ell(_c.byref(ms), _c.byref(md), _stream(src.counts.device)), "twell_to_row_ell")
     return out
+
+
+def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, y_dtype: torch.dtype | None = None,
+                   want_stats: bool = True):
+    """Layer norm of s = x + residual (s = x without one) over the rows of x [T][d]: returns
+    (y, s, mean, rstd), mean and rstd fp32 [T] (None unless want_stats). weight and bias are
+    fp32; y has x's dtype unless y_dtype is given; s is x itself where there is no residual. x and
+    residual may have a row stride (a multiple of 8 elements)."""
+    T, d = x.shape
+    if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
+        raise TypeError("residual must have x's dtype and shape")
+    y = torch.empty((T, d), dtype=y_dtype or x.dtype, device=x.device)
+    s = torch.empty((T, d), dtype=x.dtype, device=x.device) if residual is not None else x
+    mean = torch.empty((T,), dtype=torch.float32, device=x.device) if want_stats else None
+    rstd = torch.empty((T,), dtype=torch.float32, device=x.device) if want_stats else None
+    (xp, ldx), (rp, ldr) = _rows(x, d), _rows(residual, d)
+    _check(lib().layer_norm_fwd(xp, ldx, rp, ldr, _vec(weight, d, "weight"), _vec(bias, d, "bias"), _dt(x.dtype), T, d,
+                                eps, _ptr(y), _dt(y.dtype), _ptr(s) if residual is not None else None, _ptr(mean),
+                                _ptr(rstd), _stream(x.device)), "layer_norm_fwd")
+    return y, s, mean, rstd
+
+
+def layer_norm_bwd_workspace_bytes(T: int, d: int) -> int:
+    return lib().layer_norm_bwd_workspace_bytes(T, d)
+
+
+def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype | None = None,
+                   want_bias: bool = True, workspace: torch.Tensor | None = None):
+    """Gradients (dx, dweight, dbias) of layer_norm_fwd for dy [T][d] (fp32 or bf16, whatever s
+    is); dres: the gradient that reaches s past the norm, in dx's dtype (default s's), added to
+    dx. dweight and dbias are fp32; dbias is None unless want_bias."""
+    T, d = s.shape
+    dev = s.device
+    dx = torch.empty((T, d), dtype=dx_dtype or s.dtype, device=dev)
+    if dy.shape != s.shape or (dres is not None and dres.shape != s.shape):
+        raise ValueError("dy and dres must have s's shape")
+    if dres is not None and dres.dtype != dx.dtype:
+        raise TypeError("dres must have dx's dtype")
+    dw = torch.empty((d,), dtype=torch.float32, device=dev)
+    db = torch.empty((d,), dtype=torch.float32, device=dev) if want_bias else None
+    need = layer_norm_bwd_workspace_bytes(T, d)
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    (yp, lddy), (sp, lds), (rp, lddr) = _rows(dy, d), _rows(s, d), _rows(dres, d)
+    _check(lib().layer_norm_bwd(yp, lddy, _dt(dy.dtype), sp, lds, _dt(s.dtype), _vec(weight, d, "weight"),
+                                _vec(mean, T, "mean"), _vec(rstd, T, "rstd"), rp, lddr, T, d, _ptr(dx), _dt(dx.dtype),
+                                _ptr(dw), _ptr(db), _ptr(workspace),
+                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                _stream(dev)), "layer_norm_bwd")
+    return dx, dw, db
+
+
+def grad_norm_workspace_bytes(n: int) -> int:
+    return lib().grad_norm_workspace_bytes(n)
+
+
+def _grad_call(grads, outs, max_norm, norm, workspace):
+    grads = list(grads)
+    n = len(grads)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise TypeError("norm must be one float32")
+    dev = norm.device
+    if any(g.device != dev for g in grads):
+        raise ValueError("all gradients must live on one GPU")
+    if workspace is None:
+        workspace = torch.empty((max(grad_norm_workspace_bytes(n), 16),), dtype=torch.uint8, device=dev)
+    ptrs = (_P * max(n, 1))(*[_ptr(g) for g in grads])
+    sizes = (_L * max(n, 1))(*[g.numel() for g in grads])
+    types = (_I * max(n, 1))(*[_dt(g.dtype) for g in grads])
+    wb = workspace.numel() * workspace.element_size()
+    if outs is None:
+        _check(lib().grad_norm(ptrs, sizes, types, n, _ptr(norm), _ptr(workspace), wb, _stream(dev)), "grad_norm")
+        return norm
+    if len(outs) != n or any(o.shape != g.shape or o.device != dev for o, g in zip(outs, grads)):
+        raise ValueError("out must match the gradients' shapes and device")
+    optrs = (_P * max(n, 1))(*[_ptr(o) for o in outs])
+    otypes = (_I * max(n, 1))(*[_dt(o.dtype) for o in outs])
+    _check(lib().grad_clip(ptrs, optrs, sizes, types, otypes, n, float(max_norm), _ptr(norm), _ptr(workspace), wb,
+                           _stream(dev)), "grad_clip")
+    return norm
+
+
+def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The L2 norm over all elements of the gradients (fp32 and bf16 tensors, mixed): a device
+    fp32 scalar."""
+    return _grad_call(grads, None, 0.0, norm, workspace)
+
+
+def grad_clip(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), norm over all of them: in place,
+    or into ``out`` (tensors of the same shapes, fp32 or bf16). Returns (norm, out)."""
+    outs = list(grads) if out is None else list(out)
+    return _grad_call(grads, outs, max_norm, norm, workspace), outs

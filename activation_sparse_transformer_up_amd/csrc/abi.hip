@@ -611,6 +611,111 @@ int twell_to_row_ell(const twell_matrix_t *src, twell_matrix_t *dst, void *strea
   return TWELL_OK;
 }
 
+// A row stride: at least d, and whole 16-byte units, so that every row starts aligned.
+static bool ld_ok(int64_t ld, int32_t d) { return ld >= d && ld % 8 == 0; }
+
+int layer_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, const float *w, const float *b,
+                   int32_t x_dtype, int32_t T, int32_t d, float eps, void *y, int32_t y_dtype, void *s, float *mean,
+                   float *rstd, void *stream) {
+  if (!w || (T > 0 && (!x || !y)) || (T > 0 && residual && !s)) return TWELL_ERR_ARG;
+  if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || !(eps >= 0.f)) return TWELL_ERR_ARG;
+  if (T < 0 || d <= 0) return TWELL_ERR_SHAPE;
+  if (d % 8) return TWELL_ERR_ALIGN;
+  if (T > 1 && (ldx < d || (residual && ldr < d))) return TWELL_ERR_SHAPE;
+  if (T > 1 && (!ld_ok(ldx, d) || (residual && !ld_ok(ldr, d)))) return TWELL_ERR_ALIGN;
+  if (!al16(x) || !al16(residual) || !al16(w) || !al16(b) || !al16(y) || !al16(s) || !al4(mean) || !al4(rstd))
+    return TWELL_ERR_ALIGN;
+  if (d > kNormMaxD) return TWELL_ERR_UNSUPPORTED;
+  if (T == 0) return TWELL_OK;
+  NormFwd a;
+  a.x = x; a.res = residual; a.ldx = ldx; a.ldr = ldr;
+  a.w = w; a.b = b;
+  a.rows = T; a.d = d; a.eps = eps;
+  a.x_bf16 = x_dtype == TWELL_BF16; a.y_bf16 = y_dtype == TWELL_BF16;
+  a.y = y; a.s = s; a.mean = mean; a.rstd = rstd;
+  TW_TRY(launch_norm_fwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+size_t layer_norm_bwd_workspace_bytes(int32_t T, int32_t d) {
+  if (T <= 0 || d <= 0) return 0;
+  const int p = norm_bwd_strips(T);
+  return p > 1 ? (size_t)p * 2 * d * sizeof(float) : 0;
+}
+
+int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s, int64_t lds, int32_t x_dtype,
+                   const float *w, const float *mean, const float *rstd, const void *dres, int64_t lddr, int32_t T,
+                   int32_t d, void *dx, int32_t dx_dtype, float *dw, float *db, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+  if (!w || !dw || (T > 0 && (!dy || !s || !mean || !rstd || !dx))) return TWELL_ERR_ARG;
+  if (!dtype_ok(x_dtype) || !dtype_ok(dy_dtype) || !dtype_ok(dx_dtype)) return TWELL_ERR_ARG;
+  if (T < 0 || d <= 0) return TWELL_ERR_SHAPE;
+  if (d % 8) return TWELL_ERR_ALIGN;
+  if (T > 1 && (lddy < d || lds < d || (dres && lddr < d))) return TWELL_ERR_SHAPE;
+  if (T > 1 && (!ld_ok(lddy, d) || !ld_ok(lds, d) || (dres && !ld_ok(lddr, d)))) return TWELL_ERR_ALIGN;
+  if (!al16(dy) || !al16(s) || !al16(w) || !al16(dres) || !al16(dx) || !al16(dw) || !al16(db) || !al4(mean) ||
+      !al4(rstd))
+    return TWELL_ERR_ALIGN;
+  if (d > kNormMaxD) return TWELL_ERR_UNSUPPORTED;
+  const size_t need = layer_norm_bwd_workspace_bytes(T, d);
+  if (need && (!workspace || workspace_bytes < need)) return TWELL_ERR_WORKSPACE;
+  if (need && !al16(workspace)) return TWELL_ERR_ALIGN;
+  if (T == 0) {                             // no rows: the sums over them are zero
+    TW_TRY(launch_zero_i32((int32_t *)dw, d, S(stream)));
+    if (db) TW_TRY(launch_zero_i32((int32_t *)db, d, S(stream)));
+    return TWELL_OK;
+  }
+  NormBwd a;
+  a.dy = dy; a.s = s; a.dres = dres; a.lddy = lddy; a.lds = lds; a.lddr = lddr;
+  a.w = w; a.mean = mean; a.rstd = rstd;
+  a.rows = T; a.d = d;
+  a.x_bf16 = x_dtype == TWELL_BF16; a.dy_bf16 = dy_dtype == TWELL_BF16; a.dx_bf16 = dx_dtype == TWELL_BF16;
+  a.dx = dx; a.dw = dw; a.db = db; a.part = (float *)workspace;
+  TW_TRY(launch_norm_bwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+size_t grad_norm_workspace_bytes(int32_t n) { return n > 0 ? grad_workspace_bytes(n) : 0; }
+
+// Shared checks of grad_norm and grad_clip (outs == NULL: the norm only).
+static int grad_run(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *dtypes,
+                    const int32_t *out_dtypes, int32_t n, float max_norm, float *norm, void *workspace,
+                    size_t workspace_bytes, hipStream_t s) {
+  if (n < 0) return TWELL_ERR_SHAPE;
+  if (!norm || (n > 0 && (!grads || !sizes || !dtypes))) return TWELL_ERR_ARG;
+  if (!al4(norm)) return TWELL_ERR_ALIGN;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] < 0) return TWELL_ERR_SHAPE;
+    if (!dtype_ok(dtypes[i]) || (out_dtypes && !dtype_ok(out_dtypes[i]))) return TWELL_ERR_ARG;
+    if (sizes[i] == 0) continue;
+    if (!grads[i] || (outs && !outs[i])) return TWELL_ERR_ARG;
+    if (outs && outs[i] == grads[i] && out_dtypes[i] != dtypes[i]) return TWELL_ERR_ARG;
+    if ((uintptr_t)grads[i] % (dtypes[i] == TWELL_BF16 ? 2 : 4)) return TWELL_ERR_ALIGN;
+    if (outs && (uintptr_t)outs[i] % (out_dtypes[i] == TWELL_BF16 ? 2 : 4)) return TWELL_ERR_ALIGN;
+    // chunks of the whole set are counted in 32 bits
+    if (sizes[i] > ((int64_t)1 << 40) || (total += sizes[i]) > ((int64_t)1 << 40)) return TWELL_ERR_UNSUPPORTED;
+  }
+  if (n > 0 && (!workspace || workspace_bytes < grad_workspace_bytes(n))) return TWELL_ERR_WORKSPACE;
+  if (n > 0 && !al16(workspace)) return TWELL_ERR_ALIGN;
+  GradArgs a;
+  a.g = grads; a.out = outs; a.len = sizes; a.dtype = dtypes; a.out_dtype = out_dtypes;
+  a.n = n; a.max_norm = max_norm; a.norm = norm; a.part = (double *)workspace;
+  return hip_status(launch_grad(a, s));
+}
+
+int grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n, float *norm,
+              void *workspace, size_t workspace_bytes, void *stream) {
+  return grad_run(grads, nullptr, sizes, dtypes, nullptr, n, 0.f, norm, workspace, workspace_bytes, S(stream));
+}
+
+int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *dtypes,
+              const int32_t *out_dtypes, int32_t n, float max_norm, float *norm, void *workspace,
+              size_t workspace_bytes, void *stream) {
+  if (!(max_norm >= 0.f) || (n > 0 && (!outs || !out_dtypes))) return TWELL_ERR_ARG;
+  return grad_run(grads, outs, sizes, dtypes, out_dtypes, n, max_norm, norm, workspace, workspace_bytes, S(stream));
+}
+
 int twell_sync_status(const twell_matrix_t *h, void *stream) {
   if (!h || !h->ovf_n) return TWELL_ERR_ARG;
   if (hipStreamSynchronize(S(stream)) != hipSuccess) return TWELL_ERR_HIP;

@@ -151,4 +151,43 @@ hipError_t launch_finish_dec(int bf16, const TwellIn &h, const uint32_t *bits, i
                              int32_t *ovf_rows, int32_t *ovf_slot, const void *x, const void *w1t, const float *b1,
                              int K, void *dense, hipStream_t s);
 
+// norm.hip: layer norm of `rows` rows of d (d a multiple of 8, at most kNormMaxD)
+constexpr int kNormMaxD = 16384;
+struct NormFwd {
+  const void *x, *res;
+  int64_t ldx, ldr;       // row strides in elements
+  const float *w, *b;
+  int rows, d, x_bf16, y_bf16;
+  float eps;
+  void *y, *s;
+  float *mean, *rstd;
+};
+hipError_t launch_norm_fwd(const NormFwd &a, hipStream_t s);
+struct NormBwd {
+  const void *dy, *s, *dres;
+  int64_t lddy, lds, lddr;
+  const float *w, *mean, *rstd;
+  int rows, d, x_bf16, dy_bf16, dx_bf16;
+  void *dx;
+  float *dw, *db, *part;  // part: [norm_bwd_strips(rows)][2][d], unused where that is 1
+};
+int norm_bwd_strips(int rows);
+hipError_t launch_norm_bwd(const NormBwd &a, hipStream_t s);
+
+// grad.hip: the norm (out == NULL), or the norm and the clipped gradients. The host arrays are
+// read during the call only; a launch takes kGradTab tensors in its arguments.
+constexpr int kGradTab = 64;
+struct GradArgs {
+  const void *const *g;
+  void *const *out;
+  const int64_t *len;
+  const int32_t *dtype, *out_dtype;
+  int n;
+  float max_norm;
+  float *norm;
+  double *part;
+};
+size_t grad_workspace_bytes(int n);
+hipError_t launch_grad(const GradArgs &a, hipStream_t s);
+
 }  // namespace tw

@@ -440,6 +440,64 @@ int twell_choose_row_ell_width(const int32_t *hist, int32_t nbins, int32_t rows,
                                int32_t ovf_cap, int32_t val_dtype, size_t *stash_bytes);
 
 /*
+ * Layer norm of T token rows of d (the norm in front of the feed-forward layer), with the
+ * residual add of a pre-norm block on either side.
+ *
+ * layer_norm_fwd —
+ *   s = x + residual (rounded to x_dtype; s = x and not written where residual is NULL)
+ *   mean = mean(s), rstd = 1 / sqrt(mean((s - mean)^2) + eps)            [T] fp32
+ *   y = (s - mean) rstd w + b                                            [T][d] y_dtype
+ * x, residual: [T][d] in x_dtype, rows ldx and ldr elements apart (ld >= d, ld % 8 == 0; not
+ * looked at for T = 1); w, b: [d] fp32 (b may be NULL: no shift); s: [T][d] in x_dtype,
+ * required with a residual; mean, rstd may be NULL (inference). eps >= 0. T == 0 does nothing.
+ *
+ * layer_norm_bwd — with xh = (s - mean) rstd and g = dy w:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + dres                       [T][d] dx_dtype
+ *   dw = sum_t dy xh, db = sum_t dy                                      [d] fp32
+ * dy in dy_dtype; s (the forward's s, or x) in x_dtype; dres: the residual stream's own
+ * gradient in dx_dtype, or NULL; db may be NULL. The sums over tokens are taken in a fixed order
+ * (the same bits on every call). The workspace (layer_norm_bwd_workspace_bytes; 0 for a few
+ * rows, then it may be NULL) need not be initialised. T == 0 writes zeros to dw and db.
+ *
+ * Errors of both: TWELL_ERR_ARG (null, dtype, eps), TWELL_ERR_SHAPE (T < 0, d <= 0, ld < d),
+ * TWELL_ERR_ALIGN (d % 8, ld % 8, pointers), TWELL_ERR_WORKSPACE, TWELL_ERR_UNSUPPORTED
+ * (d > 16384: a workgroup holds a whole row). Infinities and NaN stay in their own row of y and
+ * dx; they reach all of dw and db.
+ */
+int layer_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, const float *w,
+                   const float *b, int32_t x_dtype, int32_t T, int32_t d, float eps, void *y,
+                   int32_t y_dtype, void *s, float *mean, float *rstd, void *stream);
+size_t layer_norm_bwd_workspace_bytes(int32_t T, int32_t d);
+int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s, int64_t lds,
+                   int32_t x_dtype, const float *w, const float *mean, const float *rstd,
+                   const void *dres, int64_t lddr, int32_t T, int32_t d, void *dx,
+                   int32_t dx_dtype, float *dw, float *db, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * Global gradient norm and clipping over n tensors. grads, outs, sizes (elements), dtypes and
+ * out_dtypes are HOST arrays of length n, read during the call only; the tensors are device
+ * memory, contiguous, aligned to their element (16-byte aligned ones take wider accesses). A size
+ * of 0 (pointer ignored) and n = 0 are allowed.
+ *
+ * grad_norm — *norm (device, fp32) = sqrt(sum of g^2 over all tensors), summed in fp64 in a
+ * fixed order (the same bits on every call). Infinities and NaN reach the norm.
+ * grad_clip — the same, then out_i = c g_i with c = min(1, max_norm / (norm + 1e-6)) in fp32,
+ * rounded to out_dtype. outs[i] may be grads[i] (in place, same dtype; nothing is then written
+ * where c is 1), or must not overlap any gradient. A NaN or infinite norm makes c NaN or 0, and
+ * the outputs follow from the products. max_norm >= 0.
+ * Errors: TWELL_ERR_ARG (null, dtype, max_norm negative or NaN), TWELL_ERR_SHAPE (negative n or
+ * size), TWELL_ERR_ALIGN, TWELL_ERR_WORKSPACE (grad_norm_workspace_bytes; contents need not be
+ * initialised), TWELL_ERR_UNSUPPORTED (more than 2^40 elements in all).
+ */
+size_t grad_norm_workspace_bytes(int32_t n);
+int grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n,
+              float *norm, void *workspace, size_t workspace_bytes, void *stream);
+int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+              const int32_t *dtypes, const int32_t *out_dtypes, int32_t n, float max_norm,
+              float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * twell_sync_status — waits for `stream`, then reads *ovf_n: TWELL_ERR_OVF_CAPACITY if it
  * exceeds ovf_cap, TWELL_OK otherwise (TWELL_ERR_HIP if the wait or copy fails).
  */
