@@ -21,6 +21,7 @@ __all__ = [
     "nm_prune", "ffn_up_relu_nm", "nm_ffn_down", "twell_sync_status", "twell_row_max_histogram",
     "twell_stash_bytes", "twell_choose_slots", "twell_to_row_ell", "twell_row_nnz_histogram",
     "twell_choose_row_ell_width", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+    "linear_xent_fwd", "linear_xent_fwd_bwd", "linear_xent_workspace_bytes",
     "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "F32", "BF16",
 ]
 
@@ -83,6 +84,9 @@ _SIGS = {
     "layer_norm_fwd": ([_P, _L, _P, _L, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _P, _P], _I),
     "layer_norm_bwd_workspace_bytes": ([_I, _I], _Z),
     "layer_norm_bwd": ([_P, _L, _I, _P, _L, _I, _P, _P, _P, _P, _L, _I, _I, _P, _I, _P, _P, _P, _Z, _P], _I),
+    "linear_xent_workspace_bytes": ([_I, _I, _I, _I, _I], _Z),
+    "linear_xent_fwd": ([_P, _L, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "linear_xent_fwd_bwd": ([_P, _L, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "grad_norm_workspace_bytes": ([_I], _Z),
     "grad_norm": ([_P, _P, _P, _I, _P, _P, _Z, _P], _I),
     "grad_clip": ([_P, _P, _P, _P, _P, _I, _F, _P, _P, _Z, _P], _I),
@@ -559,6 +563,49 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype |
                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                 _stream(dev)), "layer_norm_bwd")
     return dx, dw, db
+
+
+def linear_xent_workspace_bytes(T: int, d: int, V: int, dtype=torch.bfloat16, want_grad: bool = True) -> int:
+    return lib().linear_xent_workspace_bytes(T, d, V, _dt(dtype), int(want_grad))
+
+
+def _xent_io(x, w, targets, workspace, want_grad):
+    T, d = x.shape
+    V = w.shape[0]
+    if w.dtype != x.dtype:
+        raise TypeError("x and w must share a dtype")
+    if w.dim() != 2 or w.shape[1] != d:
+        raise ValueError(f"w must be [V][{d}], got {tuple(w.shape)}")
+    if workspace is None:
+        need = linear_xent_workspace_bytes(T, d, V, x.dtype, want_grad)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=x.device)
+    loss = torch.empty((T,), dtype=torch.float32, device=x.device)
+    lse = torch.empty((T,), dtype=torch.float32, device=x.device)
+    return T, d, V, _vec(targets, T, "targets", torch.int64), workspace, loss, lse
+
+
+def linear_xent_fwd(x, w, targets, workspace: torch.Tensor | None = None):
+    """Cross entropy of softmax(x w^T) against targets (int64 [T]; negative: token left out):
+    (loss, lse), fp32 [T]. x [T][d] may have a row stride; w [V][d] in x's dtype."""
+    T, d, V, tp, workspace, loss, lse = _xent_io(x, w, targets, workspace, False)
+    xp, ldx = _rows(x, d)
+    _check(lib().linear_xent_fwd(xp, ldx, _ptr(w), tp, _dt(x.dtype), T, d, V, _ptr(loss), _ptr(lse), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(x.device)), "linear_xent_fwd")
+    return loss, lse
+
+
+def linear_xent_fwd_bwd(x, w, targets, dloss, workspace: torch.Tensor | None = None):
+    """The same with the gradients of sum(dloss * loss) (dloss fp32 [T]): (loss, lse, dx, dw), dx
+    and dw in x's dtype. No [T][V] array of logits is formed."""
+    T, d, V, tp, workspace, loss, lse = _xent_io(x, w, targets, workspace, True)
+    dx = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    dw = torch.empty((V, d), dtype=x.dtype, device=x.device)
+    xp, ldx = _rows(x, d)
+    _check(lib().linear_xent_fwd_bwd(xp, ldx, _ptr(w), tp, _vec(dloss, T, "dloss"), _dt(x.dtype), T, d, V, _ptr(loss),
+                                     _ptr(lse), _ptr(dx), _ptr(dw), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(x.device)),
+           "linear_xent_fwd_bwd")
+    return loss, lse, dx, dw
 
 
 def grad_norm_workspace_bytes(n: int) -> int:

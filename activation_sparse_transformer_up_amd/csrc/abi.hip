@@ -675,6 +675,69 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
   return TWELL_OK;
 }
 
+// the tiles of w and of the kept exponentials are addressed with 32-bit byte offsets
+static constexpr int kXentMaxV = 1 << 21, kXentMaxT = 1 << 24, kXentMaxD = 1 << 16;
+
+static int xent_shape(int32_t T, int32_t d, int32_t V) {
+  if (T < 0 || d <= 0 || V <= 0) return TWELL_ERR_SHAPE;
+  if (d % 8) return TWELL_ERR_ALIGN;
+  if (T > kXentMaxT || d > kXentMaxD || V > kXentMaxV) return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+size_t linear_xent_workspace_bytes(int32_t T, int32_t d, int32_t V, int32_t dtype, int32_t want_grad) {
+  if (T <= 0 || !dtype_ok(dtype) || xent_shape(T, d, V) != TWELL_OK) return 0;
+  return xent_workspace_bytes(T, d, V, dtype == TWELL_BF16, want_grad != 0);
+}
+
+static int xent_check(const XentArgs &a, int32_t dtype, bool grad, size_t workspace_bytes) {
+  if (!a.w || (a.T > 0 && (!a.x || !a.y || !a.loss || !a.lse))) return TWELL_ERR_ARG;
+  if (grad && (!a.dw || (a.T > 0 && (!a.dx || !a.dloss)))) return TWELL_ERR_ARG;
+  if (!dtype_ok(dtype)) return TWELL_ERR_ARG;
+  const int st = xent_shape(a.T, a.d, a.V);
+  if (st) return st;
+  if (a.T > 1 && a.ldx < a.d) return TWELL_ERR_SHAPE;
+  if (a.T > 1 && !ld_ok(a.ldx, a.d)) return TWELL_ERR_ALIGN;
+  if (!al16(a.x) || !al16(a.w) || !al16(a.dx) || !al16(a.dw) || ((uintptr_t)a.y & 7u) || !al4(a.loss) || !al4(a.lse) ||
+      !al4(a.dloss))
+    return TWELL_ERR_ALIGN;
+  if (a.T == 0) return TWELL_OK;
+  if (!a.ws || workspace_bytes < xent_workspace_bytes(a.T, a.d, a.V, a.bf16, grad)) return TWELL_ERR_WORKSPACE;
+  if (!al16(a.ws)) return TWELL_ERR_ALIGN;
+  return TWELL_OK;
+}
+
+static XentArgs xent_args(const void *x, int64_t ldx, const void *w, const int64_t *targets, int32_t dtype, int32_t T,
+                          int32_t d, int32_t V, float *loss, float *lse, void *workspace) {
+  XentArgs a = {};
+  a.x = x; a.w = w; a.ldx = ldx; a.y = targets;
+  a.T = T; a.d = d; a.V = V; a.bf16 = dtype == TWELL_BF16;
+  a.loss = loss; a.lse = lse;
+  a.ws = workspace;
+  return a;
+}
+
+int linear_xent_fwd(const void *x, int64_t ldx, const void *w, const int64_t *targets, int32_t dtype, int32_t T,
+                    int32_t d, int32_t V, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+  const XentArgs a = xent_args(x, ldx, w, targets, dtype, T, d, V, loss, lse, workspace);
+  const int st = xent_check(a, dtype, false, workspace_bytes);
+  if (st || T == 0) return st;
+  TW_TRY(launch_xent(a, S(stream)));
+  return TWELL_OK;
+}
+
+int linear_xent_fwd_bwd(const void *x, int64_t ldx, const void *w, const int64_t *targets, const float *dloss,
+                        int32_t dtype, int32_t T, int32_t d, int32_t V, float *loss, float *lse, void *dx, void *dw,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+  XentArgs a = xent_args(x, ldx, w, targets, dtype, T, d, V, loss, lse, workspace);
+  a.dloss = dloss; a.dx = dx; a.dw = dw;
+  const int st = xent_check(a, dtype, true, workspace_bytes);
+  if (st) return st;
+  TW_TRY(launch_xent(a, S(stream)));
+  return TWELL_OK;
+}
+
 size_t grad_norm_workspace_bytes(int32_t n) { return n > 0 ? grad_workspace_bytes(n) : 0; }
 
 // Shared checks of grad_norm and grad_clip (outs == NULL: the norm only).

@@ -190,4 +190,18 @@ struct GradArgs {
 size_t grad_workspace_bytes(int n);
 hipError_t launch_grad(const GradArgs &a, hipStream_t s);
 
+// xent.hip: loss and lse of T rows; with dw also dx and dw (all in the operands' type)
+struct XentArgs {
+  const void *x, *w;
+  int64_t ldx;
+  const int64_t *y;
+  int T, d, V, bf16;
+  float *loss, *lse;
+  const float *dloss;
+  void *dx, *dw;
+  void *ws;
+};
+size_t xent_workspace_bytes(int T, int d, int V, int bf16, bool grad);
+hipError_t launch_xent(const XentArgs &a, hipStream_t s);
+
 }  // namespace tw

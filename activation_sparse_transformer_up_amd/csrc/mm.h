@@ -1,0 +1,234 @@
+// Matrix products on gfx950 matrix cores with either operand stored along k or across it.
+//
+//   D[m][n] = sum_k A(m, k) B(n, k),   bf16 operands, fp32 accumulators
+//
+// An operand "along k" has rows of consecutive k (A[m][k]); one "across k" has rows of
+// consecutive m (A[k][m]), as the gradients' products need it, and is turned on the way from
+// LDS to registers (ds_read_b64_tr_b16), so that no transposed copy is ever made.
+//
+// A workgroup computes BM x BN, a wave WM x WN of 16 x 16 blocks (v_mfma_f32_16x16x32_bf16).
+// Every stage of the LDS ring holds 32 k of both operands, moved straight from HBM by loads that
+// write LDS (lane l of a wave fills bytes [16 l, 16 l + 16) of a 1 KB block); NS - 1 stages are
+// in flight while one is multiplied. Where the stage lies in LDS:
+//   along k:   row r at 64 r, its 16-byte chunk c at c ^ ((r >> 2) & 3)
+//   across k:  k row j at 2 BX j, its 32-byte chunk c at c ^ swz(j)
+// Both keep the 32 lanes of a half-wave's fragment read on different banks: along k the 16 rows
+// of a quarter start in 16 bank groups; across k the 8 k rows that a half-wave reads (its lane i
+// brings 8 bytes of k row 8 (i / 16) + i % 16 / 4) land in 8 different 32-byte groups.
+// Elements outside the operands read as zeros (a byte offset beyond the buffer's range), so
+// ragged sizes need no branches.
+//
+// fp32 operands come as three bf16 planes (hi + mid + lo, 24 bits, exact) and the loop runs over
+// the six products of planes that reach 2^-24 of the largest, smallest first: fp32 accuracy at a
+// sixth of the bf16 rate, which is above the rate of the fp32 matrix instructions (1/16).
+#pragma once
+#include "common.h"
+#include "stage.h"
+
+namespace tw {
+
+template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> struct MM {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr bool ATR = ATR_, BTR = BTR_;
+  static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, NT = NW * 64;
+  static constexpr int FM = WM / 16, FN = WN / 16;
+  static constexpr int KS = 32;                           // k per stage
+  static constexpr int A_BYTES = BM * KS * 2, STAGE = (BM + BN) * KS * 2, SMEM = NS * STAGE;
+  static constexpr int LPW = STAGE / 1024 / NW;           // 1 KB wave-loads per wave and stage
+  static constexpr int A_BLK = A_BYTES / 1024;            // 1 KB blocks of A in a stage, then B's
+  static_assert(STAGE % (1024 * NW) == 0 && NS >= 3, "tile");
+};
+
+// p: element (first row of the tile, k = 0) for an operand along k, (k = 0, first column of the
+// tile) for one across k; ld: elements between rows; n: rows (columns) of the tile that exist (a
+// multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand.
+struct MmOperand {
+  const uint16_t *p;
+  int64_t ld, plane;
+  int n;
+};
+
+// The six products of planes, smallest first: (lo, hi) (hi, lo) (mid, mid) (mid, hi) (hi, mid)
+// (hi, hi), as planes 0 = hi, 1 = mid, 2 = lo.
+TW_DEV int mm_plane_a(int term) { return term == 0 ? 2 : term == 2 || term == 3 ? 1 : 0; }
+TW_DEV int mm_plane_b(int term) { return term == 1 ? 2 : term == 2 || term == 4 ? 1 : 0; }
+
+template <int BX> TW_DEV int mm_swz(int j) {
+  if constexpr (BX == 256) return (j & 3) | ((j >> 3) & 3) << 2;
+  else if constexpr (BX == 128) return (j & 3) | ((j >> 3) & 1) << 2;
+  else return ((j >> 1) & 1) | ((j >> 3) & 1) << 1;
+}
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
+// A wave's 16-row fragment at row r0 of a staged operand (BX rows): lane l gets row r0 + l % 16,
+// k = 8 (l / 16) .. + 7.
+template <int BX, bool TR> TW_DEV u32x4_t mm_frag(const char *st, int r0, int lane) {
+  if constexpr (!TR) {
+    const int r = r0 + (lane & 15);
+    return *(const u32x4_t *)(st + r * 64 + (((lane >> 4) ^ ((r >> 2) & 3)) << 4));
+  } else {
+    static_assert(BX == 256 || BX == 128 || BX == 64, "swizzle");
+    const int j = 8 * (lane >> 4) + ((lane & 15) >> 2);   // the +4 below leaves swz(j) as it is
+    const char *a = st + j * (2 * BX) + (((r0 >> 4) ^ mm_swz<BX>(j)) << 5) + ((lane & 3) << 3);
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)a);
+    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(a + 4 * 2 * BX));
+    u32x4_t v;
+    __builtin_memcpy(&v, &lo, 8);
+    __builtin_memcpy((char *)&v + 8, &hi, 8);
+    return v;
+  }
+}
+
+// acc += A B^T over k in [0, K) (NP = 1: bf16 operands; NP = 6: three planes each). smem: G::SMEM
+// bytes; every wave of the workgroup calls it, and no wave may touch smem afterwards before a
+// barrier. One barrier per stage:
+//   wait for stage kt + 1's loads, barrier
+//   products of stage kt's fragments, between them the reads of stage kt + 1's fragments (into the
+//   other set) and the loads of stage kt + NS - 1
+// The stage overwritten by those loads, (kt - 1) mod NS, was read during step kt - 2, and the
+// barrier that follows a wave's reads waits for them (lgkmcnt).
+template <class G, int NP>
+TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc)[G::FM][G::FN], char *smem) {
+  constexpr int NM = G::FM * G::FN, NR = G::FM + G::FN;
+  constexpr int RI = NM / NR >= 2 ? NM / NR : 1;          // a fragment read after every RI products
+  constexpr int DI = NM / G::LPW >= 1 ? NM / G::LPW : 1;  // a stage load after every DI products
+  constexpr uint32_t OOB = 0x80000000u;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+
+  uint32_t voff[G::LPW];                                  // this lane's byte offset in each load
+  int kof[G::LPW];                                        // and the k (row) it starts at
+  bool isA[G::LPW];
+#pragma unroll
+  for (int i = 0; i < G::LPW; ++i) {
+    const int q = wave + G::NW * i;                       // 1 KB block of the stage
+    isA[i] = G::A_BLK % G::NW == 0 ? i * G::NW < G::A_BLK : q < G::A_BLK;
+    auto place = [&](const MmOperand &o, int blk, auto tr, auto bx) {
+      if constexpr (!decltype(tr)::value) {
+        const int r = blk * 16 + (lane >> 2), c = (lane & 3) ^ ((r >> 2) & 3);
+        kof[i] = c * 8;
+        voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 8) * 2 : OOB;
+      } else {
+        constexpr int BX = decltype(bx)::value, LR = BX / 8;          // lanes per k row
+        const int j = blk * (64 / LR) + lane / LR, pc = lane % LR;
+        const int col = ((pc >> 1) ^ mm_swz<BX>(j)) * 16 + (pc & 1) * 8;
+        kof[i] = j;
+        voff[i] = col < o.n ? (uint32_t)(j * o.ld + col) * 2 : OOB;
+      }
+    };
+    if (isA[i]) place(A, q, std::integral_constant<bool, G::ATR>(), std::integral_constant<int, G::BM>());
+    else place(B, q - G::A_BLK, std::integral_constant<bool, G::BTR>(), std::integral_constant<int, G::BN>());
+  }
+  const int nk1 = (K + G::KS - 1) / G::KS;                // stages of one product of planes
+  const int nk = nk1 * NP;
+  if (nk == 0) return;
+
+  int lt = 0, lk = 0;                                     // term and k of the next stage to load
+  auto issue1 = [&](int kt, int i) {
+    char *dst = smem + (kt % G::NS) * G::STAGE + (wave + G::NW * i) * 1024;
+    const uint32_t vo = lk + kof[i] < K ? voff[i] : OOB;
+    const uint16_t *base;
+    if (isA[i]) base = A.p + (NP > 1 ? mm_plane_a(lt) * A.plane : 0) + (G::ATR ? (int64_t)lk * A.ld : lk);
+    else base = B.p + (NP > 1 ? mm_plane_b(lt) * B.plane : 0) + (G::BTR ? (int64_t)lk * B.ld : lk);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)dst, 16, vo, 0, 0, 0);
+  };
+  auto issued = [&]() {
+    lk += G::KS;
+    if (NP > 1 && lk >= K) {
+      lk = 0;
+      ++lt;
+    }
+  };
+  typedef u32x4_t FA[G::FM];
+  typedef u32x4_t FB[G::FN];
+  auto read1 = [&](int kt, int j, FA &a, FB &b) {
+    const char *st = smem + (kt % G::NS) * G::STAGE;
+    if (j < G::FM) a[j] = mm_frag<G::BM, G::ATR>(st, wm * G::WM + j * 16, lane);
+    else b[j - G::FM] = mm_frag<G::BN, G::BTR>(st + G::A_BYTES, wn * G::WN + (j - G::FM) * 16, lane);
+  };
+  auto mma = [&](int i, const FA &a, const FB &b) {
+    acc[i / G::FN][i % G::FN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8_t, a[i / G::FN]), __builtin_bit_cast(bf16x8_t, b[i % G::FN]),
+        acc[i / G::FN][i % G::FN], 0, 0, 0);
+  };
+  for (int st = 0; st < G::NS - 1 && st < nk; ++st) {
+#pragma unroll
+    for (int i = 0; i < G::LPW; ++i) issue1(st, i);
+    issued();
+  }
+  if (nk >= G::NS - 1) wait_vmcnt<(G::NS - 2) * G::LPW>();
+  else wait_vmcnt<0>();
+  block_barrier();
+  FA a0, a1;
+  FB b0, b1;
+#pragma unroll
+  for (int j = 0; j < NR; ++j) read1(0, j, a0, b0);
+  // step kt < nk - 1; LOAD: stage kt + NS - 1 exists and is loaded in this step
+  auto step = [&](int kt, const FA &ac, const FB &bc, FA &an, FB &bn, auto load_tag) {
+    constexpr bool LOAD = decltype(load_tag)::value;
+    if (LOAD) wait_vmcnt<(G::NS - 3) * G::LPW>();         // stage kt + 1 has landed
+    else wait_vmcnt<0>();
+    block_barrier_lds();
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<NM>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      mma(i, ac, bc);
+      if constexpr (i % RI == 0 && i / RI < NR) read1(kt + 1, i / RI, an, bn);
+      if constexpr (LOAD && i % DI == DI - 1 && i / DI < G::LPW) issue1(kt + G::NS - 1, i / DI);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr ((NM + RI - 1) / RI < NR)
+#pragma unroll
+      for (int j = (NM + RI - 1) / RI; j < NR; ++j) read1(kt + 1, j, an, bn);
+    if constexpr (LOAD && NM / DI < G::LPW)
+#pragma unroll
+      for (int i = NM / DI; i < G::LPW; ++i) issue1(kt + G::NS - 1, i);
+    if (LOAD) issued();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<bool, true> ld;
+  const std::integral_constant<bool, false> nold;
+  auto settle = [&]() {                                   // next fragment set -> current (tail only)
+#pragma unroll
+    for (int j = 0; j < G::FM; ++j) a0[j] = a1[j];
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) b0[j] = b1[j];
+  };
+  const int nl = nk >= G::NS ? nk - G::NS + 1 : 0;        // steps that load
+  int kt = 0;
+  for (; kt + 1 < nl; kt += 2) {
+    step(kt, a0, b0, a1, b1, ld);
+    step(kt + 1, a1, b1, a0, b0, ld);
+  }
+  if (kt < nl) {
+    step(kt, a0, b0, a1, b1, ld);
+    settle();
+    ++kt;
+  }
+  for (; kt + 1 < nk; ++kt) {
+    step(kt, a0, b0, a1, b1, nold);
+    settle();
+  }
+#pragma unroll
+  for (int i = 0; i < NM; ++i) mma(i, a0, b0);
+}
+
+// Workgroup b of `total` tiles -> tile. The XCDs take workgroups in turn (b % 8), each its own
+// L2: every XCD gets a contiguous run of tiles, so that neighbours share operand rows there. A
+// launch has 8 ceil(total / 8) workgroups; those past the end get -1.
+TW_DEV int mm_xcd_tile(int b, int total) {
+  const int per = (total + 7) / 8, t = (b & 7) * per + (b >> 3);
+  return (b >> 3) < per && t < total ? t : -1;
+}
+// Tile -> (m, n) in groups of GM m tiles: within a group all n of the m's before the next, so
+// that the 32 tiles in flight on an XCD form a block of about GM x 32 / GM.
+template <int GM> TW_DEV void mm_tile_mn(int t, int mt, int nt, int &m, int &n) {
+  const int g = t / (GM * nt), m0 = g * GM, gm = mt - m0 < GM ? mt - m0 : GM, r = t - m0 * nt;
+  m = m0 + r % gm;
+  n = r / gm;
+}
+
+}  // namespace tw

@@ -1,0 +1,513 @@
+// Softmax cross entropy of a large vocabulary, straight from the hidden states x [T][d] and the
+// head's weights w [V][d], forward and with its gradients, on gfx950 matrix cores.
+//
+//   z = x w^T;  lse = log sum_j exp z_j;  loss = lse - z_target
+//   G = (exp(z - lse) - onehot(target)) dloss;  dx = G w;  dw = G^T x
+//
+// The three products (2 T V d operations each) bound it. The logits live in accumulators only:
+// the first product's epilogue reduces a tile's block of PW vocabulary columns to (max, sum of
+// exp) per token, and for a gradient leaves e = exp(z - block max) in the operand type, which
+// costs no more accuracy than rounding G itself for the next product (a bf16 e is off by 2^-9
+// of itself whatever the size of z, where a bf16 z would be off by 2^-9 |z|). Once a row's
+// blocks are joined, one pass turns e into G in place; the target's element is formed from the
+// fp32 logit instead, so that p - 1 of a token the model is sure of keeps its digits.
+//
+// Tokens without a target (negative) take no part: the rows with one are gathered first, in
+// order, and all products run over that list (its length stays on the device; workgroups beyond
+// it leave at once). Whatever such rows hold, also NaN, reaches nothing.
+//
+// Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is; dw is summed
+// over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h).
+#include "launch.h"
+#include "mm.h"
+#include "row8.h"
+
+namespace tw {
+namespace {
+
+typedef uint16_t bf16_t;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// ------------------------------------------------------------------------------ rows, planes
+
+// list[i] = i-th token with a target, pos[t] = its place or -1, *n_act = their number. One
+// workgroup: every thread counts a contiguous run of tokens, the counts are scanned.
+__global__ __launch_bounds__(1024) void k_xent_rows(const int64_t *__restrict__ y, int T, int32_t *__restrict__ list,
+                                                    int32_t *__restrict__ pos, int32_t *__restrict__ n_act) {
+  __shared__ int wsum[16];
+  const int per = (T + 1023) / 1024, t0 = min(T, (int)threadIdx.x * per), t1 = min(T, t0 + per);
+  int c = 0;
+  for (int t = t0; t < t1; ++t) c += y[t] >= 0;
+  int total;
+  int at = wave_excl_scan(c, &total);
+  if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = total;
+  __syncthreads();
+  int all = 0;
+  for (int i = 0; i < 16; ++i) {
+    if (i < (int)(threadIdx.x >> 6)) at += wsum[i];
+    all += wsum[i];
+  }
+  for (int t = t0; t < t1; ++t) {
+    const bool a = y[t] >= 0;
+    pos[t] = a ? at : -1;
+    if (a) list[at++] = t;
+  }
+  if (threadIdx.x == 0) *n_act = all;
+}
+
+// Splits 8 fp32 values into three bf16 planes, hi + mid + lo = v (24 bits; rounded to nearest,
+// so mid and lo are at most 2^-9 and 2^-18 of v).
+TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
+  float h[8], r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    h[k] = rounded<bf16_t>(v[k]);
+    r[k] = v[k] - h[k];
+  }
+  store8(p, h);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    h[k] = rounded<bf16_t>(r[k]);
+    r[k] -= h[k];
+  }
+  store8(p + plane, h);
+  store8(p + 2 * plane, r);
+}
+
+// Token blockIdx.x: with a target, its row of x into the gathered operand (fp32: three planes);
+// without, zeros to its loss, lse and row of dx.
+template <typename T, typename DXT>
+__global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int64_t ldx, int d,
+                                                    const int32_t *__restrict__ pos, bf16_t *__restrict__ xc,
+                                                    int64_t plane, float *__restrict__ loss, float *__restrict__ lse,
+                                                    DXT *__restrict__ dx) {
+  const int t = blockIdx.x, p = pos[t];
+  if (p < 0) {
+    if (threadIdx.x == 0) {
+      loss[t] = 0.f;
+      lse[t] = 0.f;
+    }
+    const float z[8] = {};
+    if (dx)
+      for (int i = threadIdx.x * 8; i < d; i += 256 * 8) store8(dx + (size_t)t * d + i, z);
+    return;
+  }
+  for (int i = threadIdx.x * 8; i < d; i += 256 * 8) {
+    if constexpr (std::is_same<T, float>::value) {
+      float v[8];
+      load8(x + t * ldx + i, v);
+      split8(v, xc + (size_t)p * d + i, plane);
+    } else {
+      *(uint4 *)(xc + (size_t)p * d + i) = *(const uint4 *)(x + t * ldx + i);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_xent_planes(const float *__restrict__ w, size_t n, bf16_t *__restrict__ out) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float v[8];
+  load8(w + i, v);
+  split8(v, out + i, (int64_t)n);
+}
+
+// ------------------------------------------------------------------------------------ logits
+
+// Tokens [row0, row0 + R) of the list that exist.
+TW_DEV int piece_rows(const int32_t *n_act, int row0, int R) { return min(max(*n_act - row0, 0), R); }
+
+// D[vocabulary][token] = w x^T: a lane holds 4 consecutive logits of a token per block, so that a
+// token's maximum and sum are taken over a lane's registers and two exchanges, and e is stored 4
+// elements at a time. part[token][block of WM columns] = (max, sum of exp(z - max)).
+template <class G, int NP, typename ET, bool KEEP>
+__global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict__ w, int64_t wplane,
+                                                       const bf16_t *__restrict__ xc, int64_t xplane,
+                                                       const int64_t *__restrict__ y, const int32_t *__restrict__ list,
+                                                       const int32_t *__restrict__ n_act, int row0, int R, int V, int d,
+                                                       int mt, int nt, ET *__restrict__ e, int64_t lde,
+                                                       float2 *__restrict__ part, int nblk, float *__restrict__ zt) {
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  const int t = mm_xcd_tile(blockIdx.x, mt * nt);
+  if (t < 0) return;
+  int m, n;
+  mm_tile_mn<8>(t, mt, nt, m, n);
+  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  if (n0 >= rows) return;
+  f32x4_t acc[G::FM][G::FN];
+#pragma unroll
+  for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
+  const MmOperand A = {w + (size_t)m0 * d, d, wplane, min(V - m0, G::BM)};
+  const MmOperand B = {xc + (size_t)(row0 + n0) * d, d, xplane, min(rows - n0, G::BN)};
+  mm_loop<G, NP>(A, B, d, acc, smem);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+  const int v0 = m0 + wm * G::WM, blk = v0 / G::WM;       // this wave's block of the vocabulary
+#pragma unroll
+  for (int fn = 0; fn < G::FN; ++fn) {
+    const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);          // row of the piece
+    const bool ok = r < rows;
+    const int64_t off = ok ? y[list[row0 + r]] - v0 : -1;
+    const int tgt = off >= 0 && off < G::WM ? (int)off : -1;        // column of the block
+    float mx = -INFINITY;
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = fm * 16 + grp * 4 + i;
+        if (v0 + c >= V) acc[fm][fn][i] = -INFINITY;
+        if (c == tgt) zt[row0 + r] = acc[fm][fn][i];
+        mx = fmaxf(mx, acc[fm][fn][i]);
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float ref = mx == -INFINITY ? 0.f : mx;         // a block past the vocabulary: e = 0
+    float s = 0.f;
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = acc[fm][fn][i] - ref;
+        if constexpr (NP == 1) v[i] = __builtin_amdgcn_exp2f(x * kLog2e);
+        else v[i] = expf(x);
+        s += v[i];
+      }
+      if constexpr (KEEP) {
+        if (ok) {
+          ET *p = e + (size_t)r * lde + v0 + fm * 16 + grp * 4;
+          if constexpr (std::is_same<ET, float>::value) *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+          else *(uint2 *)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        }
+      }
+    }
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (ok && grp == 0) part[(size_t)r * nblk + blk] = make_float2(mx, s);
+  }
+}
+
+// Row of a piece: joins its blocks to lse and loss; for a gradient turns its e into G (zero in
+// the padding, where e is 0). A target beyond the vocabulary makes loss and G NaN.
+template <typename ET, bool GRAD, int PW>
+__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, const float *__restrict__ zt,
+                                                   const int64_t *__restrict__ y, const int32_t *__restrict__ list,
+                                                   const int32_t *__restrict__ n_act, int row0, int R, int V,
+                                                   const float *__restrict__ dloss, ET *__restrict__ e, int64_t lde,
+                                                   bf16_t *__restrict__ g, int64_t gplane, float *__restrict__ loss,
+                                                   float *__restrict__ lse) {
+  __shared__ float red[8];
+  const int r = blockIdx.x, wave = threadIdx.x >> 6;
+  if (r >= piece_rows(n_act, row0, R)) return;
+  const float2 *p = part + (size_t)r * nblk;
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < nblk; i += 256) mx = fmaxf(mx, p[i].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  if ((threadIdx.x & 63) == 0) red[wave] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < nblk; i += 256) s += p[i].y * expf(p[i].x - ref);
+  s = wave_sumf(s);
+  if ((threadIdx.x & 63) == 0) red[4 + wave] = s;
+  __syncthreads();
+  const float l = ref + logf((red[4] + red[5]) + (red[6] + red[7]));
+  const int t = list[row0 + r];
+  const int64_t tgt = y[t];
+  const bool bad = tgt >= V;
+  const float z = bad ? NAN : zt[row0 + r];
+  if (threadIdx.x == 0) {
+    lse[t] = l;
+    loss[t] = l - z;
+  }
+  if constexpr (GRAD) {
+    const float dl = bad ? NAN : dloss[t];
+    for (int i = threadIdx.x * 8; i < lde; i += 256 * 8) {
+      // one block covers the 8 columns (PW is a multiple of 8)
+      const int b = i / PW;
+      const float f = b < nblk ? expf(p[b].x - l) * dl : 0.f;
+      float v[8];
+      load8(e + (size_t)r * lde + i, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = i + k < V ? v[k] * f : 0.f;
+        if (i + k == tgt) v[k] = expm1f(z - l) * dl;
+      }
+      if constexpr (std::is_same<ET, float>::value) {
+        split8(v, g + (size_t)r * lde + i, gplane);
+      } else {
+        *(uint4 *)(e + (size_t)r * lde + i) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                         pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------- gradients
+
+// dx: D[column of d][token] = w^T G^T over the vocabulary range of split blockIdx.x / tiles
+// (w across k, G along k). One split: to the token's row of dx; several: fp32 partial sums.
+template <class G, int NP, typename DXT>
+__global__ __launch_bounds__(G::NT) void k_xent_dx(const bf16_t *__restrict__ w, int64_t wplane,
+                                                   const bf16_t *__restrict__ g, int64_t lde, int64_t gplane,
+                                                   const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
+                                                   int row0, int R, int V, int d, int mt, int nt, int S, int ks,
+                                                   DXT *__restrict__ dx, float *__restrict__ part) {
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  const int t = mm_xcd_tile(blockIdx.x, mt * nt * S);
+  if (t < 0) return;
+  int m, n;
+  const int sp = t / (mt * nt);
+  mm_tile_mn<8>(t % (mt * nt), mt, nt, m, n);
+  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  if (n0 >= rows) return;
+  f32x4_t acc[G::FM][G::FN];
+#pragma unroll
+  for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
+  const int k0 = sp * ks, k1 = min(V, k0 + ks);
+  const MmOperand A = {w + (size_t)k0 * d + m0, d, wplane, min(d - m0, G::BM)};
+  const MmOperand B = {g + (size_t)n0 * lde + k0, lde, gplane, min(rows - n0, G::BN)};
+  if (k0 < k1) mm_loop<G, NP>(A, B, k1 - k0, acc, smem);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+#pragma unroll
+  for (int fn = 0; fn < G::FN; ++fn) {
+    const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);
+    if (r >= rows) continue;
+    const size_t at = S == 1 ? (size_t)list[row0 + r] * d : ((size_t)sp * R + r) * d;
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) {
+      const int c = m0 + wm * G::WM + fm * 16 + (lane >> 4) * 4;
+      if (c >= d) continue;                               // d is a multiple of 8
+      const f32x4_t v = acc[fm][fn];
+      if (S > 1) *(f32x4_t *)(part + at + c) = v;
+      else if constexpr (std::is_same<DXT, float>::value) *(f32x4_t *)(dx + at + c) = v;
+      else *(uint2 *)(dx + at + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+  }
+}
+
+template <typename DXT>
+__global__ __launch_bounds__(256) void k_xent_dx_sum(const float *__restrict__ part, int S, int R, int d,
+                                                     const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
+                                                     int row0, DXT *__restrict__ dx) {
+  const int cb = (d / 8 + 255) / 256, r = blockIdx.x / cb, c = (blockIdx.x % cb * 256 + threadIdx.x) * 8;
+  if (r >= piece_rows(n_act, row0, R) || c >= d) return;
+  float a[8] = {};
+  for (int s = 0; s < S; ++s) {
+    float v[8];
+    load8(part + ((size_t)s * R + r) * d + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] += v[k];
+  }
+  store8(dx + (size_t)list[row0 + r] * d + c, a);
+}
+
+// dw: D[column of d][vocabulary] = x^T G over the piece's tokens (both across k). sum: fp32 sums
+// of the pieces so far (added where `add`, written where dw is NULL; may be dw itself).
+template <class G, int NP, typename DWT>
+__global__ __launch_bounds__(G::NT) void k_xent_dw(const bf16_t *__restrict__ xc, int64_t xplane,
+                                                   const bf16_t *__restrict__ g, int64_t lde, int64_t gplane,
+                                                   const int32_t *__restrict__ n_act, int row0, int R, int V, int d, int mt,
+                                                   int nt, bool add, float *sum, DWT *dw) {
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  const int t = mm_xcd_tile(blockIdx.x, mt * nt);
+  if (t < 0) return;
+  int m, n;
+  mm_tile_mn<8>(t, mt, nt, m, n);
+  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  f32x4_t acc[G::FM][G::FN];
+#pragma unroll
+  for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
+  const MmOperand A = {xc + (size_t)row0 * d + m0, d, xplane, min(d - m0, G::BM)};
+  // the padding of G's rows up to lde is zero
+  const MmOperand B = {g + n0, lde, gplane, (int)min(lde - n0, (int64_t)G::BN)};
+  mm_loop<G, NP>(A, B, rows, acc, smem);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+#pragma unroll
+  for (int fn = 0; fn < G::FN; ++fn) {
+    const int v = n0 + wn * G::WN + fn * 16 + (lane & 15);
+    if (v >= V) continue;
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) {
+      const int c = m0 + wm * G::WM + fm * 16 + (lane >> 4) * 4;
+      if (c >= d) continue;
+      const size_t at = (size_t)v * d + c;
+      f32x4_t a = acc[fm][fn];
+      if (add) a += *(const f32x4_t *)(sum + at);
+      if (!dw) *(f32x4_t *)(sum + at) = a;
+      else if constexpr (std::is_same<DWT, float>::value) *(f32x4_t *)(dw + at) = a;
+      else *(uint2 *)(dw + at) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t n) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------------------------- plan
+
+// Tiles: 8 waves of 64 x 128 for many tokens; for at most 64 the products are bound by the
+// stream of w: a 64 x 64 tile with a ring of 8 stages keeps 28 KB of it in flight per workgroup.
+typedef MM<256, 256, 64, 128, 4, false, false> TileZ;     // logits
+typedef MM<64, 64, 16, 64, 8, false, false> TileZS;
+typedef MM<256, 256, 64, 128, 4, true, false> TileX;      // dx
+typedef MM<256, 64, 64, 64, 4, true, false> TileXS;
+typedef MM<256, 256, 64, 128, 4, true, true> TileW;       // dw
+
+constexpr int kFewRows = 64;
+constexpr size_t kPieceBytes = (size_t)1 << 30;
+
+struct Plan {
+  int R, pieces, nblk, S, ks, np;
+  int64_t lde;
+  bool few, sums;
+  size_t list, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;        // offsets of the workspace
+};
+
+Plan plan_of(int T, int d, int V, int bf16, bool grad) {
+  Plan p = {};
+  p.np = bf16 ? 1 : 6;
+  p.few = T <= kFewRows;
+  p.lde = ((int64_t)V + 255) / 256 * 256;
+  p.nblk = (int)(p.lde / (p.few ? TileZS::WM : TileZ::WM));
+  const size_t planes = bf16 ? 1 : 3;
+  // rows of a piece: as many as kPieceBytes hold of what a row keeps between the launches. bf16
+  // gradients of several pieces need dw's sums in fp32; where all rows at once take no more
+  // memory than that, there is one piece.
+  const size_t row = (size_t)p.nblk * 8 + (grad ? (size_t)p.lde * (bf16 ? 2 : 10) : 0);
+  const size_t sums = grad && bf16 ? (size_t)V * d * 4 : 0;
+  const int64_t all = ((int64_t)T + 255) / 256 * 256;
+  int64_t R = (int64_t)(kPieceBytes / row) / 256 * 256;
+  if (R < 256) R = 256;
+  if (R >= all || (size_t)all * row <= kPieceBytes + sums) R = all;
+  p.R = p.few ? kFewRows : (int)R;
+  p.pieces = (T + p.R - 1) / p.R;
+  p.sums = sums && p.pieces > 1;
+  // dx: the vocabulary is split until the launch has two workgroups per CU
+  const int tiles = p.few ? (d + 255) / 256 : (int)(((int64_t)d + 255) / 256 * (p.R / 256));
+  p.S = tiles >= 512 ? 1 : 512 / tiles;
+  const int most = (int)(p.lde / 256);
+  if (p.S > most) p.S = most;
+  if (p.S > 32) p.S = 32;
+  p.ks = (int)((p.lde / 256 + p.S - 1) / p.S) * 256;
+  p.S = (int)((p.lde + p.ks - 1) / p.ks);
+  size_t at = 256;                                        // n_act
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  p.list = take((size_t)T * 4);
+  p.pos = take((size_t)T * 4);
+  p.zt = take((size_t)T * 4);
+  p.xc = take((size_t)T * d * 2 * planes);
+  if (!bf16) p.wp = take((size_t)V * d * 2 * planes);
+  p.part = take((size_t)p.R * p.nblk * 8);
+  if (grad) {
+    p.e = take((size_t)p.R * p.lde * (bf16 ? 2 : 4));
+    if (!bf16) p.g = take((size_t)p.R * p.lde * 6);
+    if (p.S > 1) p.dxp = take((size_t)p.S * p.R * d * 4);
+    if (p.sums) p.sum = take((size_t)V * d * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
+
+template <class Z, class X, typename T, typename ET, typename DXT, typename DWT, int NP>
+hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
+  char *ws = (char *)a.ws;
+  int32_t *n_act = (int32_t *)ws, *list = (int32_t *)(ws + p.list), *pos = (int32_t *)(ws + p.pos);
+  float *zt = (float *)(ws + p.zt);
+  bf16_t *xc = (bf16_t *)(ws + p.xc);
+  float2 *part = (float2 *)(ws + p.part);
+  ET *e = (ET *)(ws + p.e);
+  bf16_t *g = NP == 1 ? (bf16_t *)e : (bf16_t *)(ws + p.g);
+  const int64_t xplane = (int64_t)a.T * a.d, wplane = (int64_t)a.V * a.d, gplane = (int64_t)p.R * p.lde;
+  const bool grad = a.dw != nullptr;
+  k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, list, pos, n_act);
+  TW_TRY_HIP(hipGetLastError());
+  k_xent_stage<T, DXT><<<a.T, 256, 0, s>>>((const T *)a.x, a.ldx, a.d, pos, xc, xplane, a.loss, a.lse, (DXT *)a.dx);
+  TW_TRY_HIP(hipGetLastError());
+  const bf16_t *w = (const bf16_t *)a.w;
+  if constexpr (NP > 1) {
+    const size_t n = (size_t)a.V * a.d;
+    k_xent_planes<<<(unsigned)((n / 8 + 255) / 256), 256, 0, s>>>((const float *)a.w, n, (bf16_t *)(ws + p.wp));
+    TW_TRY_HIP(hipGetLastError());
+    w = (const bf16_t *)(ws + p.wp);
+  }
+  for (int q = 0; q < p.pieces; ++q) {
+    const int row0 = q * p.R, R = a.T - row0 < p.R ? a.T - row0 : p.R;
+    {
+      const int mt = (int)(p.lde / Z::BM), nt = (R + Z::BN - 1) / Z::BN;
+      auto go = [&](auto keep) {
+        k_xent_logits<Z, NP, ET, decltype(keep)::value><<<grid8((int64_t)mt * nt), Z::NT, 0, s>>>(
+            w, wplane, xc, xplane, a.y, list, n_act, row0, R, a.V, a.d, mt, nt, e, p.lde, part, p.nblk, zt);
+      };
+      if (grad) go(std::integral_constant<bool, true>());
+      else go(std::integral_constant<bool, false>());
+      TW_TRY_HIP(hipGetLastError());
+    }
+    if (grad)
+      k_xent_join<ET, true, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, a.y, list, n_act, row0, R, a.V, a.dloss, e, p.lde,
+                                                     g, gplane, a.loss, a.lse);
+    else
+      k_xent_join<ET, false, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, a.y, list, n_act, row0, R, a.V, nullptr, e, p.lde,
+                                                      g, gplane, a.loss, a.lse);
+    TW_TRY_HIP(hipGetLastError());
+    if (!grad) continue;
+    {
+      const int mt = (a.d + X::BM - 1) / X::BM, nt = (R + X::BN - 1) / X::BN;
+      float *dxp = p.S > 1 ? (float *)(ws + p.dxp) : nullptr;
+      k_xent_dx<X, NP, DXT><<<grid8((int64_t)mt * nt * p.S), X::NT, 0, s>>>(
+          w, wplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt, nt, p.S, p.ks, (DXT *)a.dx, dxp);
+      TW_TRY_HIP(hipGetLastError());
+      if (p.S > 1) {
+        k_xent_dx_sum<DXT><<<(unsigned)((a.d / 8 + 255) / 256 * R), 256, 0, s>>>(dxp, p.S, R, a.d, list, n_act, row0, (DXT *)a.dx);
+        TW_TRY_HIP(hipGetLastError());
+      }
+    }
+    const int mt = (a.d + TileW::BM - 1) / TileW::BM, nt = (a.V + TileW::BN - 1) / TileW::BN;
+    const bool last = q + 1 == p.pieces, f32 = std::is_same<DWT, float>::value;
+    float *sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
+    k_xent_dw<TileW, NP, DWT><<<grid8((int64_t)mt * nt), TileW::NT, 0, s>>>(
+        xc, xplane, g, p.lde, gplane, n_act, row0, R, a.V, a.d, mt, nt, q > 0, sum, last || f32 ? (DWT *)a.dw : nullptr);
+    TW_TRY_HIP(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int T, int d, int V, int bf16, bool grad) { return plan_of(T, d, V, bf16, grad).bytes; }
+
+hipError_t launch_xent(const XentArgs &a, hipStream_t s) {
+  if (a.T == 0) {                           // no tokens: dw is zero
+    const size_t n16 = (size_t)a.V * a.d * (a.bf16 ? 2 : 4) / 16;
+    k_xent_zero<<<(unsigned)((n16 + 255) / 256), 256, 0, s>>>((uint4 *)a.dw, n16);
+    return hipGetLastError();
+  }
+  const Plan p = plan_of(a.T, a.d, a.V, a.bf16, a.dw != nullptr);
+  if (a.bf16)
+    return p.few ? xent_run<TileZS, TileXS, bf16_t, bf16_t, bf16_t, bf16_t, 1>(a, p, s)
+                 : xent_run<TileZ, TileX, bf16_t, bf16_t, bf16_t, bf16_t, 1>(a, p, s);
+  return p.few ? xent_run<TileZS, TileXS, float, float, float, float, 6>(a, p, s)
+               : xent_run<TileZ, TileX, float, float, float, float, 6>(a, p, s);
+}
+
+}  // namespace tw

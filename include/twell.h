@@ -475,6 +475,40 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
                    size_t workspace_bytes, void *stream);
 
 /*
+ * Softmax cross entropy of a vocabulary of V, straight from hidden states and head weights; the
+ * [T][V] logits are never written.
+ *   z = x w^T (fp32 sums);  lse = log sum_j exp z_j;  loss = lse - z_target          [T] fp32
+ *   G = (exp(z - lse) - onehot(target)) dloss;  dx = G w [T][d];  dw = G^T x [V][d]
+ * x [T][d] (rows ldx elements apart, as for layer_norm_fwd) and w [V][d], dx and dw in dtype;
+ * targets [T] int64, dloss [T] fp32 (the loss's incoming gradient per token, e.g. 1 / tokens).
+ * A negative target takes its token out: loss, lse and its row of dx are 0, and its x and dloss,
+ * whatever they hold, reach nothing (the products run over the other tokens only). A target of V
+ * or more gives a NaN loss and, with gradients, NaN in its row of dx and in dw.
+ *
+ * linear_xent_fwd — loss and lse only (scoring). linear_xent_fwd_bwd — with both gradients.
+ * bf16: G is held in bf16 (two roundings per element off the target, one on it), the sums are
+ * fp32. fp32: operands and G are split into three bf16 parts, which carry all 24 bits. The same
+ * bits on every call.
+ *
+ * The workspace (linear_xent_workspace_bytes; contents need not be initialised) holds the
+ * exponentials of one piece of tokens, about 1 GiB at most (bf16: up to 1 GiB + 4 V d bytes, the
+ * size of dw's fp32 sums that several pieces need), a copy of x's rows and, for fp32, the parts of w.
+ * T == 0 writes zeros to dw (linear_xent_fwd: nothing).
+ * Errors: TWELL_ERR_ARG (null, dtype), TWELL_ERR_SHAPE (T < 0, d or V <= 0, ldx < d),
+ * TWELL_ERR_ALIGN (d % 8, ldx % 8, pointers), TWELL_ERR_WORKSPACE, TWELL_ERR_UNSUPPORTED
+ * (V > 2^21, T > 2^24, d > 2^16).
+ */
+size_t linear_xent_workspace_bytes(int32_t T, int32_t d, int32_t V, int32_t dtype,
+                                   int32_t want_grad);
+int linear_xent_fwd(const void *x, int64_t ldx, const void *w, const int64_t *targets,
+                    int32_t dtype, int32_t T, int32_t d, int32_t V, float *loss, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+int linear_xent_fwd_bwd(const void *x, int64_t ldx, const void *w, const int64_t *targets,
+                        const float *dloss, int32_t dtype, int32_t T, int32_t d, int32_t V,
+                        float *loss, float *lse, void *dx, void *dw, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
  * Global gradient norm and clipping over n tensors. grads, outs, sizes (elements), dtypes and
  * out_dtypes are HOST arrays of length n, read during the call only; the tensors are device
  * memory, contiguous, aligned to their element (16-byte aligned ones take wider accesses). A size

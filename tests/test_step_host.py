@@ -110,3 +110,38 @@ def test_grad_clip_rejects(kw, want):
 def test_grad_workspace():
     f = tw.lib().grad_norm_workspace_bytes
     assert f(0) == 0 and f(-4) == 0 and f(1) > 0 and f(64) == f(1) and f(65) == 2 * f(1)
+
+
+XENT_F = dict(x=FAKE, ldx=64, w=FAKE, y=FAKE, dt=1, T=4, d=64, V=100, loss=FAKE, lse=FAKE, ws=FAKE, wb=1 << 30, stream=None)
+XENT_B = dict(x=FAKE, ldx=64, w=FAKE, y=FAKE, dl=FAKE, dt=1, T=4, d=64, V=100, loss=FAKE, lse=FAKE, dx=FAKE, dw=FAKE, ws=FAKE,
+              wb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("name", ["linear_xent_fwd", "linear_xent_fwd_bwd"])
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), ARG), (dict(w=None), ARG), (dict(y=None), ARG), (dict(loss=None), ARG), (dict(lse=None), ARG),
+    (dict(dt=2), ARG), (dict(T=-1), SHAPE), (dict(d=0), SHAPE), (dict(V=0), SHAPE), (dict(ldx=32), SHAPE),
+    (dict(d=63), ALIGN), (dict(ldx=65), ALIGN), (dict(x=MIS), ALIGN), (dict(w=MIS), ALIGN), (dict(y=MIS), ALIGN),
+    (dict(loss=MIS + 1), ALIGN), (dict(ws=None), WS), (dict(wb=1000), WS), (dict(ws=MIS), ALIGN),
+    (dict(V=(1 << 21) + 1), UNSUP), (dict(T=(1 << 24) + 1), UNSUP), (dict(d=(1 << 16) + 8, ldx=1 << 17), UNSUP),
+])
+def test_linear_xent(name, kw, want):
+    assert call(name, XENT_F if name == "linear_xent_fwd" else XENT_B, kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [(dict(dl=None), ARG), (dict(dx=None), ARG), (dict(dw=None), ARG), (dict(dx=MIS), ALIGN),
+                                     (dict(dw=MIS), ALIGN), (dict(dl=MIS + 2), ALIGN)])
+def test_linear_xent_gradients(kw, want):
+    assert call("linear_xent_fwd_bwd", XENT_B, kw) == want
+
+
+def test_linear_xent_empty_and_workspace():
+    assert call("linear_xent_fwd", XENT_F, dict(T=0, x=None, y=None, loss=None, lse=None, ws=None, wb=0)) == 0
+    f = tw.lib().linear_xent_workspace_bytes
+    assert f(0, 64, 100, 1, 1) == 0 and f(4, 60, 100, 1, 1) == 0 and f(4, 64, 100, 5, 1) == 0
+    assert 0 < f(4, 64, 100, 1, 0) < f(4, 64, 100, 1, 1) < f(4, 64, 100, 0, 1)
+    # what is kept between the launches is bounded, whatever the number of tokens: the growth past
+    # the first pieces is x's copy and the row lists
+    a, b = f(1 << 16, 512, 32000, 1, 1), f(1 << 20, 512, 32000, 1, 1)
+    assert b - a <= ((1 << 20) - (1 << 16)) * (512 * 2 + 12) + (1 << 20)
+    assert a <= (1 << 30) + 2 * 32000 * 512 * 4 + (1 << 16) * (512 * 2 + 12) + (1 << 26)
