@@ -10,11 +10,15 @@
 // Every stage of the LDS ring holds 32 k of both operands, moved straight from HBM by loads that
 // write LDS (lane l of a wave fills bytes [16 l, 16 l + 16) of a 1 KB block); NS - 1 stages are
 // in flight while one is multiplied. Where the stage lies in LDS:
-//   along k:   row r at 64 r, its 16-byte chunk c at c ^ ((r >> 2) & 3)
-//   across k:  k row j at 2 BX j, its 32-byte chunk c at c ^ swz(j)
-// Both keep the 32 lanes of a half-wave's fragment read on different banks: along k the 16 rows
-// of a quarter start in 16 bank groups; across k the 8 k rows that a half-wave reads (its lane i
-// brings 8 bytes of k row 8 (i / 16) + i % 16 / 4) land in 8 different 32-byte groups.
+//   along k:   row r at 64 r, its 16-byte chunk c at c ^ ((r >> 1) & 3)
+//   across k:  1 KB block q (k rows 2 q and 2 q + 1) at 1056 q, in it the 64-byte chunk c of an odd
+//              k row at c ^ 1
+// Both keep the lanes that LDS serves together on different banks (SQ_LDS_BANK_CONFLICT = 0).
+// Along k a 16-byte read serves lanes 0-3, 12-15 and 20-27 of a half-wave in one turn and the
+// others in the next: their 16 rows are r = 0 .. 15 once each, with two different c, and (r & 3,
+// c ^ ((r >> 1) & 3)) takes 16 values (with (r >> 2) in its place, 8: twice the time). Across k
+// the 8 k rows that a half-wave reads (its lane i brings 8 bytes of k row 8 (i / 16) + i % 16 / 4)
+// land in 8 different 32-byte groups.
 // Elements outside the operands read as zeros (a byte offset beyond the buffer's range), so
 // ragged sizes need no branches.
 //
@@ -27,16 +31,20 @@
 
 namespace tw {
 
+constexpr int kMmBlkTr = 1056;                            // bytes from block to block across k
+
 template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> struct MM {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr bool ATR = ATR_, BTR = BTR_;
   static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, NT = NW * 64;
   static constexpr int FM = WM / 16, FN = WN / 16;
   static constexpr int KS = 32;                           // k per stage
-  static constexpr int A_BYTES = BM * KS * 2, STAGE = (BM + BN) * KS * 2, SMEM = NS * STAGE;
-  static constexpr int LPW = STAGE / 1024 / NW;           // 1 KB wave-loads per wave and stage
-  static constexpr int A_BLK = A_BYTES / 1024;            // 1 KB blocks of A in a stage, then B's
-  static_assert(STAGE % (1024 * NW) == 0 && NS >= 3, "tile");
+  static constexpr int A_BLK = BM * KS * 2 / 1024, B_BLK = BN * KS * 2 / 1024;      // 1 KB blocks of a stage
+  static constexpr int LPW = (A_BLK + B_BLK) / NW;        // 1 KB wave-loads per wave and stage
+  static constexpr int A_BYTES = A_BLK * (ATR ? kMmBlkTr : 1024);
+  static constexpr int STAGE = A_BYTES + B_BLK * (BTR ? kMmBlkTr : 1024), SMEM = NS * STAGE;
+  static_assert((A_BLK + B_BLK) % NW == 0 && NS >= 3, "tile");
+  static_assert((!ATR || (BM == 256 && WM % 64 == 0)) && (!BTR || (BN == 256 && WN % 64 == 0)), "across k");
 };
 
 // p: element (first row of the tile, k = 0) for an operand along k, (k = 0, first column of the
@@ -53,27 +61,29 @@ struct MmOperand {
 TW_DEV int mm_plane_a(int term) { return term == 0 ? 2 : term == 2 || term == 3 ? 1 : 0; }
 TW_DEV int mm_plane_b(int term) { return term == 1 ? 2 : term == 2 || term == 4 ? 1 : 0; }
 
-template <int BX> TW_DEV int mm_swz(int j) {
-  if constexpr (BX == 256) return (j & 3) | ((j >> 3) & 3) << 2;
-  else if constexpr (BX == 128) return (j & 3) | ((j >> 3) & 1) << 2;
-  else return ((j >> 1) & 1) | ((j >> 3) & 1) << 1;
-}
-
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
-// A wave's 16-row fragment at row r0 of a staged operand (BX rows): lane l gets row r0 + l % 16,
-// k = 8 (l / 16) .. + 7.
-template <int BX, bool TR> TW_DEV u32x4_t mm_frag(const char *st, int r0, int lane) {
+// One turning read. The pointer is __restrict__ for the alias scope that this gives the builtin's
+// memory operand: without one the compiler takes the read for a user of every load into LDS that is
+// in flight and waits for all of them (vmcnt(0)), which stops the ring (dw at T = 8192, d = 4096, V =
+// 128000: 10.9 ms). mm_loop's own waits order the reads behind the loads of their stage.
+TW_DEV i16x4_t mm_read_tr(const lds_i16x4_t *__restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p);
+}
+
+// Fragment i of a wave (16 rows from w0 + 16 i) of a staged operand: lane l gets row l % 16, k =
+// 8 (l / 16) .. + 7. Across k, w0 is a multiple of 64: the exchange of chunks stays within i.
+template <bool TR> TW_DEV u32x4_t mm_frag(const char *st, int w0, int i, int lane) {
   if constexpr (!TR) {
-    const int r = r0 + (lane & 15);
-    return *(const u32x4_t *)(st + r * 64 + (((lane >> 4) ^ ((r >> 2) & 3)) << 4));
+    const int r = w0 + (lane & 15);
+    return *(const u32x4_t *)(st + r * 64 + (((lane >> 4) ^ ((r >> 1) & 3)) << 4) + i * 1024);
   } else {
-    static_assert(BX == 256 || BX == 128 || BX == 64, "swizzle");
-    const int j = 8 * (lane >> 4) + ((lane & 15) >> 2);   // the +4 below leaves swz(j) as it is
-    const char *a = st + j * (2 * BX) + (((r0 >> 4) ^ mm_swz<BX>(j)) << 5) + ((lane & 3) << 3);
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)a);
-    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(a + 4 * 2 * BX));
+    const int j = 8 * (lane >> 4) + ((lane & 15) >> 2);   // and j + 4, two blocks further
+    const char *a = st + j / 2 * kMmBlkTr + (j & 1) * 512 + w0 * 2 + (((i >> 1) ^ (j & 1)) << 6) + ((i & 1) << 5) +
+                    ((lane & 3) << 3);
+    const i16x4_t lo = mm_read_tr((const lds_i16x4_t *)a);
+    const i16x4_t hi = mm_read_tr((const lds_i16x4_t *)(a + 2 * kMmBlkTr));
     u32x4_t v;
     __builtin_memcpy(&v, &lo, 8);
     __builtin_memcpy((char *)&v + 8, &hi, 8);
@@ -100,27 +110,29 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
   const int wm = wave / G::NWN, wn = wave % G::NWN;
 
   uint32_t voff[G::LPW];                                  // this lane's byte offset in each load
-  int kof[G::LPW];                                        // and the k (row) it starts at
+  int kof[G::LPW];                                        // the k (row) it starts at
+  int dst[G::LPW];                                        // and the load's place in the stage
   bool isA[G::LPW];
 #pragma unroll
   for (int i = 0; i < G::LPW; ++i) {
     const int q = wave + G::NW * i;                       // 1 KB block of the stage
     isA[i] = G::A_BLK % G::NW == 0 ? i * G::NW < G::A_BLK : q < G::A_BLK;
-    auto place = [&](const MmOperand &o, int blk, auto tr, auto bx) {
+    auto place = [&](const MmOperand &o, int blk, auto tr) {
       if constexpr (!decltype(tr)::value) {
-        const int r = blk * 16 + (lane >> 2), c = (lane & 3) ^ ((r >> 2) & 3);
+        const int r = blk * 16 + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
         kof[i] = c * 8;
         voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 8) * 2 : OOB;
       } else {
-        constexpr int BX = decltype(bx)::value, LR = BX / 8;          // lanes per k row
-        const int j = blk * (64 / LR) + lane / LR, pc = lane % LR;
-        const int col = ((pc >> 1) ^ mm_swz<BX>(j)) * 16 + (pc & 1) * 8;
+        const int j = blk * 2 + (lane >> 5);
+        const int col = (((lane >> 2 & 7) ^ (j & 1)) * 32) + (lane & 3) * 8;
         kof[i] = j;
         voff[i] = col < o.n ? (uint32_t)(j * o.ld + col) * 2 : OOB;
       }
     };
-    if (isA[i]) place(A, q, std::integral_constant<bool, G::ATR>(), std::integral_constant<int, G::BM>());
-    else place(B, q - G::A_BLK, std::integral_constant<bool, G::BTR>(), std::integral_constant<int, G::BN>());
+    const int qb = q - G::A_BLK;
+    dst[i] = isA[i] ? q * (G::ATR ? kMmBlkTr : 1024) : G::A_BYTES + qb * (G::BTR ? kMmBlkTr : 1024);
+    if (isA[i]) place(A, q, std::integral_constant<bool, G::ATR>());
+    else place(B, qb, std::integral_constant<bool, G::BTR>());
   }
   const int nk1 = (K + G::KS - 1) / G::KS;                // stages of one product of planes
   const int nk = nk1 * NP;
@@ -128,12 +140,12 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
 
   int lt = 0, lk = 0;                                     // term and k of the next stage to load
   auto issue1 = [&](int kt, int i) {
-    char *dst = smem + (kt % G::NS) * G::STAGE + (wave + G::NW * i) * 1024;
+    char *at = smem + (kt % G::NS) * G::STAGE + dst[i];
     const uint32_t vo = lk + kof[i] < K ? voff[i] : OOB;
     const uint16_t *base;
-    if (isA[i]) base = A.p + (NP > 1 ? mm_plane_a(lt) * A.plane : 0) + (G::ATR ? (int64_t)lk * A.ld : lk);
-    else base = B.p + (NP > 1 ? mm_plane_b(lt) * B.plane : 0) + (G::BTR ? (int64_t)lk * B.ld : lk);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)dst, 16, vo, 0, 0, 0);
+    if (isA[i]) base = A.p + (NP > 1 ? mm_plane_a(lt) * A.plane : 0) + (G::ATR ? lk * A.ld : lk);
+    else base = B.p + (NP > 1 ? mm_plane_b(lt) * B.plane : 0) + (G::BTR ? lk * B.ld : lk);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)at, 16, vo, 0, 0, 0);
   };
   auto issued = [&]() {
     lk += G::KS;
@@ -146,8 +158,8 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
   typedef u32x4_t FB[G::FN];
   auto read1 = [&](int kt, int j, FA &a, FB &b) {
     const char *st = smem + (kt % G::NS) * G::STAGE;
-    if (j < G::FM) a[j] = mm_frag<G::BM, G::ATR>(st, wm * G::WM + j * 16, lane);
-    else b[j - G::FM] = mm_frag<G::BN, G::BTR>(st + G::A_BYTES, wn * G::WN + (j - G::FM) * 16, lane);
+    if (j < G::FM) a[j] = mm_frag<G::ATR>(st, wm * G::WM, j, lane);
+    else b[j - G::FM] = mm_frag<G::BTR>(st + G::A_BYTES, wn * G::WN, j - G::FM, lane);
   };
   auto mma = [&](int i, const FA &a, const FB &b) {
     acc[i / G::FN][i % G::FN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(

@@ -30,9 +30,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 // ------------------------------------------------------------------------------ rows, planes
 
-// list[i] = i-th token with a target, pos[t] = its place or -1, *n_act = their number. One
-// workgroup: every thread counts a contiguous run of tokens, the counts are scanned.
-__global__ __launch_bounds__(1024) void k_xent_rows(const int64_t *__restrict__ y, int T, int32_t *__restrict__ list,
+// list[i] = i-th token with a target, tgt[i] = its target (V where that is V or more), pos[t] = its
+// place or -1, *n_act = their number. One workgroup: every thread counts a contiguous run of
+// tokens, the counts are scanned.
+__global__ __launch_bounds__(1024) void k_xent_rows(const int64_t *__restrict__ y, int T, int V,
+                                                    int32_t *__restrict__ list, int32_t *__restrict__ tgt,
                                                     int32_t *__restrict__ pos, int32_t *__restrict__ n_act) {
   __shared__ int wsum[16];
   const int per = (T + 1023) / 1024, t0 = min(T, (int)threadIdx.x * per), t1 = min(T, t0 + per);
@@ -48,9 +50,12 @@ __global__ __launch_bounds__(1024) void k_xent_rows(const int64_t *__restrict__ 
     all += wsum[i];
   }
   for (int t = t0; t < t1; ++t) {
-    const bool a = y[t] >= 0;
-    pos[t] = a ? at : -1;
-    if (a) list[at++] = t;
+    const int64_t v = y[t];
+    pos[t] = v >= 0 ? at : -1;
+    if (v >= 0) {
+      tgt[at] = v < V ? (int)v : V;
+      list[at++] = t;
+    }
   }
   if (threadIdx.x == 0) *n_act = all;
 }
@@ -122,7 +127,7 @@ TW_DEV int piece_rows(const int32_t *n_act, int row0, int R) { return min(max(*n
 template <class G, int NP, typename ET, bool KEEP>
 __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict__ w, int64_t wplane,
                                                        const bf16_t *__restrict__ xc, int64_t xplane,
-                                                       const int64_t *__restrict__ y, const int32_t *__restrict__ list,
+                                                       const int32_t *__restrict__ tgt,
                                                        const int32_t *__restrict__ n_act, int row0, int R, int V, int d,
                                                        int mt, int nt, ET *__restrict__ e, int64_t lde,
                                                        float2 *__restrict__ part, int nblk, float *__restrict__ zt) {
@@ -145,34 +150,48 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
   const int wm = wave / G::NWN, wn = wave % G::NWN;
   const int v0 = m0 + wm * G::WM, blk = v0 / G::WM;       // this wave's block of the vocabulary
+  int toff[G::FN];                                        // each row's target as a column of the block
 #pragma unroll
   for (int fn = 0; fn < G::FN; ++fn) {
     const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);          // row of the piece
+    toff[fn] = r < rows ? tgt[row0 + r] - v0 : -1;
+  }
+  if (v0 + G::WM > V)                                     // the last block ends inside the vocabulary
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (v0 + fm * 16 + grp * 4 + i >= V)
+#pragma unroll
+          for (int fn = 0; fn < G::FN; ++fn) acc[fm][fn][i] = -INFINITY;
+#pragma unroll
+  for (int fn = 0; fn < G::FN; ++fn) {
+    const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);
     const bool ok = r < rows;
-    const int64_t off = ok ? y[list[row0 + r]] - v0 : -1;
-    const int tgt = off >= 0 && off < G::WM ? (int)off : -1;        // column of the block
+    if (ballot64((uint32_t)toff[fn] < (uint32_t)G::WM)) { // rare: one block in nblk has a row's target
+#pragma unroll
+      for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (fm * 16 + grp * 4 + i == toff[fn]) zt[row0 + r] = acc[fm][fn][i];
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = fm * 16 + grp * 4 + i;
-        if (v0 + c >= V) acc[fm][fn][i] = -INFINITY;
-        if (c == tgt) zt[row0 + r] = acc[fm][fn][i];
-        mx = fmaxf(mx, acc[fm][fn][i]);
-      }
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, acc[fm][fn][i]);
     mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
     const float ref = mx == -INFINITY ? 0.f : mx;         // a block past the vocabulary: e = 0
+    const float refl = ref * kLog2e;
     float s = 0.f;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) {
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float x = acc[fm][fn][i] - ref;
-        if constexpr (NP == 1) v[i] = __builtin_amdgcn_exp2f(x * kLog2e);
-        else v[i] = expf(x);
+        if constexpr (NP == 1) v[i] = __builtin_amdgcn_exp2f(fmaf(acc[fm][fn][i], kLog2e, -refl));
+        else v[i] = expf(acc[fm][fn][i] - ref);
         s += v[i];
       }
       if constexpr (KEEP) {
@@ -193,7 +212,7 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 // the padding, where e is 0). A target beyond the vocabulary makes loss and G NaN.
 template <typename ET, bool GRAD, int PW>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, const float *__restrict__ zt,
-                                                   const int64_t *__restrict__ y, const int32_t *__restrict__ list,
+                                                   const int32_t *__restrict__ tgts, const int32_t *__restrict__ list,
                                                    const int32_t *__restrict__ n_act, int row0, int R, int V,
                                                    const float *__restrict__ dloss, ET *__restrict__ e, int64_t lde,
                                                    bf16_t *__restrict__ g, int64_t gplane, float *__restrict__ loss,
@@ -216,8 +235,7 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   if ((threadIdx.x & 63) == 0) red[4 + wave] = s;
   __syncthreads();
   const float l = ref + logf((red[4] + red[5]) + (red[6] + red[7]));
-  const int t = list[row0 + r];
-  const int64_t tgt = y[t];
+  const int t = list[row0 + r], tgt = tgts[row0 + r];
   const bool bad = tgt >= V;
   const float z = bad ? NAN : zt[row0 + r];
   if (threadIdx.x == 0) {
@@ -375,7 +393,7 @@ struct Plan {
   int R, pieces, nblk, S, ks, np;
   int64_t lde;
   bool few, sums;
-  size_t list, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;        // offsets of the workspace
+  size_t list, tgt, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;        // offsets of the workspace
 };
 
 Plan plan_of(int T, int d, int V, int bf16, bool grad) {
@@ -412,8 +430,8 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
     return o;
   };
   p.list = take((size_t)T * 4);
-  p.pos = take((size_t)T * 4);
-  p.zt = take((size_t)T * 4);
+  p.tgt = take((size_t)T * 4);
+  p.pos = p.zt = take((size_t)T * 4);                     // pos is done with before zt begins
   p.xc = take((size_t)T * d * 2 * planes);
   if (!bf16) p.wp = take((size_t)V * d * 2 * planes);
   p.part = take((size_t)p.R * p.nblk * 8);
@@ -432,7 +450,8 @@ int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 template <class Z, class X, typename T, typename ET, typename DXT, typename DWT, int NP>
 hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   char *ws = (char *)a.ws;
-  int32_t *n_act = (int32_t *)ws, *list = (int32_t *)(ws + p.list), *pos = (int32_t *)(ws + p.pos);
+  int32_t *n_act = (int32_t *)ws, *list = (int32_t *)(ws + p.list), *tgt = (int32_t *)(ws + p.tgt);
+  int32_t *pos = (int32_t *)(ws + p.pos);
   float *zt = (float *)(ws + p.zt);
   bf16_t *xc = (bf16_t *)(ws + p.xc);
   float2 *part = (float2 *)(ws + p.part);
@@ -440,7 +459,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   bf16_t *g = NP == 1 ? (bf16_t *)e : (bf16_t *)(ws + p.g);
   const int64_t xplane = (int64_t)a.T * a.d, wplane = (int64_t)a.V * a.d, gplane = (int64_t)p.R * p.lde;
   const bool grad = a.dw != nullptr;
-  k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, list, pos, n_act);
+  k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, a.V, list, tgt, pos, n_act);
   TW_TRY_HIP(hipGetLastError());
   k_xent_stage<T, DXT><<<a.T, 256, 0, s>>>((const T *)a.x, a.ldx, a.d, pos, xc, xplane, a.loss, a.lse, (DXT *)a.dx);
   TW_TRY_HIP(hipGetLastError());
@@ -457,17 +476,17 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       const int mt = (int)(p.lde / Z::BM), nt = (R + Z::BN - 1) / Z::BN;
       auto go = [&](auto keep) {
         k_xent_logits<Z, NP, ET, decltype(keep)::value><<<grid8((int64_t)mt * nt), Z::NT, 0, s>>>(
-            w, wplane, xc, xplane, a.y, list, n_act, row0, R, a.V, a.d, mt, nt, e, p.lde, part, p.nblk, zt);
+            w, wplane, xc, xplane, tgt, n_act, row0, R, a.V, a.d, mt, nt, e, p.lde, part, p.nblk, zt);
       };
       if (grad) go(std::integral_constant<bool, true>());
       else go(std::integral_constant<bool, false>());
       TW_TRY_HIP(hipGetLastError());
     }
     if (grad)
-      k_xent_join<ET, true, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, a.y, list, n_act, row0, R, a.V, a.dloss, e, p.lde,
+      k_xent_join<ET, true, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, tgt, list, n_act, row0, R, a.V, a.dloss, e, p.lde,
                                                      g, gplane, a.loss, a.lse);
     else
-      k_xent_join<ET, false, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, a.y, list, n_act, row0, R, a.V, nullptr, e, p.lde,
+      k_xent_join<ET, false, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, tgt, list, n_act, row0, R, a.V, nullptr, e, p.lde,
                                                       g, gplane, a.loss, a.lse);
     TW_TRY_HIP(hipGetLastError());
     if (!grad) continue;
