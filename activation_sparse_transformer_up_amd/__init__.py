@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -144,11 +145,19 @@ def _rows(t, d: int):
         return None, d
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
-    if t.dim() != 2 or t.shape[1] != d:
-        raise ValueError(f"expected [T][{d}], got {tuple(t.shape)}")
-    if t.shape[0] > 0 and t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != d:
+        raise ValueError(f"expected [T][{d}], got {tuple(shape)}")
+    if stride[1] != 1 and shape[0] > 0:
         raise ValueError("the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else d
+    return t.data_ptr(), stride[0] if shape[0] > 1 else d
+
+
+def _rows_like(x, dtype: torch.dtype | None = None):
+    """A contiguous tensor of x's shape, in x's dtype or the one given."""
+    if (dtype is None or dtype == x.dtype) and x.is_contiguous():
+        return torch.empty_like(x)
+    return x.new_empty(x.shape, dtype=dtype)
 
 
 def _vec(t, n: int, name: str, dtype=torch.float32):
@@ -163,6 +172,8 @@ def _vec(t, n: int, name: str, dtype=torch.float32):
 
 
 def _stream(device=None):
+    if device is not None and device.index is not None:
+        return torch._C._cuda_getCurrentRawStream(device.index)       # 0.1 us against 1.9
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -524,10 +535,9 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, y_dty
     T, d = x.shape
     if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
         raise TypeError("residual must have x's dtype and shape")
-    y = torch.empty((T, d), dtype=y_dtype or x.dtype, device=x.device)
-    s = torch.empty((T, d), dtype=x.dtype, device=x.device) if residual is not None else x
-    mean = torch.empty((T,), dtype=torch.float32, device=x.device) if want_stats else None
-    rstd = torch.empty((T,), dtype=torch.float32, device=x.device) if want_stats else None
+    y = _rows_like(x, y_dtype)
+    s = _rows_like(x) if residual is not None else x
+    mean, rstd = x.new_empty((2, T), dtype=torch.float32).unbind() if want_stats else (None, None)
     (xp, ldx), (rp, ldr) = _rows(x, d), _rows(residual, d)
     _check(lib().layer_norm_fwd(xp, ldx, rp, ldr, _vec(weight, d, "weight"), _vec(bias, d, "bias"), _dt(x.dtype), T, d,
                                 eps, _ptr(y), _dt(y.dtype), _ptr(s) if residual is not None else None, _ptr(mean),
@@ -545,23 +555,22 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype |
     is); dres: the gradient that reaches s past the norm, in dx's dtype (default s's), added to
     dx. dweight and dbias are fp32; dbias is None unless want_bias."""
     T, d = s.shape
-    dev = s.device
-    dx = torch.empty((T, d), dtype=dx_dtype or s.dtype, device=dev)
+    dx = _rows_like(s, dx_dtype)
     if dy.shape != s.shape or (dres is not None and dres.shape != s.shape):
         raise ValueError("dy and dres must have s's shape")
     if dres is not None and dres.dtype != dx.dtype:
         raise TypeError("dres must have dx's dtype")
-    dw = torch.empty((d,), dtype=torch.float32, device=dev)
-    db = torch.empty((d,), dtype=torch.float32, device=dev) if want_bias else None
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(weight) if want_bias else None
     need = layer_norm_bwd_workspace_bytes(T, d)
     if need and workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = s.new_empty((need,), dtype=torch.uint8)
     (yp, lddy), (sp, lds), (rp, lddr) = _rows(dy, d), _rows(s, d), _rows(dres, d)
     _check(lib().layer_norm_bwd(yp, lddy, _dt(dy.dtype), sp, lds, _dt(s.dtype), _vec(weight, d, "weight"),
                                 _vec(mean, T, "mean"), _vec(rstd, T, "rstd"), rp, lddr, T, d, _ptr(dx), _dt(dx.dtype),
                                 _ptr(dw), _ptr(db), _ptr(workspace),
                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                _stream(dev)), "layer_norm_bwd")
+                                _stream(s.device)), "layer_norm_bwd")
     return dx, dw, db
 
 
@@ -612,43 +621,56 @@ def grad_norm_workspace_bytes(n: int) -> int:
     return lib().grad_norm_workspace_bytes(n)
 
 
+def _addresses(tensors, dev):
+    """Host arrays of the tensors' pointers and dtype codes."""
+    ptrs, types = [], []
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError("all gradients and outputs must live on one GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        ptrs.append(t.data_ptr())
+        types.append(_dt(t.dtype))
+    return array.array("Q", ptrs), array.array("i", types)
+
+
 def _grad_call(grads, outs, max_norm, norm, workspace):
-    grads = list(grads)
     n = len(grads)
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
-    if norm.dtype != torch.float32 or norm.numel() != 1:
+        norm = grads[0].new_empty((), dtype=torch.float32) if n else torch.empty((), device="cuda")
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise TypeError("norm must be one float32")
     dev = norm.device
-    if any(g.device != dev for g in grads):
-        raise ValueError("all gradients must live on one GPU")
+    ptrs, types = _addresses(grads, dev)
+    sizes = array.array("q", [g.numel() for g in grads])
     if workspace is None:
-        workspace = torch.empty((max(grad_norm_workspace_bytes(n), 16),), dtype=torch.uint8, device=dev)
-    ptrs = (_P * max(n, 1))(*[_ptr(g) for g in grads])
-    sizes = (_L * max(n, 1))(*[g.numel() for g in grads])
-    types = (_I * max(n, 1))(*[_dt(g.dtype) for g in grads])
+        workspace = norm.new_empty((max(grad_norm_workspace_bytes(n), 16),), dtype=torch.uint8)
+    # addresses of the host arrays, which outlive the call
+    p, s, t = (a.buffer_info()[0] for a in (ptrs, sizes, types))
     wb = workspace.numel() * workspace.element_size()
     if outs is None:
-        _check(lib().grad_norm(ptrs, sizes, types, n, _ptr(norm), _ptr(workspace), wb, _stream(dev)), "grad_norm")
+        _check(lib().grad_norm(p, s, t, n, _ptr(norm), _ptr(workspace), wb, _stream(dev)), "grad_norm")
         return norm
-    if len(outs) != n or any(o.shape != g.shape or o.device != dev for o, g in zip(outs, grads)):
-        raise ValueError("out must match the gradients' shapes and device")
-    optrs = (_P * max(n, 1))(*[_ptr(o) for o in outs])
-    otypes = (_I * max(n, 1))(*[_dt(o.dtype) for o in outs])
-    _check(lib().grad_clip(ptrs, optrs, sizes, types, otypes, n, float(max_norm), _ptr(norm), _ptr(workspace), wb,
-                           _stream(dev)), "grad_clip")
+    optrs, otypes = ptrs, types
+    if outs is not grads:
+        if len(outs) != n or any(o.shape != g.shape for o, g in zip(outs, grads)):
+            raise ValueError("out must match the gradients' shapes")
+        optrs, otypes = _addresses(outs, dev)
+    _check(lib().grad_clip(p, optrs.buffer_info()[0], s, t, otypes.buffer_info()[0], n, float(max_norm), _ptr(norm),
+                           _ptr(workspace), wb, _stream(dev)), "grad_clip")
     return norm
 
 
 def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The L2 norm over all elements of the gradients (fp32 and bf16 tensors, mixed): a device
     fp32 scalar."""
-    return _grad_call(grads, None, 0.0, norm, workspace)
+    return _grad_call(list(grads), None, 0.0, norm, workspace)
 
 
 def grad_clip(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
               workspace: torch.Tensor | None = None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), norm over all of them: in place,
     or into ``out`` (tensors of the same shapes, fp32 or bf16). Returns (norm, out)."""
-    outs = list(grads) if out is None else list(out)
+    grads = list(grads)
+    outs = grads if out is None else list(out)
     return _grad_call(grads, outs, max_norm, norm, workspace), outs
