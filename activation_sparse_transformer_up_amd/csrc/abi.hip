@@ -639,7 +639,7 @@ int layer_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr
 
 size_t layer_norm_bwd_workspace_bytes(int32_t T, int32_t d) {
   if (T <= 0 || d <= 0) return 0;
-  const int p = norm_bwd_strips(T);
+  const int p = norm_bwd_strips(T, d);
   return p > 1 ? (size_t)p * 2 * d * sizeof(float) : 0;
 }
 

@@ -169,9 +169,9 @@ struct NormBwd {
   const float *w, *mean, *rstd;
   int rows, d, x_bf16, dy_bf16, dx_bf16;
   void *dx;
-  float *dw, *db, *part;  // part: [norm_bwd_strips(rows)][2][d], unused where that is 1
+  float *dw, *db, *part;  // part: [norm_bwd_strips(rows, d)][2][d], unused where that is 1
 };
-int norm_bwd_strips(int rows);
+int norm_bwd_strips(int rows, int d);
 hipError_t launch_norm_bwd(const NormBwd &a, hipStream_t s);
 
 // grad.hip: the norm (out == NULL), or the norm and the clipped gradients. The host arrays are

@@ -18,6 +18,25 @@ TW_DEV void load8(const float *p, float (&o)[8]) {
   o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
 }
 
+// The same 8 elements as loaded, widened later: a load in flight then takes 4 registers of bf16.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
+  uint4 u;
+  TW_DEV void load(const uint16_t *p) { u = *(const uint4 *)p; }
+  TW_DEV void to(float (&o)[8]) const { Vec16<uint16_t>::load((const uint16_t *)&u, o); }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  TW_DEV void load(const float *p) {
+    a = *(const float4 *)p;
+    b = *(const float4 *)(p + 4);
+  }
+  TW_DEV void to(float (&o)[8]) const {
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  }
+};
+
 // Nontemporal: outputs that the writing kernel never reads again.
 TW_DEV void store8(float *p, const float (&v)[8]) {
   __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_t *)p);
