@@ -11,8 +11,8 @@
 // write LDS (lane l of a wave fills bytes [16 l, 16 l + 16) of a 1 KB block); NS - 1 stages are
 // in flight while one is multiplied. Where the stage lies in LDS:
 //   along k:   row r at 64 r, its 16-byte chunk c at c ^ ((r >> 1) & 3)
-//   across k:  1 KB block q (k rows 2 q and 2 q + 1) at 1056 q, in it the 64-byte chunk c of an odd
-//              k row at c ^ 1
+//   across k:  1 KB block q (512 / BX k rows) at MmTr::BLK q, in it the 64-byte chunk c of k row j
+//              at c ^ MmTr::swz(j)
 // Both keep the lanes that LDS serves together on different banks (SQ_LDS_BANK_CONFLICT = 0).
 // Along k a 16-byte read serves lanes 0-3, 12-15 and 20-27 of a half-wave in one turn and the
 // others in the next: their 16 rows are r = 0 .. 15 once each, with two different c, and (r & 3,
@@ -31,7 +31,15 @@
 
 namespace tw {
 
-constexpr int kMmBlkTr = 1056;                            // bytes from block to block across k
+// An operand across k in the stage, BX columns.
+template <int BX> struct MmTr {
+  static_assert(BX == 64 || BX == 256, "columns");
+  static constexpr int RPB = 512 / BX;                    // k rows of a block
+  static constexpr int BLK = 1056;                        // bytes from block to block
+  // from k row j (j % 8 < 4) to j + 4, whose exchange is the same
+  static constexpr int DOWN4 = BX == 64 ? 512 : 2 * BLK;
+  static TW_DEV int swz(int j) { return BX == 256 ? j & 1 : (j >> 1) & 1; }
+};
 
 template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> struct MM {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
@@ -41,19 +49,22 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> str
   static constexpr int KS = 32;                           // k per stage
   static constexpr int A_BLK = BM * KS * 2 / 1024, B_BLK = BN * KS * 2 / 1024;      // 1 KB blocks of a stage
   static constexpr int LPW = (A_BLK + B_BLK) / NW;        // 1 KB wave-loads per wave and stage
-  static constexpr int A_BYTES = A_BLK * (ATR ? kMmBlkTr : 1024);
-  static constexpr int STAGE = A_BYTES + B_BLK * (BTR ? kMmBlkTr : 1024), SMEM = NS * STAGE;
+  static constexpr int A_STEP = ATR ? MmTr<BM>::BLK : 1024, B_STEP = BTR ? MmTr<BN>::BLK : 1024;
+  static constexpr int A_BYTES = A_BLK * A_STEP;
+  static constexpr int STAGE = A_BYTES + B_BLK * B_STEP, SMEM = NS * STAGE;
   static_assert((A_BLK + B_BLK) % NW == 0 && NS >= 3, "tile");
-  static_assert((!ATR || (BM == 256 && WM % 64 == 0)) && (!BTR || (BN == 256 && WN % 64 == 0)), "across k");
+  static_assert((!ATR || WM % 64 == 0) && (!BTR || WN % 64 == 0), "across k");
 };
 
 // p: element (first row of the tile, k = 0) for an operand along k, (k = 0, first column of the
 // tile) for one across k; ld: elements between rows; n: rows (columns) of the tile that exist (a
-// multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand.
+// multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand; rows: where
+// the tile's rows are not consecutive, their numbers (n of them, in LDS).
 struct MmOperand {
   const uint16_t *p;
   int64_t ld, plane;
   int n;
+  const int *rows = nullptr;
 };
 
 // The six products of planes, smallest first: (lo, hi) (hi, lo) (mid, mid) (mid, hi) (hi, mid)
@@ -72,18 +83,19 @@ TW_DEV i16x4_t mm_read_tr(const lds_i16x4_t *__restrict__ p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p);
 }
 
-// Fragment i of a wave (16 rows from w0 + 16 i) of a staged operand: lane l gets row l % 16, k =
-// 8 (l / 16) .. + 7. Across k, w0 is a multiple of 64: the exchange of chunks stays within i.
-template <bool TR> TW_DEV u32x4_t mm_frag(const char *st, int w0, int i, int lane) {
+// Fragment i of a wave (16 rows from w0 + 16 i) of a staged operand of BX rows: lane l gets row
+// l % 16, k = 8 (l / 16) .. + 7. Across k, w0 is a multiple of 64: the exchange of chunks stays in i.
+template <int BX, bool TR> TW_DEV u32x4_t mm_frag(const char *st, int w0, int i, int lane) {
   if constexpr (!TR) {
     const int r = w0 + (lane & 15);
     return *(const u32x4_t *)(st + r * 64 + (((lane >> 4) ^ ((r >> 1) & 3)) << 4) + i * 1024);
   } else {
-    const int j = 8 * (lane >> 4) + ((lane & 15) >> 2);   // and j + 4, two blocks further
-    const char *a = st + j / 2 * kMmBlkTr + (j & 1) * 512 + w0 * 2 + (((i >> 1) ^ (j & 1)) << 6) + ((i & 1) << 5) +
+    typedef MmTr<BX> L;
+    const int j = 8 * (lane >> 4) + ((lane & 15) >> 2), sw = L::swz(j);
+    const char *a = st + j / L::RPB * L::BLK + j % L::RPB * (2 * BX) + w0 * 2 + (((i >> 1) ^ sw) << 6) + ((i & 1) << 5) +
                     ((lane & 3) << 3);
     const i16x4_t lo = mm_read_tr((const lds_i16x4_t *)a);
-    const i16x4_t hi = mm_read_tr((const lds_i16x4_t *)(a + 2 * kMmBlkTr));
+    const i16x4_t hi = mm_read_tr((const lds_i16x4_t *)(a + L::DOWN4));
     u32x4_t v;
     __builtin_memcpy(&v, &lo, 8);
     __builtin_memcpy((char *)&v + 8, &hi, 8);
@@ -117,22 +129,23 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
   for (int i = 0; i < G::LPW; ++i) {
     const int q = wave + G::NW * i;                       // 1 KB block of the stage
     isA[i] = G::A_BLK % G::NW == 0 ? i * G::NW < G::A_BLK : q < G::A_BLK;
-    auto place = [&](const MmOperand &o, int blk, auto tr) {
+    auto place = [&](const MmOperand &o, int blk, auto tr, auto bx) {
       if constexpr (!decltype(tr)::value) {
         const int r = blk * 16 + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
         kof[i] = c * 8;
-        voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 8) * 2 : OOB;
+        voff[i] = r < o.n ? (uint32_t)((o.rows ? o.rows[r] : r) * o.ld + c * 8) * 2 : OOB;
       } else {
-        const int j = blk * 2 + (lane >> 5);
-        const int col = (((lane >> 2 & 7) ^ (j & 1)) * 32) + (lane & 3) * 8;
+        constexpr int BX = decltype(bx)::value, LR = BX / 8;          // lanes per k row
+        const int j = blk * MmTr<BX>::RPB + lane / LR;
+        const int col = (((lane % LR) >> 2) ^ MmTr<BX>::swz(j)) * 32 + (lane & 3) * 8;
         kof[i] = j;
         voff[i] = col < o.n ? (uint32_t)(j * o.ld + col) * 2 : OOB;
       }
     };
     const int qb = q - G::A_BLK;
-    dst[i] = isA[i] ? q * (G::ATR ? kMmBlkTr : 1024) : G::A_BYTES + qb * (G::BTR ? kMmBlkTr : 1024);
-    if (isA[i]) place(A, q, std::integral_constant<bool, G::ATR>());
-    else place(B, qb, std::integral_constant<bool, G::BTR>());
+    dst[i] = isA[i] ? q * G::A_STEP : G::A_BYTES + qb * G::B_STEP;
+    if (isA[i]) place(A, q, std::integral_constant<bool, G::ATR>(), std::integral_constant<int, G::BM>());
+    else place(B, qb, std::integral_constant<bool, G::BTR>(), std::integral_constant<int, G::BN>());
   }
   const int nk1 = (K + G::KS - 1) / G::KS;                // stages of one product of planes
   const int nk = nk1 * NP;
@@ -158,8 +171,8 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
   typedef u32x4_t FB[G::FN];
   auto read1 = [&](int kt, int j, FA &a, FB &b) {
     const char *st = smem + (kt % G::NS) * G::STAGE;
-    if (j < G::FM) a[j] = mm_frag<G::ATR>(st, wm * G::WM, j, lane);
-    else b[j - G::FM] = mm_frag<G::BTR>(st + G::A_BYTES, wn * G::WN, j - G::FM, lane);
+    if (j < G::FM) a[j] = mm_frag<G::BM, G::ATR>(st, wm * G::WM, j, lane);
+    else b[j - G::FM] = mm_frag<G::BN, G::BTR>(st + G::A_BYTES, wn * G::WN, j - G::FM, lane);
   };
   auto mma = [&](int i, const FA &a, const FB &b) {
     acc[i / G::FN][i % G::FN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -226,6 +239,148 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
   }
 #pragma unroll
   for (int i = 0; i < NM; ++i) mma(i, a0, b0);
+}
+
+// The same for two operands along k, in stages of 64 k: a row's 128 bytes of a stage are one cache
+// line. (With 32 k the two halves of a line are fetched by different stages, and the L2 serves half
+// lines at the price of whole ones: 13 TB/s at most, which bound the logits' 128 x 128 tiles: 10.0 ms
+// at T = 8192, d = 4096, V = 128000, with whole lines 7.4.) A's ring has NSA stages, B's NSB = NSA or NSA
+// - 1: what LDS has left goes to A, which comes from HBM. In LDS row r lies at 128 r, its 16-byte
+// chunk c at c ^ ((r >> 1) & 7), again without bank conflicts. A stage is multiplied in two halves,
+// with one barrier:
+//   products of (kt, first half), between them the reads of the second half's fragments
+//   wait for stage kt + 1's loads, barrier (all waves have read stage kt)
+//   products of (kt, second half), between them the reads of (kt + 1, first half) and the loads of
+//   stages kt + NSB of B and kt + NSA of A into the places of stage kt
+// The order of the loads (B's before A's in every step) makes the wait a fixed count.
+template <int BM_, int BN_, int WM_, int WN_, int NSA_, int NSB_> struct MM64 {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NSA = NSA_, NSB = NSB_;
+  static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, NT = NW * 64;
+  static constexpr int FM = WM / 16, FN = WN / 16;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;            // 1 KB wave-loads per wave and stage
+  static constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, SMEM = NSA * A_STAGE + NSB * B_STAGE;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NSB >= 2 && (NSA == NSB || NSA == NSB + 1), "tile");
+};
+
+template <class G, int NP>
+TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc)[G::FM][G::FN], char *smem) {
+  constexpr int NM = G::FM * G::FN, NR = G::FM + G::FN, NL = G::LA + G::LB;
+  constexpr int RI = NM / NR >= 2 ? NM / NR : 1;          // a fragment read after every RI products
+  constexpr int DI = NM / NL >= 1 ? NM / NL : 1;          // a stage load after every DI products
+  constexpr uint32_t OOB = 0x80000000u;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+
+  // B's loads, then A's: this lane's byte offset in each and the k it starts at. A load is a block of 8
+  // rows; its row of this lane is 8 blk + lane / 8.
+  uint32_t voff[NL];
+  int kof[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const MmOperand &o = i < G::LB ? B : A;
+    const int blk = wave + G::NW * (i < G::LB ? i : i - G::LB), r = blk * 8 + (lane >> 3);
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    kof[i] = c * 8;
+    voff[i] = r < o.n ? (uint32_t)((o.rows ? o.rows[r] : r) * o.ld + c * 8) * 2 : OOB;
+  }
+  const int nk = (K + 63) / 64 * NP;
+  if (nk == 0) return;
+
+  // term, k and place of the next stage to load, of B and of A. Loads past the last stage fill a free
+  // place with zeros: the count of the waits stays the same.
+  int lt[2] = {0, 0}, lk[2] = {0, 0}, lp[2] = {0, 0};
+  auto issue1 = [&](int i) {
+    const bool isB = i < G::LB;
+    const int o = isB ? 0 : 1, blk = wave + G::NW * (isB ? i : i - G::LB);
+    char *at = smem + (isB ? G::NSA * G::A_STAGE + lp[0] * G::B_STAGE : lp[1] * G::A_STAGE) + blk * 1024;
+    const uint32_t vo = lk[o] + kof[i] < K && (NP == 1 || lt[o] < NP) ? voff[i] : OOB;
+    const uint16_t *base = isB ? B.p + (NP > 1 ? mm_plane_b(lt[0]) * B.plane : 0) : A.p + (NP > 1 ? mm_plane_a(lt[1]) * A.plane : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base + lk[o]), (lds_void_t *)at, 16, vo, 0, 0, 0);
+    if (i != G::LB - 1 && i != NL - 1) return;            // the operand's last load of the stage
+    lk[o] += 64;
+    if (NP > 1 && lk[o] >= K) {
+      lk[o] = 0;
+      ++lt[o];
+    }
+    lp[o] = lp[o] + 1 == (isB ? G::NSB : G::NSA) ? 0 : lp[o] + 1;
+  };
+  typedef u32x4_t FA[G::FM];
+  typedef u32x4_t FB[G::FN];
+  const int r0 = lane & 15;
+  const int at0 = r0 * 128 + (((lane >> 4) ^ (r0 >> 1)) << 4);        // second half: chunk + 4
+  int pa = 0, pb = 0;                                     // places of the stage to read next
+  auto read1 = [&](int h, int j, FA &a, FB &b) {
+    const char *sa = smem + pa * G::A_STAGE, *sb = smem + G::NSA * G::A_STAGE + pb * G::B_STAGE;
+    const int at = at0 ^ (h << 6);
+    if (j < G::FM) a[j] = *(const u32x4_t *)(sa + (wm * G::WM + j * 16) * 128 + at);
+    else b[j - G::FM] = *(const u32x4_t *)(sb + (wn * G::WN + (j - G::FM) * 16) * 128 + at);
+  };
+  auto next = [&]() {
+    pa = pa + 1 == G::NSA ? 0 : pa + 1;
+    pb = pb + 1 == G::NSB ? 0 : pb + 1;
+  };
+  auto mma = [&](int i, const FA &a, const FB &b) {
+    acc[i / G::FN][i % G::FN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8_t, a[i / G::FN]), __builtin_bit_cast(bf16x8_t, b[i % G::FN]),
+        acc[i / G::FN][i % G::FN], 0, 0, 0);
+  };
+  // the order that the steady state has: A's extra stage first, then B and A of a stage in turn
+  if (G::NSA > G::NSB)
+#pragma unroll
+    for (int i = G::LB; i < NL; ++i) issue1(i);
+#pragma unroll
+  for (int st = 0; st < G::NSB; ++st)
+#pragma unroll
+    for (int i = 0; i < NL; ++i) issue1(i);
+  // loads issued after those of the stage waited for
+  constexpr int AFTER = (G::NSA > G::NSB ? G::LA : 0);
+  wait_vmcnt<AFTER + (G::NSB - 1) * NL>();
+  block_barrier();
+  FA a0, a1;
+  FB b0, b1;
+#pragma unroll
+  for (int j = 0; j < NR; ++j) read1(0, j, a0, b0);
+  auto first = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<NM>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      mma(i, a0, b0);
+      if constexpr (i % RI == 0 && i / RI < NR) read1(1, i / RI, a1, b1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr ((NM + RI - 1) / RI < NR)
+#pragma unroll
+      for (int j = (NM + RI - 1) / RI; j < NR; ++j) read1(1, j, a1, b1);
+  };
+  auto second = [&]() {
+    wait_vmcnt<AFTER + (G::NSB - 2) * NL>();              // stage kt + 1 has landed
+    block_barrier_lds();
+    next();
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<NM>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      mma(i, a1, b1);
+      if constexpr (i % RI == 0 && i / RI < NR) read1(0, i / RI, a0, b0);
+      if constexpr (i % DI == DI - 1 && i / DI < NL) issue1(i / DI);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr ((NM + RI - 1) / RI < NR)
+#pragma unroll
+      for (int j = (NM + RI - 1) / RI; j < NR; ++j) read1(0, j, a0, b0);
+    if constexpr (NM / DI < NL)
+#pragma unroll
+      for (int i = NM / DI; i < NL; ++i) issue1(i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int kt = 0; kt + 1 < nk; ++kt) {
+    first();
+    second();
+  }
+  first();
+  wait_vmcnt<0>();                                        // no load into LDS outlives the loop
+#pragma unroll
+  for (int i = 0; i < NM; ++i) mma(i, a1, b1);
 }
 
 // Workgroup b of `total` tiles -> tile. The XCDs take workgroups in turn (b % 8), each its own

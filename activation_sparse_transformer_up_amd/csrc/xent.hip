@@ -14,7 +14,9 @@
 //
 // Tokens without a target (negative) take no part: the rows with one are gathered first, in
 // order, and all products run over that list (its length stays on the device; workgroups beyond
-// it leave at once). Whatever such rows hold, also NaN, reaches nothing.
+// it leave at once). Whatever such rows hold, also NaN, reaches nothing. The forward of at most 64
+// bf16 tokens makes the list in every workgroup instead and reads the rows of x where they lie,
+// which saves a launch.
 //
 // Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is; dw is summed
 // over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h).
@@ -79,14 +81,50 @@ TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
   store8(p + 2 * plane, r);
 }
 
-// Token blockIdx.x: with a target, its row of x into the gathered operand (fp32: three planes);
-// without, zeros to its loss, lse and row of dx.
+// Token blockIdx.x < T: with a target, its row of x into the gathered operand (fp32: three planes);
+// without, zeros to its loss, lse and row of dx. pos == NULL: the token's place is counted here (and
+// list, tgt and n_act written), which for few tokens costs less than the launch of k_xent_rows.
+// fp32: the workgroups past T split w.
 template <typename T, typename DXT>
-__global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int64_t ldx, int d,
-                                                    const int32_t *__restrict__ pos, bf16_t *__restrict__ xc,
-                                                    int64_t plane, float *__restrict__ loss, float *__restrict__ lse,
-                                                    DXT *__restrict__ dx) {
-  const int t = blockIdx.x, p = pos[t];
+__global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int64_t ldx, int tokens, int d, int V,
+                                                    const int64_t *__restrict__ y, const int32_t *__restrict__ pos,
+                                                    int32_t *__restrict__ list, int32_t *__restrict__ tgt,
+                                                    int32_t *__restrict__ n_act, bf16_t *__restrict__ xc, int64_t plane,
+                                                    float *__restrict__ loss, float *__restrict__ lse,
+                                                    DXT *__restrict__ dx, const T *__restrict__ w, size_t wn,
+                                                    bf16_t *__restrict__ wp) {
+  if constexpr (std::is_same<T, float>::value) {
+    if ((int)blockIdx.x >= tokens) {
+      const size_t i = ((size_t)(blockIdx.x - tokens) * 256 + threadIdx.x) * 8;
+      if (i >= wn) return;
+      float v[8];
+      load8(w + i, v);
+      split8(v, wp + i, (int64_t)wn);
+      return;
+    }
+  }
+  const int t = blockIdx.x;
+  int p;
+  if (pos) {
+    p = pos[t];
+  } else {
+    __shared__ int red[4];
+    int c = 0;
+    for (int i = threadIdx.x; i < t; i += 256) c += y[i] >= 0;
+    c = wave_sum(c);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
+    __syncthreads();
+    c = (red[0] + red[1]) + (red[2] + red[3]);
+    const int64_t v = y[t];
+    p = v >= 0 ? c : -1;
+    if (threadIdx.x == 0) {
+      if (p >= 0) {
+        list[p] = t;
+        tgt[p] = v < V ? (int)v : V;
+      }
+      if (t == tokens - 1) *n_act = c + (v >= 0);
+    }
+  }
   if (p < 0) {
     if (threadIdx.x == 0) {
       loss[t] = 0.f;
@@ -108,35 +146,53 @@ __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int
   }
 }
 
-__global__ __launch_bounds__(256) void k_xent_planes(const float *__restrict__ w, size_t n, bf16_t *__restrict__ out) {
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  float v[8];
-  load8(w + i, v);
-  split8(v, out + i, (int64_t)n);
-}
-
 // ------------------------------------------------------------------------------------ logits
 
 // Tokens [row0, row0 + R) of the list that exist.
 TW_DEV int piece_rows(const int32_t *n_act, int row0, int R) { return min(max(*n_act - row0, 0), R); }
 
+// The list of at most 64 tokens, in a wave's registers: bit t of the result is set where token t
+// has a target; v is lane t's target.
+TW_DEV uint64_t wave_list(const int64_t *y, int T, int64_t &v) {
+  const int lane = threadIdx.x & 63;
+  v = lane < T ? y[lane] : -1;
+  return ballot64(v >= 0);
+}
+
 // D[vocabulary][token] = w x^T: a lane holds 4 consecutive logits of a token per block, so that a
 // token's maximum and sum are taken over a lane's registers and two exchanges, and e is stored 4
-// elements at a time. part[token][block of WM columns] = (max, sum of exp(z - max)).
-template <class G, int NP, typename ET, bool KEEP>
+// elements at a time. part[token][block of WM columns] = (max, sum of exp(z - max) over all but the
+// target), zt[token] = the target's logit.
+// DIRECT: xc is x itself with rows ldx apart, y the targets of its R <= 64 tokens; the list is made
+// here.
+template <class G, int NP, typename ET, bool KEEP, bool DIRECT>
 __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict__ w, int64_t wplane,
-                                                       const bf16_t *__restrict__ xc, int64_t xplane,
-                                                       const int32_t *__restrict__ tgt,
+                                                       const bf16_t *__restrict__ xc, int64_t ldx, int64_t xplane,
+                                                       const int64_t *__restrict__ y, const int32_t *__restrict__ tgt,
                                                        const int32_t *__restrict__ n_act, int row0, int R, int V, int d,
                                                        int mt, int nt, ET *__restrict__ e, int64_t lde,
                                                        float2 *__restrict__ part, int nblk, float *__restrict__ zt) {
-  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  // one LDS object: next to a second one the compiler takes the fragment reads for users of the
+  // loads in flight, and waits
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM + (DIRECT ? 512 : 0)];
+  int *rowl = (int *)(smem + G::SMEM), *tgtl = rowl + 64;
   const int t = mm_xcd_tile(blockIdx.x, mt * nt);
   if (t < 0) return;
-  int m, n;
+  int m, n, rows;
   mm_tile_mn<8>(t, mt, nt, m, n);
-  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  const int m0 = m * G::BM, n0 = n * G::BN;
+  if constexpr (DIRECT) {
+    int64_t v;
+    const uint64_t act = wave_list(y, R, v);
+    rows = __popcll(act);
+    if (threadIdx.x < 64 && v >= 0) {
+      rowl[mbcnt64(act)] = threadIdx.x;
+      tgtl[mbcnt64(act)] = v < V ? (int)v : V;
+    }
+    __syncthreads();
+  } else {
+    rows = piece_rows(n_act, row0, R);
+  }
   if (n0 >= rows) return;
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
@@ -144,8 +200,9 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
   const MmOperand A = {w + (size_t)m0 * d, d, wplane, min(V - m0, G::BM)};
-  const MmOperand B = {xc + (size_t)(row0 + n0) * d, d, xplane, min(rows - n0, G::BN)};
-  mm_loop<G, NP>(A, B, d, acc, smem);
+  const MmOperand B = {xc + (DIRECT ? 0 : (size_t)(row0 + n0) * d), ldx, xplane, min(rows - n0, G::BN),
+                       DIRECT ? rowl : nullptr};
+  mm_loop64<G, NP>(A, B, d, acc, smem);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
   const int wm = wave / G::NWN, wn = wave % G::NWN;
@@ -154,7 +211,7 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 #pragma unroll
   for (int fn = 0; fn < G::FN; ++fn) {
     const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);          // row of the piece
-    toff[fn] = r < rows ? tgt[row0 + r] - v0 : -1;
+    toff[fn] = r < rows ? (DIRECT ? tgtl[r] : tgt[row0 + r]) - v0 : -1;
   }
   if (v0 + G::WM > V)                                     // the last block ends inside the vocabulary
 #pragma unroll
@@ -168,7 +225,9 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
   for (int fn = 0; fn < G::FN; ++fn) {
     const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);
     const bool ok = r < rows;
-    if (ballot64((uint32_t)toff[fn] < (uint32_t)G::WM)) { // rare: one block in nblk has a row's target
+    // rare: one block in nblk holds a row's target
+    const bool hit = ballot64((uint32_t)toff[fn] < (uint32_t)G::WM) != 0;
+    if (hit) {
 #pragma unroll
       for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
@@ -184,14 +243,17 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
     const float ref = mx == -INFINITY ? 0.f : mx;         // a block past the vocabulary: e = 0
     const float refl = ref * kLog2e;
+    auto ex = [&](float z) {
+      if constexpr (NP == 1) return __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -refl));
+      else return expf(z - ref);
+    };
     float s = 0.f;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) {
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (NP == 1) v[i] = __builtin_amdgcn_exp2f(fmaf(acc[fm][fn][i], kLog2e, -refl));
-        else v[i] = expf(acc[fm][fn][i] - ref);
+        v[i] = ex(acc[fm][fn][i]);
         s += v[i];
       }
       if constexpr (KEEP) {
@@ -202,24 +264,52 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
         }
       }
     }
+    if (hit) {                                            // the same without the target
+      s = 0.f;
+#pragma unroll
+      for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += fm * 16 + grp * 4 + i == toff[fn] ? 0.f : ex(acc[fm][fn][i]);
+    }
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
     if (ok && grp == 0) part[(size_t)r * nblk + blk] = make_float2(mx, s);
   }
 }
 
-// Row of a piece: joins its blocks to lse and loss; for a gradient turns its e into G (zero in
-// the padding, where e is 0). A target beyond the vocabulary makes loss and G NaN.
-template <typename ET, bool GRAD, int PW>
-__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, const float *__restrict__ zt,
+// Row of a piece: joins its blocks (of 1 << pw columns) to lse and loss; for a gradient turns its e
+// into G (zero in the padding, where e is 0). With R the sum of exp(z - max) over all but the target
+// and E the target's: loss = log(1 + R / E) and p - 1 = -R / (R + E), which keep the digits of a token
+// that the model is sure of (R << E), where lse - z and exp(z - lse) - 1 have none left. A target
+// beyond the vocabulary makes loss and G NaN.
+// DIRECT: a workgroup per token of y instead, zeros for one without a target.
+template <typename ET, bool GRAD, bool DIRECT>
+__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, int pw,
+                                                   const float *__restrict__ zt, const int64_t *__restrict__ y,
                                                    const int32_t *__restrict__ tgts, const int32_t *__restrict__ list,
                                                    const int32_t *__restrict__ n_act, int row0, int R, int V,
                                                    const float *__restrict__ dloss, ET *__restrict__ e, int64_t lde,
                                                    bf16_t *__restrict__ g, int64_t gplane, float *__restrict__ loss,
                                                    float *__restrict__ lse) {
   __shared__ float red[8];
-  const int r = blockIdx.x, wave = threadIdx.x >> 6;
-  if (r >= piece_rows(n_act, row0, R)) return;
+  const int wave = threadIdx.x >> 6;
+  int r = blockIdx.x, t, tgt;
+  if constexpr (DIRECT) {
+    int64_t v;
+    const uint64_t act = wave_list(y, R, v);
+    t = r;
+    const int64_t vt = __shfl(v, t, 64);
+    if (vt < 0) {
+      if (threadIdx.x == 0) loss[t] = lse[t] = 0.f;
+      return;
+    }
+    r = __popcll(act & ((1ull << t) - 1));
+    tgt = vt < V ? (int)vt : V;
+  } else {
+    if (r >= piece_rows(n_act, row0, R)) return;
+    t = list[row0 + r];
+    tgt = tgts[row0 + r];
+  }
   const float2 *p = part + (size_t)r * nblk;
   float mx = -INFINITY;
   for (int i = threadIdx.x; i < nblk; i += 256) mx = fmaxf(mx, p[i].x);
@@ -234,26 +324,25 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   s = wave_sumf(s);
   if ((threadIdx.x & 63) == 0) red[4 + wave] = s;
   __syncthreads();
-  const float l = ref + logf((red[4] + red[5]) + (red[6] + red[7]));
-  const int t = list[row0 + r], tgt = tgts[row0 + r];
-  const bool bad = tgt >= V;
-  const float z = bad ? NAN : zt[row0 + r];
+  const float rest = (red[4] + red[5]) + (red[6] + red[7]);
+  const bool bad = tgt >= V;                              // then rest is the sum over all
+  const float z = bad ? NAN : zt[row0 + r], et = bad ? 0.f : expf(z - ref), all = rest + et;
+  const float ls = logf(all), l = ref + ls;
   if (threadIdx.x == 0) {
     lse[t] = l;
-    loss[t] = l - z;
+    loss[t] = et > 0.5f ? log1pf(rest / et) : (ref - z) + ls;
   }
   if constexpr (GRAD) {
     const float dl = bad ? NAN : dloss[t];
     for (int i = threadIdx.x * 8; i < lde; i += 256 * 8) {
-      // one block covers the 8 columns (PW is a multiple of 8)
-      const int b = i / PW;
+      const int b = i >> pw;                              // one block covers the 8 columns
       const float f = b < nblk ? expf(p[b].x - l) * dl : 0.f;
       float v[8];
       load8(e + (size_t)r * lde + i, v);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[k] = i + k < V ? v[k] * f : 0.f;
-        if (i + k == tgt) v[k] = expm1f(z - l) * dl;
+        if (i + k == tgt) v[k] = -rest / all * dl;
       }
       if constexpr (std::is_same<ET, float>::value) {
         split8(v, g + (size_t)r * lde + i, gplane);
@@ -312,35 +401,37 @@ __global__ __launch_bounds__(G::NT) void k_xent_dx(const bf16_t *__restrict__ w,
   }
 }
 
-template <typename DXT>
-__global__ __launch_bounds__(256) void k_xent_dx_sum(const float *__restrict__ part, int S, int R, int d,
-                                                     const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
-                                                     int row0, DXT *__restrict__ dx) {
-  const int cb = (d / 8 + 255) / 256, r = blockIdx.x / cb, c = (blockIdx.x % cb * 256 + threadIdx.x) * 8;
-  if (r >= piece_rows(n_act, row0, R) || c >= d) return;
-  float a[8] = {};
-  for (int s = 0; s < S; ++s) {
-    float v[8];
-    load8(part + ((size_t)s * R + r) * d + c, v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] += v[k];
-  }
-  store8(dx + (size_t)list[row0 + r] * d + c, a);
-}
-
 // dw: D[column of d][vocabulary] = x^T G over the piece's tokens (both across k). sum: fp32 sums
-// of the pieces so far (added where `add`, written where dw is NULL; may be dw itself).
-template <class G, int NP, typename DWT>
+// of the pieces so far (added where `add`, written where dw is NULL; may be dw itself). The
+// workgroups from `tiles` on add dx's S partial sums, which are complete when this launch begins.
+template <class G, int NP, typename DWT, typename DXT>
 __global__ __launch_bounds__(G::NT) void k_xent_dw(const bf16_t *__restrict__ xc, int64_t xplane,
                                                    const bf16_t *__restrict__ g, int64_t lde, int64_t gplane,
-                                                   const int32_t *__restrict__ n_act, int row0, int R, int V, int d, int mt,
-                                                   int nt, bool add, float *sum, DWT *dw) {
+                                                   const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
+                                                   int row0, int R, int V, int d, int mt, int nt, bool add, float *sum,
+                                                   DWT *dw, int tiles, int S, const float *__restrict__ part,
+                                                   DXT *__restrict__ dx) {
   __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  const int rows = piece_rows(n_act, row0, R);
+  if ((int)blockIdx.x >= tiles) {
+    const size_t i = ((size_t)(blockIdx.x - tiles) * G::NT + threadIdx.x) * 8;
+    const int r = (int)(i / d), c = (int)(i % d);         // d is a multiple of 8
+    if (r >= rows) return;
+    float a[8] = {};
+    for (int s = 0; s < S; ++s) {
+      float v[8];
+      load8(part + (size_t)s * R * d + i, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a[k] += v[k];
+    }
+    store8(dx + (size_t)list[row0 + r] * d + c, a);
+    return;
+  }
   const int t = mm_xcd_tile(blockIdx.x, mt * nt);
   if (t < 0) return;
   int m, n;
   mm_tile_mn<8>(t, mt, nt, m, n);
-  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  const int m0 = m * G::BM, n0 = n * G::BN;
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
   for (int i = 0; i < G::FM; ++i)
@@ -378,51 +469,118 @@ __global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t
 
 // ------------------------------------------------------------------------------------- plan
 
-// Tiles: 8 waves of 64 x 128 for many tokens; for at most 64 the products are bound by the
-// stream of w: a 64 x 64 tile with a ring of 8 stages keeps 28 KB of it in flight per workgroup.
-typedef MM<256, 256, 64, 128, 4, false, false> TileZ;     // logits
-typedef MM<64, 64, 16, 64, 8, false, false> TileZS;
-typedef MM<256, 256, 64, 128, 4, true, false> TileX;      // dx
-typedef MM<256, 64, 64, 64, 4, true, false> TileXS;
-typedef MM<256, 256, 64, 128, 4, true, true> TileW;       // dw
+// The products' tiles. Large: 8 waves of 64 x 128, one workgroup per CU, the least traffic per
+// operation. The smaller ones, two workgroups per CU, are for calls whose large tiles would leave CUs
+// idle or hold mostly rows that do not exist. The smallest logits tile's ring of four 64-k stages
+// keeps 24 KB of w per workgroup in flight, for few tokens, where the stream of w is all there is.
+enum { kSmall, kMid, kLarge };
+template <int C> struct Tiles;
+template <> struct Tiles<kSmall> {
+  typedef MM64<64, 64, 16, 64, 4, 4> Z;                   // logits
+  typedef MM<256, 64, 64, 64, 3, true, false> X;          // dx
+  typedef MM<256, 64, 64, 64, 3, true, true> W;           // dw
+};
+template <> struct Tiles<kMid> {
+  typedef MM64<128, 128, 64, 64, 3, 2> Z;
+};
+template <> struct Tiles<kLarge> {
+  typedef MM64<256, 256, 64, 128, 3, 2> Z;
+  typedef MM<256, 256, 64, 128, 4, true, false> X;
+  typedef MM<256, 256, 64, 128, 4, true, true> W;
+};
 
-constexpr int kFewRows = 64;
+constexpr int kCUs = 256;
+constexpr int kDirectRows = 64;                           // tokens of the forward without a gather
+constexpr int kCountT = 2048;                             // tokens up to which k_xent_stage counts
 constexpr size_t kPieceBytes = (size_t)1 << 30;
 
+// Nanoseconds of `tiles` tiles of a class over `stages` stages: rounds of resident workgroups, each
+// with its stages (all workgroups of a CU together) and its start and epilogue. Measured per kernel
+// with every class forced, T x d x V in bf16 (small / mid / large, us): logits 100 x 1024 x 8000: 11 / 15
+// / 32, 1000 x 4096 x 8000: 108 / 66 / 92, 4096 x 1024 x 16000: 293 / 153 / 140; dx 500 x 512 x 2000: 15 / 17
+// (small / large), 1000 x 4096 x 8000: 98 / 63; dw 128 x 256 x 1009 in fp32: 16 / 25, 4096 x 1024 x 16000:
+// 203 / 118. (Tiles of 256 x 128 for dx and dw were slower than either everywhere.)
+struct Cost {
+  int per_cu, stage, alone, start;                        // alone: a stage where no CU has two workgroups
+};
+constexpr Cost kCostZ[3] = {{2, 450, 450, 2500}, {2, 1000, 750, 4000}, {1, 1450, 1450, 9000}};      // 64-k stages
+constexpr Cost kCostG[3] = {{2, 750, 700, 4500}, {}, {1, 850, 850, 10000}};       // dx, dw: 32-k stages
+int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
+  if (tiles <= kCUs) return stages * c.alone + c.start;
+  const int64_t slots = kCUs * c.per_cu;
+  return (tiles + slots - 1) / slots * (stages * c.stage + c.start);
+}
+// Whether a smaller tile's cost n is to be preferred: near ties go to the larger, whose tiles of
+// tokens without a target cost nothing.
+bool cheaper(int64_t n, int64_t best) { return n * 10 < best * 9; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// log2 of the logits tile's columns per wave
+int block_log(int c) { return c == kSmall ? 4 : 6; }
+static_assert(Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 64, "block_log");
+
 struct Plan {
-  int R, pieces, nblk, S, ks, np;
+  int R, pieces, nblk, S, ks, zc, dc, wc;                 // zc, dc, wc: classes of logits, dx, dw
   int64_t lde;
-  bool few, sums;
-  size_t list, tgt, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;        // offsets of the workspace
+  bool direct, sums;
+  size_t list, tgt, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;   // offsets of the workspace
 };
 
 Plan plan_of(int T, int d, int V, int bf16, bool grad) {
   Plan p = {};
-  p.np = bf16 ? 1 : 6;
-  p.few = T <= kFewRows;
-  p.lde = ((int64_t)V + 255) / 256 * 256;
-  p.nblk = (int)(p.lde / (p.few ? TileZS::WM : TileZ::WM));
+  const int np = bf16 ? 1 : 6;
+  p.lde = ceil_div(V, 256) * 256;
+  p.direct = bf16 && !grad && T <= kDirectRows;
+  int64_t best = 0;
+  for (int c = p.direct ? kSmall : kLarge; c >= kSmall; --c) {
+    const int b = 64 << c;
+    const int64_t n = cost_of(kCostZ[c], ceil_div(V, b) * ceil_div(T, b), ceil_div(d, 64) * np);
+    if (!best || cheaper(n, best)) {
+      best = n;
+      p.zc = c;
+    }
+  }
+  // blocks of all columns that the tiles cover (with e kept, its padding too)
+  p.nblk = (int)((grad ? p.lde : ceil_div(V, 64 << p.zc) * (64 << p.zc)) >> block_log(p.zc));
   const size_t planes = bf16 ? 1 : 3;
   // rows of a piece: as many as kPieceBytes hold of what a row keeps between the launches. bf16
   // gradients of several pieces need dw's sums in fp32; where all rows at once take no more
   // memory than that, there is one piece.
   const size_t row = (size_t)p.nblk * 8 + (grad ? (size_t)p.lde * (bf16 ? 2 : 10) : 0);
   const size_t sums = grad && bf16 ? (size_t)V * d * 4 : 0;
-  const int64_t all = ((int64_t)T + 255) / 256 * 256;
+  const int64_t all = ceil_div(T, 64) * 64;
   int64_t R = (int64_t)(kPieceBytes / row) / 256 * 256;
   if (R < 256) R = 256;
   if (R >= all || (size_t)all * row <= kPieceBytes + sums) R = all;
-  p.R = p.few ? kFewRows : (int)R;
+  p.R = (int)R;
   p.pieces = (T + p.R - 1) / p.R;
   p.sums = sums && p.pieces > 1;
-  // dx: the vocabulary is split until the launch has two workgroups per CU
-  const int tiles = p.few ? (d + 255) / 256 : (int)(((int64_t)d + 255) / 256 * (p.R / 256));
-  p.S = tiles >= 512 ? 1 : 512 / tiles;
-  const int most = (int)(p.lde / 256);
-  if (p.S > most) p.S = most;
-  if (p.S > 32) p.S = 32;
-  p.ks = (int)((p.lde / 256 + p.S - 1) / p.S) * 256;
-  p.S = (int)((p.lde + p.ks - 1) / p.ks);
+  if (grad) {
+    // dx: the vocabulary split 1, 2, 4, .. 64 times; the partial sums cost their traffic (about 5
+    // bytes per ps)
+    best = 0;
+    for (int c = kLarge; c >= kSmall; c -= kLarge) {
+      const int64_t tiles = ceil_div(d, 256) * ceil_div(p.R, 64 << c);
+      for (int S0 = 1; S0 <= 64 && (S0 == 1 || tiles * S0 <= kCUs * kCostG[c].per_cu); S0 *= 2) {
+        const int64_t ks = ceil_div(ceil_div(V, S0), 64) * 64, S = ceil_div(V, ks);
+        const int64_t n = cost_of(kCostG[c], tiles * S, ks / 32 * np) + (S > 1 ? S * p.R * d * 8 / 5000 : 0);
+        if (!best || cheaper(n, best)) {
+          best = n;
+          p.dc = c;
+          p.S = (int)S;
+          p.ks = (int)ks;
+        }
+      }
+    }
+    best = 0;
+    for (int c = kLarge; c >= kSmall; c -= kLarge) {
+      const int64_t n = cost_of(kCostG[c], ceil_div(d, 256) * ceil_div(V, 64 << c), ceil_div(p.R, 32) * np);
+      if (!best || cheaper(n, best)) {
+        best = n;
+        p.wc = c;
+      }
+    }
+  }
   size_t at = 256;                                        // n_act
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -447,7 +605,13 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
 
 int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 
-template <class Z, class X, typename T, typename ET, typename DXT, typename DWT, int NP>
+// f(Tiles<c>()) for dx and dw
+template <typename F> hipError_t with_tiles(int c, F &&f) {
+  return c == kSmall ? f(Tiles<kSmall>()) : f(Tiles<kLarge>());
+}
+
+// T: type of the operands and results; ET: of e
+template <typename T, typename ET, int NP>
 hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   char *ws = (char *)a.ws;
   int32_t *n_act = (int32_t *)ws, *list = (int32_t *)(ws + p.list), *tgt = (int32_t *)(ws + p.tgt);
@@ -459,54 +623,74 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   bf16_t *g = NP == 1 ? (bf16_t *)e : (bf16_t *)(ws + p.g);
   const int64_t xplane = (int64_t)a.T * a.d, wplane = (int64_t)a.V * a.d, gplane = (int64_t)p.R * p.lde;
   const bool grad = a.dw != nullptr;
-  k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, a.V, list, tgt, pos, n_act);
-  TW_TRY_HIP(hipGetLastError());
-  k_xent_stage<T, DXT><<<a.T, 256, 0, s>>>((const T *)a.x, a.ldx, a.d, pos, xc, xplane, a.loss, a.lse, (DXT *)a.dx);
-  TW_TRY_HIP(hipGetLastError());
-  const bf16_t *w = (const bf16_t *)a.w;
-  if constexpr (NP > 1) {
-    const size_t n = (size_t)a.V * a.d;
-    k_xent_planes<<<(unsigned)((n / 8 + 255) / 256), 256, 0, s>>>((const float *)a.w, n, (bf16_t *)(ws + p.wp));
-    TW_TRY_HIP(hipGetLastError());
-    w = (const bf16_t *)(ws + p.wp);
+  const int pw = block_log(p.zc);
+  const bf16_t *w = NP == 1 ? (const bf16_t *)a.w : (const bf16_t *)(ws + p.wp);
+  if constexpr (NP == 1) {
+    // rows are addressed with 32-bit byte offsets
+    if (p.direct && (a.T == 1 || a.ldx <= (1 << 20))) {
+      typedef Tiles<kSmall>::Z Z;
+      const int mt = (int)ceil_div(a.V, Z::BM);
+      k_xent_logits<Z, 1, ET, false, true><<<grid8(mt), Z::NT, 0, s>>>(w, 0, (const bf16_t *)a.x, a.ldx, 0, a.y, nullptr,
+                                                                       nullptr, 0, a.T, a.V, a.d, mt, 1, nullptr, 0, part,
+                                                                       p.nblk, zt);
+      TW_TRY_HIP(hipGetLastError());
+      k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
+                                                       nullptr, nullptr, 0, nullptr, 0, a.loss, a.lse);
+      return hipGetLastError();
+    }
   }
+  if (a.T > kCountT) {
+    k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, a.V, list, tgt, pos, n_act);
+    TW_TRY_HIP(hipGetLastError());
+  }
+  const int64_t split = NP == 1 ? 0 : ceil_div(wplane, 256 * 8);
+  k_xent_stage<T, T><<<(unsigned)(a.T + split), 256, 0, s>>>((const T *)a.x, a.ldx, a.T, a.d, a.V, a.y,
+                                                             a.T > kCountT ? pos : nullptr, list, tgt, n_act, xc, xplane,
+                                                             a.loss, a.lse, (T *)a.dx, (const T *)a.w, (size_t)wplane,
+                                                             (bf16_t *)(ws + p.wp));
+  TW_TRY_HIP(hipGetLastError());
   for (int q = 0; q < p.pieces; ++q) {
     const int row0 = q * p.R, R = a.T - row0 < p.R ? a.T - row0 : p.R;
-    {
-      const int mt = (int)(p.lde / Z::BM), nt = (R + Z::BN - 1) / Z::BN;
+    auto logits = [&](auto C) {
+      typedef typename decltype(C)::Z Z;
+      // with e kept, the tiles cover its padding too
+      const int mt = (int)ceil_div(grad ? p.lde : a.V, Z::BM), nt = (int)ceil_div(R, Z::BN);
       auto go = [&](auto keep) {
-        k_xent_logits<Z, NP, ET, decltype(keep)::value><<<grid8((int64_t)mt * nt), Z::NT, 0, s>>>(
-            w, wplane, xc, xplane, tgt, n_act, row0, R, a.V, a.d, mt, nt, e, p.lde, part, p.nblk, zt);
+        k_xent_logits<Z, NP, ET, decltype(keep)::value, false><<<grid8((int64_t)mt * nt), Z::NT, 0, s>>>(
+            w, wplane, xc, a.d, xplane, nullptr, tgt, n_act, row0, R, a.V, a.d, mt, nt, e, p.lde, part, p.nblk, zt);
       };
       if (grad) go(std::integral_constant<bool, true>());
       else go(std::integral_constant<bool, false>());
-      TW_TRY_HIP(hipGetLastError());
-    }
-    if (grad)
-      k_xent_join<ET, true, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, tgt, list, n_act, row0, R, a.V, a.dloss, e, p.lde,
-                                                     g, gplane, a.loss, a.lse);
-    else
-      k_xent_join<ET, false, Z::WM><<<R, 256, 0, s>>>(part, p.nblk, zt, tgt, list, n_act, row0, R, a.V, nullptr, e, p.lde,
-                                                      g, gplane, a.loss, a.lse);
+      return hipGetLastError();
+    };
+    TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
+    auto join = [&](auto G) {
+      k_xent_join<ET, decltype(G)::value, false><<<R, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act, row0, R,
+                                                                   a.V, a.dloss, e, p.lde, g, gplane, a.loss, a.lse);
+    };
+    if (grad) join(std::integral_constant<bool, true>());
+    else join(std::integral_constant<bool, false>());
     TW_TRY_HIP(hipGetLastError());
     if (!grad) continue;
-    {
-      const int mt = (a.d + X::BM - 1) / X::BM, nt = (R + X::BN - 1) / X::BN;
-      float *dxp = p.S > 1 ? (float *)(ws + p.dxp) : nullptr;
-      k_xent_dx<X, NP, DXT><<<grid8((int64_t)mt * nt * p.S), X::NT, 0, s>>>(
-          w, wplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt, nt, p.S, p.ks, (DXT *)a.dx, dxp);
-      TW_TRY_HIP(hipGetLastError());
-      if (p.S > 1) {
-        k_xent_dx_sum<DXT><<<(unsigned)((a.d / 8 + 255) / 256 * R), 256, 0, s>>>(dxp, p.S, R, a.d, list, n_act, row0, (DXT *)a.dx);
-        TW_TRY_HIP(hipGetLastError());
-      }
-    }
-    const int mt = (a.d + TileW::BM - 1) / TileW::BM, nt = (a.V + TileW::BN - 1) / TileW::BN;
-    const bool last = q + 1 == p.pieces, f32 = std::is_same<DWT, float>::value;
-    float *sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
-    k_xent_dw<TileW, NP, DWT><<<grid8((int64_t)mt * nt), TileW::NT, 0, s>>>(
-        xc, xplane, g, p.lde, gplane, n_act, row0, R, a.V, a.d, mt, nt, q > 0, sum, last || f32 ? (DWT *)a.dw : nullptr);
-    TW_TRY_HIP(hipGetLastError());
+    float *dxp = p.S > 1 ? (float *)(ws + p.dxp) : nullptr;
+    TW_TRY_HIP(with_tiles(p.dc, [&](auto C) {
+      typedef typename decltype(C)::X X;
+      const int mt = (int)ceil_div(a.d, X::BM), nt = (int)ceil_div(R, X::BN);
+      k_xent_dx<X, NP, T><<<grid8((int64_t)mt * nt * p.S), X::NT, 0, s>>>(
+          w, wplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt, nt, p.S, p.ks, (T *)a.dx, dxp);
+      return hipGetLastError();
+    }));
+    TW_TRY_HIP(with_tiles(p.wc, [&](auto C) {
+      typedef typename decltype(C)::W W;
+      const int mt = (int)ceil_div(a.d, W::BM), nt = (int)ceil_div(a.V, W::BN), tiles = grid8((int64_t)mt * nt);
+      const int adds = p.S > 1 ? (int)ceil_div((int64_t)R * a.d, W::NT * 8) : 0;
+      const bool last = q + 1 == p.pieces, f32 = NP > 1;
+      float *sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
+      k_xent_dw<W, NP, T, T><<<tiles + adds, W::NT, 0, s>>>(xc, xplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt,
+                                                            nt, q > 0, sum, last || f32 ? (T *)a.dw : nullptr, tiles, p.S,
+                                                            dxp, (T *)a.dx);
+      return hipGetLastError();
+    }));
   }
   return hipSuccess;
 }
@@ -522,11 +706,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s) {
     return hipGetLastError();
   }
   const Plan p = plan_of(a.T, a.d, a.V, a.bf16, a.dw != nullptr);
-  if (a.bf16)
-    return p.few ? xent_run<TileZS, TileXS, bf16_t, bf16_t, bf16_t, bf16_t, 1>(a, p, s)
-                 : xent_run<TileZ, TileX, bf16_t, bf16_t, bf16_t, bf16_t, 1>(a, p, s);
-  return p.few ? xent_run<TileZS, TileXS, float, float, float, float, 6>(a, p, s)
-               : xent_run<TileZ, TileX, float, float, float, float, 6>(a, p, s);
+  return a.bf16 ? xent_run<bf16_t, bf16_t, 1>(a, p, s) : xent_run<float, float, 6>(a, p, s);
 }
 
 }  // namespace tw

@@ -270,3 +270,40 @@ def test_graph_and_side_stream(T):
         torch.cuda.synchronize()
         for a, b in zip(out, tw.linear_xent_fwd_bwd(x, w, y, dl)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d,V", [(2049, 328, 2500), (600, 264, 9001), (1030, 520, 20011), (90, 1032, 6007),
+                                   (70, 72, 30001)])
+def test_tile_sizes(T, d, V, dtype):
+    """Calls that take each of the tiles of the three products, ragged in every direction, with the
+    tokens' list counted by its own launch (T > 2048) or not, and dx whole or split."""
+    say("xent tiles", T, d, V, dtype)
+    x, w, y, dl = problem(T + d, T, d, V, dtype, ignored=T // 7)
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, w, y, dl, got)
+    fwd = tw.linear_xent_fwd(x, w, y)
+    check(x, w, y, dl, fwd)
+    for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 2, 40, 64])
+@pytest.mark.parametrize("stride", [0, 264, (1 << 20) + 8])
+def test_few_tokens_in_place(T, stride):
+    """The forward of few bf16 tokens reads x's rows where they lie, however far apart, and skips those
+    without a target (NaN in them reaches nothing)."""
+    d, V = 256, 3001
+    x, w, y, dl = problem(T + 5, T, d, V, BF16, ignored=T // 2)
+    big = torch.empty((T - 1) * max(stride, d) + d, dtype=BF16, device="cuda")
+    far = big.as_strided((T, d), (max(stride, d), 1))
+    far.copy_(x)
+    far[y < 0] = float("nan")
+    got = tw.linear_xent_fwd(far, w, y)
+    check(x, w, y, dl, got)
+    if T > 1:
+        y[1] = V + 3
+        loss, lse = tw.linear_xent_fwd(far, w, y)
+        assert torch.isnan(loss[1])
+        keep = torch.arange(T, device="cuda") != 1
+        assert torch.equal(loss[keep], got[0][keep]) and torch.equal(lse[keep], got[1][keep])
