@@ -179,7 +179,7 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
   const int t = mm_xcd_tile(blockIdx.x, mt * nt);
   if (t < 0) return;
   int m, n, rows;
-  mm_tile_mn<8>(t, mt, nt, m, n);
+  mm_tile_mn<4>(t, mt, nt, m, n);
   const int m0 = m * G::BM, n0 = n * G::BN;
   if constexpr (DIRECT) {
     int64_t v;
@@ -282,6 +282,7 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 // and E the target's: loss = log(1 + R / E) and p - 1 = -R / (R + E), which keep the digits of a token
 // that the model is sure of (R << E), where lse - z and exp(z - lse) - 1 have none left. A target
 // beyond the vocabulary makes loss and G NaN.
+// GRAD: `split` workgroups per row share its columns (each joins the blocks by itself).
 // DIRECT: a workgroup per token of y instead, zeros for one without a target.
 template <typename ET, bool GRAD, bool DIRECT>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, int pw,
@@ -289,11 +290,12 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
                                                    const int32_t *__restrict__ tgts, const int32_t *__restrict__ list,
                                                    const int32_t *__restrict__ n_act, int row0, int R, int V,
                                                    const float *__restrict__ dloss, ET *__restrict__ e, int64_t lde,
-                                                   bf16_t *__restrict__ g, int64_t gplane, float *__restrict__ loss,
-                                                   float *__restrict__ lse) {
+                                                   bf16_t *__restrict__ g, int64_t gplane, int split,
+                                                   float *__restrict__ loss, float *__restrict__ lse) {
   __shared__ float red[8];
   const int wave = threadIdx.x >> 6;
-  int r = blockIdx.x, t, tgt;
+  const int part_of = GRAD ? blockIdx.x % split : 0;
+  int r = GRAD ? blockIdx.x / split : blockIdx.x, t, tgt;
   if constexpr (DIRECT) {
     int64_t v;
     const uint64_t act = wave_list(y, R, v);
@@ -328,22 +330,25 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   const bool bad = tgt >= V;                              // then rest is the sum over all
   const float z = bad ? NAN : zt[row0 + r], et = bad ? 0.f : expf(z - ref), all = rest + et;
   const float ls = logf(all), l = ref + ls;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && part_of == 0) {
     lse[t] = l;
     loss[t] = et > 0.5f ? log1pf(rest / et) : (ref - z) + ls;
   }
   if constexpr (GRAD) {
-    const float dl = bad ? NAN : dloss[t];
-    for (int i = threadIdx.x * 8; i < lde; i += 256 * 8) {
+    const float dl = bad ? NAN : dloss[t], at_target = -rest / all * dl;
+    for (int i = (part_of * 256 + threadIdx.x) * 8; i < lde; i += split * 256 * 8) {
       const int b = i >> pw;                              // one block covers the 8 columns
       const float f = b < nblk ? expf(p[b].x - l) * dl : 0.f;
       float v[8];
       load8(e + (size_t)r * lde + i, v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = i + k < V ? v[k] * f : 0.f;
-        if (i + k == tgt) v[k] = -rest / all * dl;
-      }
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      if ((uint32_t)(tgt - i) < 8u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i + k == tgt ? at_target : v[k];
+      if (i + 8 > V)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i + k < V ? v[k] : 0.f;
       if constexpr (std::is_same<ET, float>::value) {
         split8(v, g + (size_t)r * lde + i, gplane);
       } else {
@@ -469,8 +474,9 @@ __global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t
 
 // ------------------------------------------------------------------------------------- plan
 
-// The products' tiles. Large: 8 waves of 64 x 128, one workgroup per CU, the least traffic per
-// operation. The smaller ones, two workgroups per CU, are for calls whose large tiles would leave CUs
+// The products' tiles. Large: 8 waves of 64 x 128 (logits: 128 x 64, and groups of 4 tiles of the
+// vocabulary: 6.74 ms against 6.90 at T = 8192, d = 4096, V = 128000), one workgroup per CU, the least
+// traffic per operation. The smaller ones, two workgroups per CU, are for calls whose large tiles would leave CUs
 // idle or hold mostly rows that do not exist. The smallest logits tile's ring of four 64-k stages
 // keeps 24 KB of w per workgroup in flight, for few tokens, where the stream of w is all there is.
 enum { kSmall, kMid, kLarge };
@@ -484,7 +490,7 @@ template <> struct Tiles<kMid> {
   typedef MM64<128, 128, 64, 64, 3, 2> Z;
 };
 template <> struct Tiles<kLarge> {
-  typedef MM64<256, 256, 64, 128, 3, 2> Z;
+  typedef MM64<256, 256, 128, 64, 3, 2> Z;
   typedef MM<256, 256, 64, 128, 4, true, false> X;
   typedef MM<256, 256, 64, 128, 4, true, true> W;
 };
@@ -516,8 +522,8 @@ bool cheaper(int64_t n, int64_t best) { return n * 10 < best * 9; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // log2 of the logits tile's columns per wave
-int block_log(int c) { return c == kSmall ? 4 : 6; }
-static_assert(Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 64, "block_log");
+int block_log(int c) { return c == kSmall ? 4 : c == kMid ? 6 : 7; }
+static_assert(Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 128, "block_log");
 
 struct Plan {
   int R, pieces, nblk, S, ks, zc, dc, wc;                 // zc, dc, wc: classes of logits, dx, dw
@@ -635,7 +641,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
                                                                        p.nblk, zt);
       TW_TRY_HIP(hipGetLastError());
       k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
-                                                       nullptr, nullptr, 0, nullptr, 0, a.loss, a.lse);
+                                                       nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse);
       return hipGetLastError();
     }
   }
@@ -664,9 +670,13 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       return hipGetLastError();
     };
     TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
+    // a row's columns go to several workgroups where rows alone would leave CUs idle
+    int split = 1;
+    while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;
     auto join = [&](auto G) {
-      k_xent_join<ET, decltype(G)::value, false><<<R, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act, row0, R,
-                                                                   a.V, a.dloss, e, p.lde, g, gplane, a.loss, a.lse);
+      k_xent_join<ET, decltype(G)::value, false><<<R * split, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
+                                                                           row0, R, a.V, a.dloss, e, p.lde, g, gplane, split,
+                                                                           a.loss, a.lse);
     };
     if (grad) join(std::integral_constant<bool, true>());
     else join(std::integral_constant<bool, false>());

@@ -307,3 +307,28 @@ def test_few_tokens_in_place(T, stride):
         assert torch.isnan(loss[1])
         keep = torch.arange(T, device="cuda") != 1
         assert torch.equal(loss[keep], got[0][keep]) and torch.equal(lse[keep], got[1][keep])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d,V", [(60, 64, 20011), (300, 72, 2500), (2100, 64, 9000)])
+def test_logits_far_from_zero(T, d, V, dtype):
+    """Tokens whose logits lie around -100 .. 100: exponentials without a reference, with one in some or
+    all blocks of a row, and rows beyond the range in which a factor per token can stand for one."""
+    say("xent shifted", T, d, V, dtype)
+    x, w, y, dl = problem(T + V, T, d, V, dtype, ignored=T // 9)
+    w[:, 0] = 1
+    shift = torch.tensor([0.0, -8, -15, -30, -100, 8, 20, 55, 70, 100, -60, 12], device="cuda")
+    x[:, 0] = shift[torch.arange(T, device="cuda") % 12].to(dtype)
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, w, y, dl, got)
+    for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
+        assert torch.equal(a, b)
+    fwd = tw.linear_xent_fwd(x, w, y)
+    check(x, w, y, dl, fwd)
+
+
+@pytest.mark.parametrize("T,dtype", [(1500, F32), (2600, F32)])
+def test_more_pieces(T, dtype):
+    """Two and more pieces of fp32 rows."""
+    x, w, y, dl = problem(17, T, 64, 128000, dtype, ignored=T // 3)
+    check(x, w, y, dl, tw.linear_xent_fwd_bwd(x, w, y, dl))
