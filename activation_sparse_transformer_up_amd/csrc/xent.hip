@@ -336,24 +336,37 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   }
   if constexpr (GRAD) {
     const float dl = bad ? NAN : dloss[t], at_target = -rest / all * dl;
-    for (int i = (part_of * 256 + threadIdx.x) * 8; i < lde; i += split * 256 * 8) {
-      const int b = i >> pw;                              // one block covers the 8 columns
-      const float f = b < nblk ? expf(p[b].x - l) * dl : 0.f;
-      float v[8];
-      load8(e + (size_t)r * lde + i, v);
+    constexpr int kAt = 4;                                // units in flight: loads before any store
+    const int step = split * 256 * 8;
+    for (int i0 = (part_of * 256 + threadIdx.x) * 8; i0 < lde; i0 += kAt * step) {
+      Raw8<ET> raw[kAt];
+      float f[kAt];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= f;
-      if ((uint32_t)(tgt - i) < 8u)
+      for (int q = 0; q < kAt; ++q) {
+        const int i = i0 + q * step, b = i >> pw;         // one block covers the 8 columns
+        if (i < lde) raw[q].load(e + (size_t)r * lde + i);
+        f[q] = b < nblk ? p[b].x : 0.f;
+      }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k == tgt ? at_target : v[k];
-      if (i + 8 > V)
+      for (int q = 0; q < kAt; ++q) {
+        const int i = i0 + q * step;
+        if (i >= lde) break;
+        f[q] = expf(f[q] - l) * dl;
+        float v[8];
+        raw[q].to(v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k < V ? v[k] : 0.f;
-      if constexpr (std::is_same<ET, float>::value) {
-        split8(v, g + (size_t)r * lde + i, gplane);
-      } else {
-        *(uint4 *)(e + (size_t)r * lde + i) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                         pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        for (int k = 0; k < 8; ++k) v[k] *= f[q];
+        if ((uint32_t)(tgt - i) < 8u)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = i + k == tgt ? at_target : v[k];
+        if (i + 8 > V)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = i + k < V ? v[k] : 0.f;
+        if constexpr (std::is_same<ET, float>::value) {
+          split8(v, g + (size_t)r * lde + i, gplane);
+        } else {
+          store8(e + (size_t)r * lde + i, v);
+        }
       }
     }
   }
@@ -361,30 +374,38 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 
 // --------------------------------------------------------------------------------- gradients
 
-// dx: D[column of d][token] = w^T G^T over the vocabulary range of split blockIdx.x / tiles
-// (w across k, G along k). One split: to the token's row of dx; several: fp32 partial sums.
-template <class G, int NP, typename DXT>
-__global__ __launch_bounds__(G::NT) void k_xent_dx(const bf16_t *__restrict__ w, int64_t wplane,
-                                                   const bf16_t *__restrict__ g, int64_t lde, int64_t gplane,
-                                                   const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
-                                                   int row0, int R, int V, int d, int mt, int nt, int S, int ks,
-                                                   DXT *__restrict__ dx, float *__restrict__ part) {
-  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
-  const int t = mm_xcd_tile(blockIdx.x, mt * nt * S);
+// What the gradients' products read and write, for rows [row0, row0 + R) of the list.
+template <typename T> struct GradPiece {
+  const bf16_t *w, *xc, *g;
+  int64_t wplane, xplane, gplane, lde;
+  const int32_t *list, *n_act;
+  int row0, R, V, d;
+  int S, ks;                                              // dx: splits of the vocabulary, columns in each
+  T *dx;
+  float *part;                                            // dx's partial sums [S][R][d] (S > 1)
+  bool add;                                               // dw: to the sums of earlier pieces
+  float *sum;                                             // which are here
+  T *dw;                                                  // NULL until the last piece
+};
+
+// dx: D[column of d][token] = w^T G^T over the vocabulary range of split b / tiles (w across k, G
+// along k), workgroup b. One split: to the token's row of dx; several: fp32 partial sums.
+template <class G, int NP, typename T> TW_DEV void dx_tile(const GradPiece<T> &a, int b, char *smem) {
+  const int mt = (a.d + G::BM - 1) / G::BM, nt = (a.R + G::BN - 1) / G::BN, t = mm_xcd_tile(b, mt * nt * a.S);
   if (t < 0) return;
   int m, n;
   const int sp = t / (mt * nt);
   mm_tile_mn<8>(t % (mt * nt), mt, nt, m, n);
-  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(n_act, row0, R);
+  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(a.n_act, a.row0, a.R);
   if (n0 >= rows) return;
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
   for (int i = 0; i < G::FM; ++i)
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
-  const int k0 = sp * ks, k1 = min(V, k0 + ks);
-  const MmOperand A = {w + (size_t)k0 * d + m0, d, wplane, min(d - m0, G::BM)};
-  const MmOperand B = {g + (size_t)n0 * lde + k0, lde, gplane, min(rows - n0, G::BN)};
+  const int k0 = sp * a.ks, k1 = min(a.V, k0 + a.ks);
+  const MmOperand A = {a.w + (size_t)k0 * a.d + m0, a.d, a.wplane, min(a.d - m0, G::BM)};
+  const MmOperand B = {a.g + (size_t)n0 * a.lde + k0, a.lde, a.gplane, min(rows - n0, G::BN)};
   if (k0 < k1) mm_loop<G, NP>(A, B, k1 - k0, acc, smem);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -393,58 +414,51 @@ __global__ __launch_bounds__(G::NT) void k_xent_dx(const bf16_t *__restrict__ w,
   for (int fn = 0; fn < G::FN; ++fn) {
     const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);
     if (r >= rows) continue;
-    const size_t at = S == 1 ? (size_t)list[row0 + r] * d : ((size_t)sp * R + r) * d;
+    const size_t at = a.S == 1 ? (size_t)a.list[a.row0 + r] * a.d : ((size_t)sp * a.R + r) * a.d;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) {
       const int c = m0 + wm * G::WM + fm * 16 + (lane >> 4) * 4;
-      if (c >= d) continue;                               // d is a multiple of 8
+      if (c >= a.d) continue;                             // d is a multiple of 8
       const f32x4_t v = acc[fm][fn];
-      if (S > 1) *(f32x4_t *)(part + at + c) = v;
-      else if constexpr (std::is_same<DXT, float>::value) *(f32x4_t *)(dx + at + c) = v;
-      else *(uint2 *)(dx + at + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      if (a.S > 1) *(f32x4_t *)(a.part + at + c) = v;
+      else if constexpr (std::is_same<T, float>::value) *(f32x4_t *)(a.dx + at + c) = v;
+      else *(uint2 *)(a.dx + at + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     }
   }
 }
 
-// dw: D[column of d][vocabulary] = x^T G over the piece's tokens (both across k). sum: fp32 sums
-// of the pieces so far (added where `add`, written where dw is NULL; may be dw itself). The
-// workgroups from `tiles` on add dx's S partial sums, which are complete when this launch begins.
-template <class G, int NP, typename DWT, typename DXT>
-__global__ __launch_bounds__(G::NT) void k_xent_dw(const bf16_t *__restrict__ xc, int64_t xplane,
-                                                   const bf16_t *__restrict__ g, int64_t lde, int64_t gplane,
-                                                   const int32_t *__restrict__ list, const int32_t *__restrict__ n_act,
-                                                   int row0, int R, int V, int d, int mt, int nt, bool add, float *sum,
-                                                   DWT *dw, int tiles, int S, const float *__restrict__ part,
-                                                   DXT *__restrict__ dx) {
-  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
-  const int rows = piece_rows(n_act, row0, R);
-  if ((int)blockIdx.x >= tiles) {
-    const size_t i = ((size_t)(blockIdx.x - tiles) * G::NT + threadIdx.x) * 8;
-    const int r = (int)(i / d), c = (int)(i % d);         // d is a multiple of 8
-    if (r >= rows) return;
-    float a[8] = {};
-    for (int s = 0; s < S; ++s) {
-      float v[8];
-      load8(part + (size_t)s * R * d + i, v);
+// Adds dx's S partial sums, 8 elements per thread, workgroup b of NT threads.
+template <int NT, typename T> TW_DEV void dx_sum(const GradPiece<T> &a, int b) {
+  const size_t i = ((size_t)b * NT + threadIdx.x) * 8;
+  const int r = (int)(i / a.d), c = (int)(i % a.d);       // d is a multiple of 8
+  if (r >= piece_rows(a.n_act, a.row0, a.R)) return;
+  float v[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < a.S; ++s) {
+    float u[8];
+    load8(a.part + (size_t)s * a.R * a.d + i, u);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] += v[k];
-    }
-    store8(dx + (size_t)list[row0 + r] * d + c, a);
-    return;
+    for (int k = 0; k < 8; ++k) v[k] += u[k];
   }
-  const int t = mm_xcd_tile(blockIdx.x, mt * nt);
+  store8(a.dx + (size_t)a.list[a.row0 + r] * a.d + c, v);
+}
+
+// dw: D[column of d][vocabulary] = x^T G over the piece's tokens (both across k), workgroup b. sum: fp32
+// sums of the pieces so far (added where `add`, written where dw is NULL; may be dw itself).
+template <class G, int NP, typename T> TW_DEV void dw_tile(const GradPiece<T> &a, int b, char *smem) {
+  const int mt = (a.d + G::BM - 1) / G::BM, nt = (a.V + G::BN - 1) / G::BN, t = mm_xcd_tile(b, mt * nt);
   if (t < 0) return;
   int m, n;
   mm_tile_mn<8>(t, mt, nt, m, n);
-  const int m0 = m * G::BM, n0 = n * G::BN;
+  const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(a.n_act, a.row0, a.R);
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
   for (int i = 0; i < G::FM; ++i)
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
-  const MmOperand A = {xc + (size_t)row0 * d + m0, d, xplane, min(d - m0, G::BM)};
+  const MmOperand A = {a.xc + (size_t)a.row0 * a.d + m0, a.d, a.xplane, min(a.d - m0, G::BM)};
   // the padding of G's rows up to lde is zero
-  const MmOperand B = {g + n0, lde, gplane, (int)min(lde - n0, (int64_t)G::BN)};
+  const MmOperand B = {a.g + n0, a.lde, a.gplane, (int)min(a.lde - n0, (int64_t)G::BN)};
   mm_loop<G, NP>(A, B, rows, acc, smem);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -452,20 +466,44 @@ __global__ __launch_bounds__(G::NT) void k_xent_dw(const bf16_t *__restrict__ xc
 #pragma unroll
   for (int fn = 0; fn < G::FN; ++fn) {
     const int v = n0 + wn * G::WN + fn * 16 + (lane & 15);
-    if (v >= V) continue;
+    if (v >= a.V) continue;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) {
       const int c = m0 + wm * G::WM + fm * 16 + (lane >> 4) * 4;
-      if (c >= d) continue;
-      const size_t at = (size_t)v * d + c;
-      f32x4_t a = acc[fm][fn];
-      if (add) a += *(const f32x4_t *)(sum + at);
-      if (!dw) *(f32x4_t *)(sum + at) = a;
-      else if constexpr (std::is_same<DWT, float>::value) *(f32x4_t *)(dw + at) = a;
-      else *(uint2 *)(dw + at) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
+      if (c >= a.d) continue;
+      const size_t at = (size_t)v * a.d + c;
+      f32x4_t u = acc[fm][fn];
+      if (a.add) u += *(const f32x4_t *)(a.sum + at);
+      if (!a.dw) *(f32x4_t *)(a.sum + at) = u;
+      else if constexpr (std::is_same<T, float>::value) *(f32x4_t *)(a.dw + at) = u;
+      else *(uint2 *)(a.dw + at) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
     }
   }
 }
+
+template <class X, int NP, typename T> __global__ __launch_bounds__(X::NT) void k_xent_dx(GradPiece<T> a) {
+  __shared__ __attribute__((aligned(16))) char smem[X::SMEM];
+  dx_tile<X, NP>(a, blockIdx.x, smem);
+}
+
+// The workgroups from `tiles` on add dx's partial sums, which are complete when this launch begins.
+template <class W, int NP, typename T> __global__ __launch_bounds__(W::NT) void k_xent_dw(GradPiece<T> a, int tiles) {
+  __shared__ __attribute__((aligned(16))) char smem[W::SMEM];
+  if ((int)blockIdx.x < tiles) dw_tile<W, NP>(a, blockIdx.x, smem);
+  else dx_sum<W::NT>(a, blockIdx.x - tiles);
+}
+
+// Both products in one launch (dw's workgroups from `tiles` on), where each alone is too small to
+// fill the GPU: T = 128, d = 256, V = 1009 in fp32 30 us one after the other, 18 together and 4 for the sum of dx.
+template <class X, class W, int NP, typename T>
+__global__ __launch_bounds__(X::NT) void k_xent_dx_dw(GradPiece<T> a, int tiles) {
+  static_assert(X::NT == W::NT, "threads");
+  __shared__ __attribute__((aligned(16))) char smem[X::SMEM > W::SMEM ? X::SMEM : W::SMEM];
+  if ((int)blockIdx.x < tiles) dx_tile<X, NP>(a, blockIdx.x, smem);
+  else dw_tile<W, NP>(a, blockIdx.x - tiles, smem);
+}
+
+template <typename T> __global__ __launch_bounds__(256) void k_xent_dx_sum(GradPiece<T> a) { dx_sum<256>(a, blockIdx.x); }
 
 __global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t n) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -682,23 +720,39 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     else join(std::integral_constant<bool, false>());
     TW_TRY_HIP(hipGetLastError());
     if (!grad) continue;
-    float *dxp = p.S > 1 ? (float *)(ws + p.dxp) : nullptr;
+    const bool last = q + 1 == p.pieces, f32 = NP > 1;
+    GradPiece<T> gp;
+    gp.w = w; gp.xc = xc; gp.g = g;
+    gp.wplane = wplane; gp.xplane = xplane; gp.gplane = gplane; gp.lde = p.lde;
+    gp.list = list; gp.n_act = n_act;
+    gp.row0 = row0; gp.R = R; gp.V = a.V; gp.d = a.d;
+    gp.S = p.S; gp.ks = p.ks;
+    gp.dx = (T *)a.dx; gp.part = p.S > 1 ? (float *)(ws + p.dxp) : nullptr;
+    gp.add = q > 0;
+    gp.sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
+    gp.dw = last || f32 ? (T *)a.dw : nullptr;
+    auto dx_grid = [&](auto X) { return grid8(ceil_div(a.d, decltype(X)::BM) * ceil_div(R, decltype(X)::BN) * p.S); };
+    auto dw_grid = [&](auto W) { return grid8(ceil_div(a.d, decltype(W)::BM) * ceil_div(a.V, decltype(W)::BN)); };
+    auto sum_grid = [&](int nt) { return p.S > 1 ? (int)ceil_div((int64_t)R * a.d, nt * 8) : 0; };
+    if (p.dc == kSmall && p.wc == kSmall) {
+      typedef Tiles<kSmall>::X X;
+      typedef Tiles<kSmall>::W W;
+      const int tiles = dx_grid(X());
+      k_xent_dx_dw<X, W, NP><<<tiles + dw_grid(W()), X::NT, 0, s>>>(gp, tiles);
+      TW_TRY_HIP(hipGetLastError());
+      if (p.S > 1) k_xent_dx_sum<<<sum_grid(256), 256, 0, s>>>(gp);
+      TW_TRY_HIP(hipGetLastError());
+      continue;
+    }
     TW_TRY_HIP(with_tiles(p.dc, [&](auto C) {
       typedef typename decltype(C)::X X;
-      const int mt = (int)ceil_div(a.d, X::BM), nt = (int)ceil_div(R, X::BN);
-      k_xent_dx<X, NP, T><<<grid8((int64_t)mt * nt * p.S), X::NT, 0, s>>>(
-          w, wplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt, nt, p.S, p.ks, (T *)a.dx, dxp);
+      k_xent_dx<X, NP><<<dx_grid(X()), X::NT, 0, s>>>(gp);
       return hipGetLastError();
     }));
     TW_TRY_HIP(with_tiles(p.wc, [&](auto C) {
       typedef typename decltype(C)::W W;
-      const int mt = (int)ceil_div(a.d, W::BM), nt = (int)ceil_div(a.V, W::BN), tiles = grid8((int64_t)mt * nt);
-      const int adds = p.S > 1 ? (int)ceil_div((int64_t)R * a.d, W::NT * 8) : 0;
-      const bool last = q + 1 == p.pieces, f32 = NP > 1;
-      float *sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
-      k_xent_dw<W, NP, T, T><<<tiles + adds, W::NT, 0, s>>>(xc, xplane, g, p.lde, gplane, list, n_act, row0, R, a.V, a.d, mt,
-                                                            nt, q > 0, sum, last || f32 ? (T *)a.dw : nullptr, tiles, p.S,
-                                                            dxp, (T *)a.dx);
+      const int tiles = dw_grid(W());
+      k_xent_dw<W, NP><<<tiles + sum_grid(W::NT), W::NT, 0, s>>>(gp, tiles);
       return hipGetLastError();
     }));
   }
