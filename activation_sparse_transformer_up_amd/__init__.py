@@ -540,8 +540,9 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, y_dty
     mean, rstd = x.new_empty((2, T), dtype=torch.float32).unbind() if want_stats else (None, None)
     (xp, ldx), (rp, ldr) = _rows(x, d), _rows(residual, d)
     _check(lib().layer_norm_fwd(xp, ldx, rp, ldr, _vec(weight, d, "weight"), _vec(bias, d, "bias"), _dt(x.dtype), T, d,
-                                eps, _ptr(y), _dt(y.dtype), _ptr(s) if residual is not None else None, _ptr(mean),
-                                _ptr(rstd), _stream(x.device)), "layer_norm_fwd")
+                                eps, y.data_ptr(), _dt(y.dtype), s.data_ptr() if residual is not None else None,
+                                mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
+                                _stream(x.device)), "layer_norm_fwd")
     return y, s, mean, rstd
 
 
@@ -567,8 +568,8 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype |
         workspace = s.new_empty((need,), dtype=torch.uint8)
     (yp, lddy), (sp, lds), (rp, lddr) = _rows(dy, d), _rows(s, d), _rows(dres, d)
     _check(lib().layer_norm_bwd(yp, lddy, _dt(dy.dtype), sp, lds, _dt(s.dtype), _vec(weight, d, "weight"),
-                                _vec(mean, T, "mean"), _vec(rstd, T, "rstd"), rp, lddr, T, d, _ptr(dx), _dt(dx.dtype),
-                                _ptr(dw), _ptr(db), _ptr(workspace),
+                                _vec(mean, T, "mean"), _vec(rstd, T, "rstd"), rp, lddr, T, d, dx.data_ptr(), _dt(dx.dtype),
+                                dw.data_ptr(), _ptr(db), _ptr(workspace),
                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                 _stream(s.device)), "layer_norm_bwd")
     return dx, dw, db
@@ -587,9 +588,9 @@ def _xent_io(x, w, targets, workspace, want_grad):
         raise ValueError(f"w must be [V][{d}], got {tuple(w.shape)}")
     if workspace is None:
         need = linear_xent_workspace_bytes(T, d, V, x.dtype, want_grad)
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=x.device)
-    loss = torch.empty((T,), dtype=torch.float32, device=x.device)
-    lse = torch.empty((T,), dtype=torch.float32, device=x.device)
+        workspace = x.new_empty((max(need, 16),), dtype=torch.uint8)
+    loss = x.new_empty((T,), dtype=torch.float32)
+    lse = torch.empty_like(loss)
     return T, d, V, _vec(targets, T, "targets", torch.int64), workspace, loss, lse
 
 
@@ -598,7 +599,7 @@ def linear_xent_fwd(x, w, targets, workspace: torch.Tensor | None = None):
     (loss, lse), fp32 [T]. x [T][d] may have a row stride; w [V][d] in x's dtype."""
     T, d, V, tp, workspace, loss, lse = _xent_io(x, w, targets, workspace, False)
     xp, ldx = _rows(x, d)
-    _check(lib().linear_xent_fwd(xp, ldx, _ptr(w), tp, _dt(x.dtype), T, d, V, _ptr(loss), _ptr(lse), _ptr(workspace),
+    _check(lib().linear_xent_fwd(xp, ldx, _ptr(w), tp, _dt(x.dtype), T, d, V, loss.data_ptr(), lse.data_ptr(), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(x.device)), "linear_xent_fwd")
     return loss, lse
 
@@ -607,11 +608,11 @@ def linear_xent_fwd_bwd(x, w, targets, dloss, workspace: torch.Tensor | None = N
     """The same with the gradients of sum(dloss * loss) (dloss fp32 [T]): (loss, lse, dx, dw), dx
     and dw in x's dtype. No [T][V] array of logits is formed."""
     T, d, V, tp, workspace, loss, lse = _xent_io(x, w, targets, workspace, True)
-    dx = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    dw = torch.empty((V, d), dtype=x.dtype, device=x.device)
+    dx = _rows_like(x)
+    dw = torch.empty_like(w)
     xp, ldx = _rows(x, d)
-    _check(lib().linear_xent_fwd_bwd(xp, ldx, _ptr(w), tp, _vec(dloss, T, "dloss"), _dt(x.dtype), T, d, V, _ptr(loss),
-                                     _ptr(lse), _ptr(dx), _ptr(dw), _ptr(workspace),
+    _check(lib().linear_xent_fwd_bwd(xp, ldx, _ptr(w), tp, _vec(dloss, T, "dloss"), _dt(x.dtype), T, d, V, loss.data_ptr(),
+                                     lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(x.device)),
            "linear_xent_fwd_bwd")
     return loss, lse, dx, dw
