@@ -59,7 +59,7 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> str
 // p: element (first row of the tile, k = 0) for an operand along k, (k = 0, first column of the
 // tile) for one across k; ld: elements between rows; n: rows (columns) of the tile that exist (a
 // multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand; rows: where
-// the tile's rows are not consecutive, their numbers (n of them, in LDS).
+// the tile's rows are not consecutive, their numbers (n of them, in LDS; mm_loop64: may lie in smem).
 struct MmOperand {
   const uint16_t *p;
   int64_t ld, plane;
@@ -286,6 +286,7 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
   }
   const int nk = (K + 63) / 64 * NP;
   if (nk == 0) return;
+  if (B.rows) __syncthreads();                            // the numbers lie where the loads go
 
   // term, k and place of the next stage to load, of B and of A. Loads past the last stage fill a free
   // place with zeros: the count of the waits stays the same.

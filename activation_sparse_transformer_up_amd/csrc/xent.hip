@@ -14,9 +14,9 @@
 //
 // Tokens without a target (negative) take no part: the rows with one are gathered first, in
 // order, and all products run over that list (its length stays on the device; workgroups beyond
-// it leave at once). Whatever such rows hold, also NaN, reaches nothing. The forward of at most 64
+// it leave at once). Whatever such rows hold, also NaN, reaches nothing. The forward of at most 512
 // bf16 tokens makes the list in every workgroup instead and reads the rows of x where they lie,
-// which saves a launch.
+// which saves a launch (one pass alone, T = 333, d = 2048, V = 50021: 85 -> 82 us).
 //
 // Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is; dw is summed
 // over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h).
@@ -151,20 +151,39 @@ __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int
 // Tokens [row0, row0 + R) of the list that exist.
 TW_DEV int piece_rows(const int32_t *n_act, int row0, int R) { return min(max(*n_act - row0, 0), R); }
 
-// The list of at most 64 tokens, in a wave's registers: bit t of the result is set where token t
-// has a target; v is lane t's target.
-TW_DEV uint64_t wave_list(const int64_t *y, int T, int64_t &v) {
-  const int lane = threadIdx.x & 63;
-  v = lane < T ? y[lane] : -1;
-  return ballot64(v >= 0);
+constexpr int kDirectRows = 512;                          // tokens of the forward without a gather
+
+// The list of T <= kDirectRows tokens, made by a workgroup of NT threads in LDS (list: kDirectRows + 8
+// ints, to be read after a barrier); returns its length, in every thread.
+template <int NT> TW_DEV int block_list(const int64_t *y, int T, int *list) {
+  constexpr int PER = kDirectRows / NT, NW = NT / 64;     // tokens of a thread, NT apart
+  const int wave = threadIdx.x >> 6;
+  uint64_t act[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int t = i * NT + threadIdx.x;
+    act[i] = ballot64(t < T && y[t] >= 0);
+    if ((threadIdx.x & 63) == 0) list[kDirectRows + i * NW + wave] = __popcll(act[i]);
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int c = list[kDirectRows + i * NW + w];
+      if (w == wave && (act[i] >> (threadIdx.x & 63) & 1)) list[n + mbcnt64(act[i])] = i * NT + threadIdx.x;
+      n += c;
+    }
+  return n;
 }
 
 // D[vocabulary][token] = w x^T: a lane holds 4 consecutive logits of a token per block, so that a
 // token's maximum and sum are taken over a lane's registers and two exchanges, and e is stored 4
 // elements at a time. part[token][block of WM columns] = (max, sum of exp(z - max) over all but the
 // target), zt[token] = the target's logit.
-// DIRECT: xc is x itself with rows ldx apart, y the targets of its R <= 64 tokens; the list is made
-// here.
+// DIRECT: xc is x itself with rows ldx apart, y the targets of its R <= kDirectRows tokens; the list
+// is made here.
 template <class G, int NP, typename ET, bool KEEP, bool DIRECT>
 __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict__ w, int64_t wplane,
                                                        const bf16_t *__restrict__ xc, int64_t ldx, int64_t xplane,
@@ -172,28 +191,42 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
                                                        const int32_t *__restrict__ n_act, int row0, int R, int V, int d,
                                                        int mt, int nt, ET *__restrict__ e, int64_t lde,
                                                        float2 *__restrict__ part, int nblk, float *__restrict__ zt) {
-  // one LDS object: next to a second one the compiler takes the fragment reads for users of the
-  // loads in flight, and waits
-  __shared__ __attribute__((aligned(16))) char smem[G::SMEM + (DIRECT ? 512 : 0)];
-  int *rowl = (int *)(smem + G::SMEM), *tgtl = rowl + 64;
+  // The list of DIRECT lies in the same LDS object: next to a second one the compiler takes the
+  // fragment reads for users of the loads in flight, and waits.
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  static_assert(G::SMEM >= (kDirectRows + 8) * 4 && kDirectRows / G::NT * (G::NT / 64) <= 8, "list");
   const int t = mm_xcd_tile(blockIdx.x, mt * nt);
   if (t < 0) return;
   int m, n, rows;
   mm_tile_mn<4>(t, mt, nt, m, n);
   const int m0 = m * G::BM, n0 = n * G::BN;
-  if constexpr (DIRECT) {
-    int64_t v;
-    const uint64_t act = wave_list(y, R, v);
-    rows = __popcll(act);
-    if (threadIdx.x < 64 && v >= 0) {
-      rowl[mbcnt64(act)] = threadIdx.x;
-      tgtl[mbcnt64(act)] = v < V ? (int)v : V;
-    }
-    __syncthreads();
-  } else {
-    rows = piece_rows(n_act, row0, R);
-  }
+  int *rowl = (int *)smem;
+  if constexpr (DIRECT) rows = block_list<G::NT>(y, R, rowl);
+  else rows = piece_rows(n_act, row0, R);
   if (n0 >= rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+  const int v0 = m0 + wm * G::WM, blk = v0 / G::WM;       // this wave's block of the vocabulary
+  int toff[G::FN];                                        // each row's target as a column of the block
+  auto targets = [&]() {
+#pragma unroll
+    for (int fn = 0; fn < G::FN; ++fn) {
+      const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);          // row of the piece
+      toff[fn] = -1;
+      if (r < rows) {
+        if constexpr (DIRECT) {
+          const int64_t v = y[rowl[r]];
+          toff[fn] = (v < V ? (int)v : V) - v0;
+        } else {
+          toff[fn] = tgt[row0 + r] - v0;
+        }
+      }
+    }
+  };
+  if constexpr (DIRECT) {                                 // before the loads take the list's place
+    __syncthreads();
+    targets();
+  }
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
   for (int i = 0; i < G::FM; ++i)
@@ -201,18 +234,10 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
   const MmOperand A = {w + (size_t)m0 * d, d, wplane, min(V - m0, G::BM)};
   const MmOperand B = {xc + (DIRECT ? 0 : (size_t)(row0 + n0) * d), ldx, xplane, min(rows - n0, G::BN),
-                       DIRECT ? rowl : nullptr};
+                       DIRECT ? rowl + n0 : nullptr};
   mm_loop64<G, NP>(A, B, d, acc, smem);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
-  const int wm = wave / G::NWN, wn = wave % G::NWN;
-  const int v0 = m0 + wm * G::WM, blk = v0 / G::WM;       // this wave's block of the vocabulary
-  int toff[G::FN];                                        // each row's target as a column of the block
-#pragma unroll
-  for (int fn = 0; fn < G::FN; ++fn) {
-    const int r = n0 + wn * G::WN + fn * 16 + (lane & 15);          // row of the piece
-    toff[fn] = r < rows ? (DIRECT ? tgtl[r] : tgt[row0 + r]) - v0 : -1;
-  }
+  if constexpr (!DIRECT) targets();
   if (v0 + G::WM > V)                                     // the last block ends inside the vocabulary
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm)
@@ -297,24 +322,36 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   const int part_of = GRAD ? blockIdx.x % split : 0;
   int r = GRAD ? blockIdx.x / split : blockIdx.x, t, tgt;
   if constexpr (DIRECT) {
-    int64_t v;
-    const uint64_t act = wave_list(y, R, v);
     t = r;
-    const int64_t vt = __shfl(v, t, 64);
-    if (vt < 0) {
+    const int64_t v = y[t];
+    if (v < 0) {
       if (threadIdx.x == 0) loss[t] = lse[t] = 0.f;
       return;
     }
-    r = __popcll(act & ((1ull << t) - 1));
-    tgt = vt < V ? (int)vt : V;
+    int c = 0;                                            // tokens of the list before this one
+    for (int i = threadIdx.x; i < t; i += 256) c += y[i] >= 0;
+    c = wave_sum(c);
+    if ((threadIdx.x & 63) == 0) red[wave] = __int_as_float(c);
+    __syncthreads();
+    r = 0;
+    for (int i = 0; i < 4; ++i) r += __float_as_int(red[i]);
+    __syncthreads();
+    tgt = v < V ? (int)v : V;
   } else {
     if (r >= piece_rows(n_act, row0, R)) return;
     t = list[row0 + r];
     tgt = tgts[row0 + r];
   }
   const float2 *p = part + (size_t)r * nblk;
+  // a thread's first blocks stay in registers between the two passes
+  constexpr int kB = 8;
+  float2 b[kB];
+#pragma unroll
+  for (int k = 0; k < kB; ++k) b[k] = threadIdx.x + k * 256 < nblk ? p[threadIdx.x + k * 256] : make_float2(-INFINITY, 0.f);
   float mx = -INFINITY;
-  for (int i = threadIdx.x; i < nblk; i += 256) mx = fmaxf(mx, p[i].x);
+#pragma unroll
+  for (int k = 0; k < kB; ++k) mx = fmaxf(mx, b[k].x);
+  for (int i = threadIdx.x + kB * 256; i < nblk; i += 256) mx = fmaxf(mx, p[i].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
   if ((threadIdx.x & 63) == 0) red[wave] = mx;
@@ -322,7 +359,10 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
   mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float ref = mx == -INFINITY ? 0.f : mx;
   float s = 0.f;
-  for (int i = threadIdx.x; i < nblk; i += 256) s += p[i].y * expf(p[i].x - ref);
+#pragma unroll
+  for (int k = 0; k < kB; ++k)
+    if (threadIdx.x + k * 256 < nblk) s += b[k].y * expf(b[k].x - ref);
+  for (int i = threadIdx.x + kB * 256; i < nblk; i += 256) s += p[i].y * expf(p[i].x - ref);
   s = wave_sumf(s);
   if ((threadIdx.x & 63) == 0) red[4 + wave] = s;
   __syncthreads();
@@ -534,7 +574,6 @@ template <> struct Tiles<kLarge> {
 };
 
 constexpr int kCUs = 256;
-constexpr int kDirectRows = 64;                           // tokens of the forward without a gather
 constexpr int kCountT = 2048;                             // tokens up to which k_xent_stage counts
 constexpr size_t kPieceBytes = (size_t)1 << 30;
 
@@ -576,7 +615,7 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
   p.lde = ceil_div(V, 256) * 256;
   p.direct = bf16 && !grad && T <= kDirectRows;
   int64_t best = 0;
-  for (int c = p.direct ? kSmall : kLarge; c >= kSmall; --c) {
+  for (int c = kLarge; c >= kSmall; --c) {
     const int b = 64 << c;
     const int64_t n = cost_of(kCostZ[c], ceil_div(V, b) * ceil_div(T, b), ceil_div(d, 64) * np);
     if (!best || cheaper(n, best)) {
@@ -672,12 +711,15 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   if constexpr (NP == 1) {
     // rows are addressed with 32-bit byte offsets
     if (p.direct && (a.T == 1 || a.ldx <= (1 << 20))) {
-      typedef Tiles<kSmall>::Z Z;
-      const int mt = (int)ceil_div(a.V, Z::BM);
-      k_xent_logits<Z, 1, ET, false, true><<<grid8(mt), Z::NT, 0, s>>>(w, 0, (const bf16_t *)a.x, a.ldx, 0, a.y, nullptr,
-                                                                       nullptr, 0, a.T, a.V, a.d, mt, 1, nullptr, 0, part,
-                                                                       p.nblk, zt);
-      TW_TRY_HIP(hipGetLastError());
+      auto logits = [&](auto C) {
+        typedef typename decltype(C)::Z Z;
+        const int mt = (int)ceil_div(a.V, Z::BM), nt = (int)ceil_div(a.T, Z::BN);
+        k_xent_logits<Z, 1, ET, false, true><<<grid8((int64_t)mt * nt), Z::NT, 0, s>>>(
+            w, 0, (const bf16_t *)a.x, a.ldx, 0, a.y, nullptr, nullptr, 0, a.T, a.V, a.d, mt, nt, nullptr, 0, part, p.nblk,
+            zt);
+        return hipGetLastError();
+      };
+      TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
       k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
                                                        nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse);
       return hipGetLastError();

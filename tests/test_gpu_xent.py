@@ -288,8 +288,8 @@ def test_tile_sizes(T, d, V, dtype):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T", [1, 2, 40, 64])
-@pytest.mark.parametrize("stride", [0, 264, (1 << 20) + 8])
+@pytest.mark.parametrize("T", [1, 2, 40, 64, 65, 300, 512, 513])
+@pytest.mark.parametrize("stride", [0, 264, 1 << 20, (1 << 20) + 8])
 def test_few_tokens_in_place(T, stride):
     """The forward of few bf16 tokens reads x's rows where they lie, however far apart, and skips those
     without a target (NaN in them reaches nothing)."""
