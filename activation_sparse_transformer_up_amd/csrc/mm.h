@@ -384,6 +384,99 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
   for (int i = 0; i < NM; ++i) mma(i, a1, b1);
 }
 
+// fp32 operands as they lie, on v_mfma_f32_16x16x4_f32 (157 TFLOP/s, below six bf16 products, but each
+// element is read once, as 4 bytes, where the planes take 10 to be made and 12 to be read): for few
+// rows and small products. A workgroup computes 64 x 64, a wave 32 x 32; a stage holds 32 k (16 KB),
+// four stages in a ring. The k of the four lane groups g of an instruction may be any four, the same
+// for both operands: instruction j of half h takes k = 16 h + 4 g + j, so that along k a lane reads its
+// four j in one load. In LDS, without bank conflicts:
+//   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
+//   across k:  k row j at 256 j, its 64-byte chunk c at c ^ ((j >> 2) & 3)
+template <bool ATR_, bool BTR_> struct MMF {
+  static constexpr int BM = 64, BN = 64, WM = 32, WN = 32, NS = 4;
+  static constexpr bool ATR = ATR_, BTR = BTR_;
+  static constexpr int NWM = 2, NWN = 2, NW = 4, NT = 256, FM = 2, FN = 2;
+  static constexpr int STAGE = 16384, SMEM = NS * STAGE;
+};
+struct MmfOperand {                                       // as MmOperand; n a multiple of 4 across k
+  const float *p;
+  int64_t ld;
+  int n;
+};
+
+// Fragment at row r0 of a staged operand, half h: element j of lane l is row r0 + l % 16, k = 16 h + 4 (l
+// / 16) + j.
+template <bool TR> TW_DEV f32x4_t mmf_frag(const char *st, int r0, int h, int lane) {
+  const int g = lane >> 4;
+  if constexpr (!TR) {
+    const int r = r0 + (lane & 15);
+    return *(const f32x4_t *)(st + r * 128 + (((4 * h + g) ^ ((r >> 1) & 7)) << 4));
+  } else {
+    const float *p = (const float *)(st + (16 * h + 4 * g) * 256 + (((r0 >> 4) ^ g) << 6)) + (lane & 15);
+    return f32x4_t{p[0], p[64], p[128], p[192]};
+  }
+}
+
+// acc += A B^T over k in [0, K), as mm_loop. A step waits for its stage, loads the one that is three
+// ahead into the place of the last step's, and multiplies.
+template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B, int K, f32x4_t (&acc)[2][2], char *smem) {
+  constexpr uint32_t OOB = 0x80000000u;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+  uint32_t voff[4];                                       // A's two 1 KB blocks of this wave, then B's
+  int kof[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const MmfOperand &o = i < 2 ? A : B;
+    const int blk = wave + 4 * (i & 1);
+    if (i < 2 ? G::ATR : G::BTR) {                        // 4 k rows
+      const int col = (((lane >> 2 & 3) ^ (blk & 3)) << 4) + (lane & 3) * 4;
+      kof[i] = blk * 4 + (lane >> 4);
+      voff[i] = col < o.n ? (uint32_t)(kof[i] * o.ld + col) * 4 : OOB;
+    } else {                                              // 8 rows
+      const int r = blk * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      kof[i] = c * 4;
+      voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 4) * 4 : OOB;
+    }
+  }
+  const int nk = (K + 31) / 32;
+  if (nk == 0) return;
+  auto issue = [&](int kt) {                              // zeros past the last stage
+    const int lk = kt * 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      char *at = smem + kt % G::NS * G::STAGE + (i < 2 ? 0 : G::STAGE / 2) + (wave + 4 * (i & 1)) * 1024;
+      const float *base = i < 2 ? A.p + (G::ATR ? lk * A.ld : lk) : B.p + (G::BTR ? lk * B.ld : lk);
+      const uint32_t vo = lk + kof[i] < K ? voff[i] : OOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)at, 16, vo, 0, 0, 0);
+    }
+  };
+  for (int st = 0; st < G::NS - 1; ++st) issue(st);
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_vmcnt<(G::NS - 2) * 4>();                        // stage kt has landed
+    block_barrier_lds();                                  // for all waves, which have read stage kt - 1
+    issue(kt + G::NS - 1);
+    const char *st = smem + kt % G::NS * G::STAGE;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4_t a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = mmf_frag<G::ATR>(st, wm * 32 + i * 16, h, lane);
+        b[i] = mmf_frag<G::BTR>(st + G::STAGE / 2, wn * 32 + i * 16, h, lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][j], b[n][j], acc[m][n], 0, 0, 0);
+    }
+  }
+  wait_vmcnt<0>();                                        // no load into LDS outlives the loop
+}
+
 // Workgroup b of `total` tiles -> tile. The XCDs take workgroups in turn (b % 8), each its own
 // L2: every XCD gets a contiguous run of tiles, so that neighbours share operand rows there. A
 // launch has 8 ceil(total / 8) workgroups; those past the end get -1.

@@ -19,7 +19,9 @@
 // which saves a launch (one pass alone, T = 333, d = 2048, V = 50021: 85 -> 82 us).
 //
 // Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is; dw is summed
-// over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h).
+// over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h) where the products are
+// large, and multiplied as they are where they are small or few rows make them a stream of w; in the
+// kernels' NP, the products of planes, these are 6 and 0, and bf16 is 1.
 #include "launch.h"
 #include "mm.h"
 #include "row8.h"
@@ -81,10 +83,10 @@ TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
   store8(p + 2 * plane, r);
 }
 
-// Token blockIdx.x < T: with a target, its row of x into the gathered operand (fp32: three planes);
+// Token blockIdx.x < T: with a target, its row of x into the gathered operand (three planes or as it is);
 // without, zeros to its loss, lse and row of dx. pos == NULL: the token's place is counted here (and
 // list, tgt and n_act written), which for few tokens costs less than the launch of k_xent_rows.
-// fp32: the workgroups past T split w.
+// fp32 planes: the workgroups past T split w (wp == NULL: x is only gathered, as fp32).
 template <typename T, typename DXT>
 __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int64_t ldx, int tokens, int d, int V,
                                                     const int64_t *__restrict__ y, const int32_t *__restrict__ pos,
@@ -139,7 +141,8 @@ __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int
     if constexpr (std::is_same<T, float>::value) {
       float v[8];
       load8(x + t * ldx + i, v);
-      split8(v, xc + (size_t)p * d + i, plane);
+      if (wp) split8(v, xc + (size_t)p * d + i, plane);
+      else store8((float *)xc + (size_t)p * d + i, v);
     } else {
       *(uint4 *)(xc + (size_t)p * d + i) = *(const uint4 *)(x + t * ldx + i);
     }
@@ -232,10 +235,16 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
   for (int i = 0; i < G::FM; ++i)
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
-  const MmOperand A = {w + (size_t)m0 * d, d, wplane, min(V - m0, G::BM)};
-  const MmOperand B = {xc + (DIRECT ? 0 : (size_t)(row0 + n0) * d), ldx, xplane, min(rows - n0, G::BN),
-                       DIRECT ? rowl + n0 : nullptr};
-  mm_loop64<G, NP>(A, B, d, acc, smem);
+  if constexpr (NP == 0) {
+    const MmfOperand A = {(const float *)w + (size_t)m0 * d, d, min(V - m0, G::BM)};
+    const MmfOperand B = {(const float *)xc + (size_t)(row0 + n0) * d, ldx, min(rows - n0, G::BN)};
+    mmf_loop<G>(A, B, d, acc, smem);
+  } else {
+    const MmOperand A = {w + (size_t)m0 * d, d, wplane, min(V - m0, G::BM)};
+    const MmOperand B = {xc + (DIRECT ? 0 : (size_t)(row0 + n0) * d), ldx, xplane, min(rows - n0, G::BN),
+                         DIRECT ? rowl + n0 : nullptr};
+    mm_loop64<G, NP>(A, B, d, acc, smem);
+  }
 
   if constexpr (!DIRECT) targets();
   if (v0 + G::WM > V)                                     // the last block ends inside the vocabulary
@@ -403,7 +412,8 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = i + k < V ? v[k] : 0.f;
         if constexpr (std::is_same<ET, float>::value) {
-          split8(v, g + (size_t)r * lde + i, gplane);
+          if (g) split8(v, g + (size_t)r * lde + i, gplane);
+          else store8(e + (size_t)r * lde + i, v);
         } else {
           store8(e + (size_t)r * lde + i, v);
         }
@@ -426,6 +436,8 @@ template <typename T> struct GradPiece {
   bool add;                                               // dw: to the sums of earlier pieces
   float *sum;                                             // which are here
   T *dw;                                                  // NULL until the last piece
+  int Sw, rs;                                             // dw: splits of the tokens, rows in each
+  float *partw;                                           // dw's partial sums [Sw][V][d] (Sw > 1)
 };
 
 // dx: D[column of d][token] = w^T G^T over the vocabulary range of split b / tiles (w across k, G
@@ -444,9 +456,15 @@ template <class G, int NP, typename T> TW_DEV void dx_tile(const GradPiece<T> &a
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
   const int k0 = sp * a.ks, k1 = min(a.V, k0 + a.ks);
-  const MmOperand A = {a.w + (size_t)k0 * a.d + m0, a.d, a.wplane, min(a.d - m0, G::BM)};
-  const MmOperand B = {a.g + (size_t)n0 * a.lde + k0, a.lde, a.gplane, min(rows - n0, G::BN)};
-  if (k0 < k1) mm_loop<G, NP>(A, B, k1 - k0, acc, smem);
+  if constexpr (NP == 0) {
+    const MmfOperand A = {(const float *)a.w + (size_t)k0 * a.d + m0, a.d, min(a.d - m0, G::BM)};
+    const MmfOperand B = {(const float *)a.g + (size_t)n0 * a.lde + k0, a.lde, min(rows - n0, G::BN)};
+    if (k0 < k1) mmf_loop<G>(A, B, k1 - k0, acc, smem);
+  } else {
+    const MmOperand A = {a.w + (size_t)k0 * a.d + m0, a.d, a.wplane, min(a.d - m0, G::BM)};
+    const MmOperand B = {a.g + (size_t)n0 * a.lde + k0, a.lde, a.gplane, min(rows - n0, G::BN)};
+    if (k0 < k1) mm_loop<G, NP>(A, B, k1 - k0, acc, smem);
+  }
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / G::NWN, wn = wave % G::NWN;
@@ -483,23 +501,50 @@ template <int NT, typename T> TW_DEV void dx_sum(const GradPiece<T> &a, int b) {
   store8(a.dx + (size_t)a.list[a.row0 + r] * a.d + c, v);
 }
 
-// dw: D[column of d][vocabulary] = x^T G over the piece's tokens (both across k), workgroup b. sum: fp32
-// sums of the pieces so far (added where `add`, written where dw is NULL; may be dw itself).
+// dw's elements [at, at + 4) from a piece's sum u: with the sums of the pieces so far, to those sums or,
+// rounded, to dw.
+template <typename T> TW_DEV void dw_out(const GradPiece<T> &a, size_t at, f32x4_t u) {
+  if (a.add) u += *(const f32x4_t *)(a.sum + at);
+  if (!a.dw) *(f32x4_t *)(a.sum + at) = u;
+  else if constexpr (std::is_same<T, float>::value) *(f32x4_t *)(a.dw + at) = u;
+  else *(uint2 *)(a.dw + at) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+}
+
+// Adds dw's Sw partial sums, 4 elements per thread, workgroup b of NT threads.
+template <int NT, typename T> TW_DEV void dw_sum(const GradPiece<T> &a, int b) {
+  const size_t n = (size_t)a.V * a.d, i = ((size_t)b * NT + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4_t u = {};
+#pragma unroll 4
+  for (int s = 0; s < a.Sw; ++s) u += *(const f32x4_t *)(a.partw + s * n + i);
+  dw_out(a, i, u);
+}
+
+// dw: D[column of d][vocabulary] = x^T G over the tokens of split b / tiles of the piece (both across k),
+// workgroup b. A small dw of many tokens would occupy few CUs without the splits.
 template <class G, int NP, typename T> TW_DEV void dw_tile(const GradPiece<T> &a, int b, char *smem) {
-  const int mt = (a.d + G::BM - 1) / G::BM, nt = (a.V + G::BN - 1) / G::BN, t = mm_xcd_tile(b, mt * nt);
+  const int mt = (a.d + G::BM - 1) / G::BM, nt = (a.V + G::BN - 1) / G::BN, t = mm_xcd_tile(b, mt * nt * a.Sw);
   if (t < 0) return;
   int m, n;
-  mm_tile_mn<8>(t, mt, nt, m, n);
+  const int sp = t / (mt * nt);
+  mm_tile_mn<8>(t % (mt * nt), mt, nt, m, n);
   const int m0 = m * G::BM, n0 = n * G::BN, rows = piece_rows(a.n_act, a.row0, a.R);
+  const int r0 = sp * a.rs, K = max(min(rows - r0, a.rs), 0);
   f32x4_t acc[G::FM][G::FN];
 #pragma unroll
   for (int i = 0; i < G::FM; ++i)
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
-  const MmOperand A = {a.xc + (size_t)a.row0 * a.d + m0, a.d, a.xplane, min(a.d - m0, G::BM)};
-  // the padding of G's rows up to lde is zero
-  const MmOperand B = {a.g + n0, a.lde, a.gplane, (int)min(a.lde - n0, (int64_t)G::BN)};
-  mm_loop<G, NP>(A, B, rows, acc, smem);
+  const int cols = (int)min(a.lde - n0, (int64_t)G::BN);  // the padding of G's rows up to lde is zero
+  if constexpr (NP == 0) {
+    const MmfOperand A = {(const float *)a.xc + (size_t)(a.row0 + r0) * a.d + m0, a.d, min(a.d - m0, G::BM)};
+    const MmfOperand B = {(const float *)a.g + (size_t)r0 * a.lde + n0, a.lde, cols};
+    mmf_loop<G>(A, B, K, acc, smem);
+  } else {
+    const MmOperand A = {a.xc + (size_t)(a.row0 + r0) * a.d + m0, a.d, a.xplane, min(a.d - m0, G::BM)};
+    const MmOperand B = {a.g + (size_t)r0 * a.lde + n0, a.lde, a.gplane, cols};
+    mm_loop<G, NP>(A, B, K, acc, smem);
+  }
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / G::NWN, wn = wave % G::NWN;
@@ -512,11 +557,8 @@ template <class G, int NP, typename T> TW_DEV void dw_tile(const GradPiece<T> &a
       const int c = m0 + wm * G::WM + fm * 16 + (lane >> 4) * 4;
       if (c >= a.d) continue;
       const size_t at = (size_t)v * a.d + c;
-      f32x4_t u = acc[fm][fn];
-      if (a.add) u += *(const f32x4_t *)(a.sum + at);
-      if (!a.dw) *(f32x4_t *)(a.sum + at) = u;
-      else if constexpr (std::is_same<T, float>::value) *(f32x4_t *)(a.dw + at) = u;
-      else *(uint2 *)(a.dw + at) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+      if (a.Sw > 1) *(f32x4_t *)(a.partw + (size_t)sp * a.V * a.d + at) = acc[fm][fn];
+      else dw_out(a, at, acc[fm][fn]);
     }
   }
 }
@@ -534,7 +576,8 @@ template <class W, int NP, typename T> __global__ __launch_bounds__(W::NT) void 
 }
 
 // Both products in one launch (dw's workgroups from `tiles` on), where each alone is too small to
-// fill the GPU: T = 128, d = 256, V = 1009 in fp32 30 us one after the other, 18 together and 4 for the sum of dx.
+// fill the GPU: T = 128, d = 256, V = 1009 in fp32 planes 30 us one after the
+// other, 18 together and 4 for the sum of dx.
 template <class X, class W, int NP, typename T>
 __global__ __launch_bounds__(X::NT) void k_xent_dx_dw(GradPiece<T> a, int tiles) {
   static_assert(X::NT == W::NT, "threads");
@@ -543,7 +586,11 @@ __global__ __launch_bounds__(X::NT) void k_xent_dx_dw(GradPiece<T> a, int tiles)
   else dw_tile<W, NP>(a, blockIdx.x - tiles, smem);
 }
 
-template <typename T> __global__ __launch_bounds__(256) void k_xent_dx_sum(GradPiece<T> a) { dx_sum<256>(a, blockIdx.x); }
+// The partial sums of dx (the first nx workgroups) and of dw.
+template <typename T> __global__ __launch_bounds__(256) void k_xent_sums(GradPiece<T> a, int nx) {
+  if ((int)blockIdx.x < nx) dx_sum<256>(a, blockIdx.x);
+  else dw_sum<256>(a, blockIdx.x - nx);
+}
 
 __global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t n) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -573,6 +620,12 @@ template <> struct Tiles<kLarge> {
   typedef MM<256, 256, 64, 128, 4, true, true> W;
 };
 
+struct TilesF {                                           // fp32 as it is
+  typedef MMF<false, false> Z;
+  typedef MMF<true, false> X;
+  typedef MMF<true, true> W;
+};
+
 constexpr int kCUs = 256;
 constexpr int kCountT = 2048;                             // tokens up to which k_xent_stage counts
 constexpr size_t kPieceBytes = (size_t)1 << 30;
@@ -582,11 +635,15 @@ constexpr size_t kPieceBytes = (size_t)1 << 30;
 // with every class forced, T x d x V in bf16 (small / mid / large, us): logits 100 x 1024 x 8000: 11 / 15
 // / 32, 1000 x 4096 x 8000: 108 / 66 / 92, 4096 x 1024 x 16000: 293 / 153 / 140; dx 500 x 512 x 2000: 15 / 17
 // (small / large), 1000 x 4096 x 8000: 98 / 63; dw 128 x 256 x 1009 in fp32: 16 / 25, 4096 x 1024 x 16000:
-// 203 / 118. (Tiles of 256 x 128 for dx and dw were slower than either everywhere.)
+// 203 / 118. (Tiles of 256 x 128 for dx and dw were slower than either everywhere.) fp32 in planes /
+// as it is, a whole call with gradients: 128 x 256 x 1009 44 / 29, 64 x 1024 x 32000 303 / 184, 16 x 4096 x 8000
+// 299 / 182, 600 x 1024 x 5000 235 / 246, 2255 x 1648 x 6125 876 / 1298.
 struct Cost {
   int per_cu, stage, alone, start;                        // alone: a stage where no CU has two workgroups
 };
 constexpr Cost kCostZ[3] = {{2, 450, 450, 2500}, {2, 1000, 750, 4000}, {1, 1450, 1450, 9000}};      // 64-k stages
+constexpr int kSums = 3000;                                                       // the launch that adds partial sums
+constexpr Cost kCostF = {2, 1050, 550, 3000};                                    // fp32 as it is: 32-k stages
 constexpr Cost kCostG[3] = {{2, 750, 700, 4500}, {}, {1, 850, 850, 10000}};       // dx, dw: 32-k stages
 int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
   if (tiles <= kCUs) return stages * c.alone + c.start;
@@ -600,13 +657,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // log2 of the logits tile's columns per wave
 int block_log(int c) { return c == kSmall ? 4 : c == kMid ? 6 : 7; }
-static_assert(Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 128, "block_log");
+constexpr int kBlockLogF = 5;
+static_assert(TilesF::Z::WM == 32 && Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 128, "block_log");
 
 struct Plan {
-  int R, pieces, nblk, S, ks, zc, dc, wc;                 // zc, dc, wc: classes of logits, dx, dw
+  int R, pieces, nblk, S, ks, Sw, rs, zc, dc, wc;                 // zc, dc, wc: classes of logits, dx, dw
   int64_t lde;
-  bool direct, sums;
-  size_t list, tgt, pos, zt, xc, wp, part, e, g, dxp, sum, bytes;   // offsets of the workspace
+  bool direct, sums, plain;                               // plain: fp32 as it is
+  size_t list, tgt, pos, zt, xc, wp, part, e, g, dxp, dwp, sum, bytes;   // offsets of the workspace
 };
 
 Plan plan_of(int T, int d, int V, int bf16, bool grad) {
@@ -614,55 +672,80 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
   const int np = bf16 ? 1 : 6;
   p.lde = ceil_div(V, 256) * 256;
   p.direct = bf16 && !grad && T <= kDirectRows;
-  int64_t best = 0;
+  int64_t z = 0, dx = 0, dw = 0;                          // the products' costs
   for (int c = kLarge; c >= kSmall; --c) {
     const int b = 64 << c;
     const int64_t n = cost_of(kCostZ[c], ceil_div(V, b) * ceil_div(T, b), ceil_div(d, 64) * np);
-    if (!best || cheaper(n, best)) {
-      best = n;
+    if (!z || cheaper(n, z)) {
+      z = n;
       p.zc = c;
     }
   }
-  // blocks of all columns that the tiles cover (with e kept, its padding too)
-  p.nblk = (int)((grad ? p.lde : ceil_div(V, 64 << p.zc) * (64 << p.zc)) >> block_log(p.zc));
+  // dx in R rows by tiles of m columns of d and b tokens: the vocabulary split 1, 2, 4, .. 64 times; the
+  // partial sums cost their traffic (about 5 bytes per ps)
+  auto split_dx = [&](const Cost &c, int m, int b, int R, int products, int64_t &best, int cls) {
+    const int64_t tiles = ceil_div(d, m) * ceil_div(R, b);
+    for (int S0 = 1; S0 <= 64 && (S0 == 1 || tiles * S0 <= kCUs * c.per_cu); S0 *= 2) {
+      const int64_t ks = ceil_div(ceil_div(V, S0), 64) * 64, S = ceil_div(V, ks);
+      const int64_t n = cost_of(c, tiles * S, ks / 32 * products) + (S > 1 ? kSums + S * R * d * 8 / 5000 : 0);
+      if (!best || cheaper(n, best)) {
+        best = n;
+        p.dc = cls;
+        p.S = (int)S;
+        p.ks = (int)ks;
+      }
+    }
+  };
+  // dw over R tokens by tiles of m columns of d and b of the vocabulary: the tokens split likewise, in
+  // partial sums of at most 64 MB
+  auto split_dw = [&](const Cost &c, int m, int b, int R, int products, int64_t &best, int cls) {
+    const int64_t tiles = ceil_div(d, m) * ceil_div(V, b);
+    for (int S0 = 1; S0 <= 64 && (S0 == 1 || (tiles * S0 <= kCUs * c.per_cu && (int64_t)S0 * V * d <= 16 << 20)); S0 *= 2) {
+      const int64_t rs = ceil_div(ceil_div(R, S0), 32) * 32, S = ceil_div(R, rs);
+      const int64_t n = cost_of(c, tiles * S, rs / 32 * products) + (S > 1 ? kSums + S * V * d * 8 / 5000 : 0);
+      if (!best || cheaper(n, best)) {
+        best = n;
+        p.wc = cls;
+        p.Sw = (int)S;
+        p.rs = (int)rs;
+      }
+    }
+  };
   const size_t planes = bf16 ? 1 : 3;
   // rows of a piece: as many as kPieceBytes hold of what a row keeps between the launches. bf16
   // gradients of several pieces need dw's sums in fp32; where all rows at once take no more
   // memory than that, there is one piece.
-  const size_t row = (size_t)p.nblk * 8 + (grad ? (size_t)p.lde * (bf16 ? 2 : 10) : 0);
-  const size_t sums = grad && bf16 ? (size_t)V * d * 4 : 0;
-  const int64_t all = ceil_div(T, 64) * 64;
-  int64_t R = (int64_t)(kPieceBytes / row) / 256 * 256;
-  if (R < 256) R = 256;
-  if (R >= all || (size_t)all * row <= kPieceBytes + sums) R = all;
-  p.R = (int)R;
-  p.pieces = (T + p.R - 1) / p.R;
-  p.sums = sums && p.pieces > 1;
+  auto rows_of = [&](int blocks, size_t element) {
+    p.nblk = blocks;
+    const size_t row = (size_t)p.nblk * 8 + (grad ? (size_t)p.lde * element : 0);
+    const size_t sums = grad && bf16 ? (size_t)V * d * 4 : 0;
+    const int64_t all = ceil_div(T, 64) * 64;
+    int64_t R = (int64_t)(kPieceBytes / row) / 256 * 256;
+    if (R < 256) R = 256;
+    if (R >= all || (size_t)all * row <= kPieceBytes + sums) R = all;
+    p.R = (int)R;
+    p.pieces = (T + p.R - 1) / p.R;
+    p.sums = sums && p.pieces > 1;
+  };
+  // blocks of all columns that the tiles cover (with e kept, its padding too)
+  rows_of((int)((grad ? p.lde : ceil_div(V, 64 << p.zc) * (64 << p.zc)) >> block_log(p.zc)), bf16 ? 2 : 10);
   if (grad) {
-    // dx: the vocabulary split 1, 2, 4, .. 64 times; the partial sums cost their traffic (about 5
-    // bytes per ps)
-    best = 0;
-    for (int c = kLarge; c >= kSmall; c -= kLarge) {
-      const int64_t tiles = ceil_div(d, 256) * ceil_div(p.R, 64 << c);
-      for (int S0 = 1; S0 <= 64 && (S0 == 1 || tiles * S0 <= kCUs * kCostG[c].per_cu); S0 *= 2) {
-        const int64_t ks = ceil_div(ceil_div(V, S0), 64) * 64, S = ceil_div(V, ks);
-        const int64_t n = cost_of(kCostG[c], tiles * S, ks / 32 * np) + (S > 1 ? S * p.R * d * 8 / 5000 : 0);
-        if (!best || cheaper(n, best)) {
-          best = n;
-          p.dc = c;
-          p.S = (int)S;
-          p.ks = (int)ks;
-        }
-      }
+    for (int c = kLarge; c >= kSmall; c -= kLarge) split_dx(kCostG[c], 256, 64 << c, p.R, np, dx, c);
+    for (int c = kLarge; c >= kSmall; c -= kLarge) split_dw(kCostG[c], 256, 64 << c, p.R, np, dw, c);
+  }
+  if (!bf16) {
+    // the planes of w are written and read again; all costs are per piece
+    const int64_t split = (int64_t)V * d * 10 / 5000, by_planes = split + (z + dx + dw) * p.pieces;
+    Plan q = p;
+    rows_of((int)((grad ? p.lde : ceil_div(V, 64) * 64) >> kBlockLogF), 4);
+    int64_t fx = 0, fw = 0;
+    const int64_t fz = cost_of(kCostF, ceil_div(V, 64) * ceil_div(p.R < T ? p.R : T, 64), ceil_div(d, 32));
+    if (grad) {
+      split_dx(kCostF, 64, 64, p.R, 1, fx, kSmall);
+      split_dw(kCostF, 64, 64, p.R, 1, fw, kSmall);
     }
-    best = 0;
-    for (int c = kLarge; c >= kSmall; c -= kLarge) {
-      const int64_t n = cost_of(kCostG[c], ceil_div(d, 256) * ceil_div(V, 64 << c), ceil_div(p.R, 32) * np);
-      if (!best || cheaper(n, best)) {
-        best = n;
-        p.wc = c;
-      }
-    }
+    p.plain = (fz + fx + fw) * p.pieces < by_planes;
+    if (!p.plain) p = q;
   }
   size_t at = 256;                                        // n_act
   auto take = [&](size_t n) {
@@ -673,13 +756,14 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
   p.list = take((size_t)T * 4);
   p.tgt = take((size_t)T * 4);
   p.pos = p.zt = take((size_t)T * 4);                     // pos is done with before zt begins
-  p.xc = take((size_t)T * d * 2 * planes);
-  if (!bf16) p.wp = take((size_t)V * d * 2 * planes);
+  p.xc = take((size_t)T * d * (p.plain ? 4 : 2 * planes));
+  if (!bf16 && !p.plain) p.wp = take((size_t)V * d * 2 * planes);
   p.part = take((size_t)p.R * p.nblk * 8);
   if (grad) {
     p.e = take((size_t)p.R * p.lde * (bf16 ? 2 : 4));
-    if (!bf16) p.g = take((size_t)p.R * p.lde * 6);
+    if (!bf16 && !p.plain) p.g = take((size_t)p.R * p.lde * 6);
     if (p.S > 1) p.dxp = take((size_t)p.S * p.R * d * 4);
+    if (p.Sw > 1) p.dwp = take((size_t)p.Sw * V * d * 4);
     if (p.sums) p.sum = take((size_t)V * d * 4);
   }
   p.bytes = at;
@@ -703,11 +787,11 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
   bf16_t *xc = (bf16_t *)(ws + p.xc);
   float2 *part = (float2 *)(ws + p.part);
   ET *e = (ET *)(ws + p.e);
-  bf16_t *g = NP == 1 ? (bf16_t *)e : (bf16_t *)(ws + p.g);
+  bf16_t *g = NP <= 1 ? (bf16_t *)e : (bf16_t *)(ws + p.g), *wp = NP <= 1 ? nullptr : (bf16_t *)(ws + p.wp);
   const int64_t xplane = (int64_t)a.T * a.d, wplane = (int64_t)a.V * a.d, gplane = (int64_t)p.R * p.lde;
   const bool grad = a.dw != nullptr;
-  const int pw = block_log(p.zc);
-  const bf16_t *w = NP == 1 ? (const bf16_t *)a.w : (const bf16_t *)(ws + p.wp);
+  const int pw = NP == 0 ? kBlockLogF : block_log(p.zc);
+  const bf16_t *w = NP <= 1 ? (const bf16_t *)a.w : wp;
   if constexpr (NP == 1) {
     // rows are addressed with 32-bit byte offsets
     if (p.direct && (a.T == 1 || a.ldx <= (1 << 20))) {
@@ -729,11 +813,11 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     k_xent_rows<<<1, 1024, 0, s>>>(a.y, a.T, a.V, list, tgt, pos, n_act);
     TW_TRY_HIP(hipGetLastError());
   }
-  const int64_t split = NP == 1 ? 0 : ceil_div(wplane, 256 * 8);
+  const int64_t split = NP <= 1 ? 0 : ceil_div(wplane, 256 * 8);
   k_xent_stage<T, T><<<(unsigned)(a.T + split), 256, 0, s>>>((const T *)a.x, a.ldx, a.T, a.d, a.V, a.y,
                                                              a.T > kCountT ? pos : nullptr, list, tgt, n_act, xc, xplane,
                                                              a.loss, a.lse, (T *)a.dx, (const T *)a.w, (size_t)wplane,
-                                                             (bf16_t *)(ws + p.wp));
+                                                             wp);
   TW_TRY_HIP(hipGetLastError());
   for (int q = 0; q < p.pieces; ++q) {
     const int row0 = q * p.R, R = a.T - row0 < p.R ? a.T - row0 : p.R;
@@ -749,20 +833,21 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       else go(std::integral_constant<bool, false>());
       return hipGetLastError();
     };
-    TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
+    if constexpr (NP == 0) TW_TRY_HIP(logits(TilesF()));
+    else TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
     // a row's columns go to several workgroups where rows alone would leave CUs idle
     int split = 1;
     while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;
     auto join = [&](auto G) {
       k_xent_join<ET, decltype(G)::value, false><<<R * split, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
-                                                                           row0, R, a.V, a.dloss, e, p.lde, g, gplane, split,
+                                                                           row0, R, a.V, a.dloss, e, p.lde, NP > 1 ? g : nullptr, gplane, split,
                                                                            a.loss, a.lse);
     };
     if (grad) join(std::integral_constant<bool, true>());
     else join(std::integral_constant<bool, false>());
     TW_TRY_HIP(hipGetLastError());
     if (!grad) continue;
-    const bool last = q + 1 == p.pieces, f32 = NP > 1;
+    const bool last = q + 1 == p.pieces, f32 = NP != 1;
     GradPiece<T> gp;
     gp.w = w; gp.xc = xc; gp.g = g;
     gp.wplane = wplane; gp.xplane = xplane; gp.gplane = gplane; gp.lde = p.lde;
@@ -773,30 +858,39 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     gp.add = q > 0;
     gp.sum = f32 ? (float *)a.dw : (float *)(ws + p.sum);
     gp.dw = last || f32 ? (T *)a.dw : nullptr;
+    gp.Sw = p.Sw; gp.rs = p.rs; gp.partw = p.Sw > 1 ? (float *)(ws + p.dwp) : nullptr;
     auto dx_grid = [&](auto X) { return grid8(ceil_div(a.d, decltype(X)::BM) * ceil_div(R, decltype(X)::BN) * p.S); };
-    auto dw_grid = [&](auto W) { return grid8(ceil_div(a.d, decltype(W)::BM) * ceil_div(a.V, decltype(W)::BN)); };
+    auto dw_grid = [&](auto W) { return grid8(ceil_div(a.d, decltype(W)::BM) * ceil_div(a.V, decltype(W)::BN) * p.Sw); };
     auto sum_grid = [&](int nt) { return p.S > 1 ? (int)ceil_div((int64_t)R * a.d, nt * 8) : 0; };
-    if (p.dc == kSmall && p.wc == kSmall) {
-      typedef Tiles<kSmall>::X X;
-      typedef Tiles<kSmall>::W W;
+    auto sums = [&](int nx) {
+      const int nw = p.Sw > 1 ? (int)ceil_div(wplane, 256 * 4) : 0;
+      if (nx + nw) k_xent_sums<<<nx + nw, 256, 0, s>>>(gp, nx);
+      return hipGetLastError();
+    };
+    if (NP == 0 || (p.dc == kSmall && p.wc == kSmall)) {
+      typedef typename std::conditional<NP == 0, TilesF, Tiles<kSmall>>::type C;
+      typedef typename C::X X;
+      typedef typename C::W W;
       const int tiles = dx_grid(X());
       k_xent_dx_dw<X, W, NP><<<tiles + dw_grid(W()), X::NT, 0, s>>>(gp, tiles);
       TW_TRY_HIP(hipGetLastError());
-      if (p.S > 1) k_xent_dx_sum<<<sum_grid(256), 256, 0, s>>>(gp);
-      TW_TRY_HIP(hipGetLastError());
+      TW_TRY_HIP(sums(sum_grid(256)));
       continue;
     }
-    TW_TRY_HIP(with_tiles(p.dc, [&](auto C) {
-      typedef typename decltype(C)::X X;
-      k_xent_dx<X, NP><<<dx_grid(X()), X::NT, 0, s>>>(gp);
-      return hipGetLastError();
-    }));
-    TW_TRY_HIP(with_tiles(p.wc, [&](auto C) {
-      typedef typename decltype(C)::W W;
-      const int tiles = dw_grid(W());
-      k_xent_dw<W, NP><<<tiles + sum_grid(W::NT), W::NT, 0, s>>>(gp, tiles);
-      return hipGetLastError();
-    }));
+    if constexpr (NP > 0) {
+      TW_TRY_HIP(with_tiles(p.dc, [&](auto C) {
+        typedef typename decltype(C)::X X;
+        k_xent_dx<X, NP><<<dx_grid(X()), X::NT, 0, s>>>(gp);
+        return hipGetLastError();
+      }));
+      TW_TRY_HIP(with_tiles(p.wc, [&](auto C) {
+        typedef typename decltype(C)::W W;
+        const int tiles = dw_grid(W());
+        k_xent_dw<W, NP><<<tiles + sum_grid(W::NT), W::NT, 0, s>>>(gp, tiles);
+        return hipGetLastError();
+      }));
+      TW_TRY_HIP(sums(0));
+    }
   }
   return hipSuccess;
 }
@@ -812,7 +906,8 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s) {
     return hipGetLastError();
   }
   const Plan p = plan_of(a.T, a.d, a.V, a.bf16, a.dw != nullptr);
-  return a.bf16 ? xent_run<bf16_t, bf16_t, 1>(a, p, s) : xent_run<float, float, 6>(a, p, s);
+  if (a.bf16) return xent_run<bf16_t, bf16_t, 1>(a, p, s);
+  return p.plain ? xent_run<float, float, 0>(a, p, s) : xent_run<float, float, 6>(a, p, s);
 }
 
 }  // namespace tw

@@ -487,8 +487,8 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
  *
  * linear_xent_fwd — loss and lse only (scoring). linear_xent_fwd_bwd — with both gradients.
  * bf16: G is held in bf16 (two roundings per element off the target, one on it), the sums are
- * fp32. fp32: operands and G are split into three bf16 parts, which carry all 24 bits. The same
- * bits on every call.
+ * fp32. fp32: large products split operands and G into three bf16 parts, which carry all 24 bits,
+ * small ones are fp32 matrix instructions. The same bits on every call.
  *
  * The workspace (linear_xent_workspace_bytes; contents need not be initialised) holds the
  * exponentials of one piece of tokens, about 1 GiB at most (bf16: up to 1 GiB + 4 V d bytes, the

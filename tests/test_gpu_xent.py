@@ -332,3 +332,17 @@ def test_more_pieces(T, dtype):
     """Two and more pieces of fp32 rows."""
     x, w, y, dl = problem(17, T, 64, 128000, dtype, ignored=T // 3)
     check(x, w, y, dl, tw.linear_xent_fwd_bwd(x, w, y, dl))
+
+
+@pytest.mark.parametrize("T,d,V,dtype", [(6000, 64, 500, BF16), (6000, 64, 500, F32), (3100, 200, 1009, BF16),
+                                         (3100, 200, 1009, F32), (1300, 1032, 2503, F32), (2100, 1544, 4099, F32)])
+def test_many_tokens_of_a_small_head(T, d, V, dtype):
+    """dw in splits of the tokens; fp32 as it is and in planes."""
+    say("xent small head", T, d, V, dtype)
+    x, w, y, dl = problem(T + V, T, d, V, dtype, ignored=T // 4)
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, w, y, dl, got)
+    for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
+        assert torch.equal(a, b)
+    fwd = tw.linear_xent_fwd(x, w, y)
+    check(x, w, y, dl, fwd)
