@@ -604,7 +604,7 @@ __global__ __launch_bounds__(256) void k_xent_zero(uint4 *__restrict__ p, size_t
 // traffic per operation. The smaller ones, two workgroups per CU, are for calls whose large tiles would leave CUs
 // idle or hold mostly rows that do not exist. The smallest logits tile's ring of four 64-k stages
 // keeps 24 KB of w per workgroup in flight, for few tokens, where the stream of w is all there is.
-enum { kSmall, kMid, kLarge };
+enum { kSmall, kMid, kLarge, kStream };
 template <int C> struct Tiles;
 template <> struct Tiles<kSmall> {
   typedef MM64<64, 64, 16, 64, 4, 4> Z;                   // logits
@@ -620,6 +620,12 @@ template <> struct Tiles<kLarge> {
   typedef MM<256, 256, 64, 128, 4, true, true> W;
 };
 
+// Logits of at most 32 bf16 tokens with more than one such tile per CU: T = 20, d = 2048, V = 128000 112 us
+// (128 x 128: 128), T = 1, d = 1024, V = 50000 26 (28). Up to one per CU, two 64 x 64 workgroups stream
+// better than one of these (T = 1, d = 4096, V = 32000: 55 us against 59).
+template <> struct Tiles<kStream> {
+  typedef MM64<128, 32, 32, 32, 4, 4> Z;
+};
 struct TilesF {                                           // fp32 as it is
   typedef MMF<false, false> Z;
   typedef MMF<true, false> X;
@@ -655,10 +661,13 @@ int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
 bool cheaper(int64_t n, int64_t best) { return n * 10 < best * 9; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// log2 of the logits tile's columns per wave
-int block_log(int c) { return c == kSmall ? 4 : c == kMid ? 6 : 7; }
+// The logits tile of class c: columns, and log2 of the columns per wave.
+int block_m(int c) { return c == kStream ? Tiles<kStream>::Z::BM : 64 << c; }
+int block_log(int c) { return c == kSmall ? 4 : c == kMid ? 6 : c == kStream ? 5 : 7; }
 constexpr int kBlockLogF = 5;
-static_assert(TilesF::Z::WM == 32 && Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 && Tiles<kLarge>::Z::WM == 128, "block_log");
+static_assert(TilesF::Z::WM == 32 && Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 &&
+                  Tiles<kLarge>::Z::WM == 128 && Tiles<kStream>::Z::WM == 32,
+              "block_log");
 
 struct Plan {
   int R, pieces, nblk, S, ks, Sw, rs, zc, dc, wc;                 // zc, dc, wc: classes of logits, dx, dw
@@ -681,6 +690,7 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
       p.zc = c;
     }
   }
+  if (bf16 && T <= 32 && ceil_div(V, block_m(kStream)) > kCUs) p.zc = kStream;
   // dx in R rows by tiles of m columns of d and b tokens: the vocabulary split 1, 2, 4, .. 64 times; the
   // partial sums cost their traffic (about 5 bytes per ps)
   auto split_dx = [&](const Cost &c, int m, int b, int R, int products, int64_t &best, int cls) {
@@ -728,23 +738,23 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
     p.sums = sums && p.pieces > 1;
   };
   // blocks of all columns that the tiles cover (with e kept, its padding too)
-  rows_of((int)((grad ? p.lde : ceil_div(V, 64 << p.zc) * (64 << p.zc)) >> block_log(p.zc)), bf16 ? 2 : 10);
+  rows_of((int)((grad ? p.lde : ceil_div(V, block_m(p.zc)) * block_m(p.zc)) >> block_log(p.zc)), bf16 ? 2 : 10);
   if (grad) {
     for (int c = kLarge; c >= kSmall; c -= kLarge) split_dx(kCostG[c], 256, 64 << c, p.R, np, dx, c);
     for (int c = kLarge; c >= kSmall; c -= kLarge) split_dw(kCostG[c], 256, 64 << c, p.R, np, dw, c);
   }
   if (!bf16) {
-    // the planes of w are written and read again; all costs are per piece
-    const int64_t split = (int64_t)V * d * 10 / 5000, by_planes = split + (z + dx + dw) * p.pieces;
+    // the planes of w are written and read again
+    const int64_t split = (int64_t)V * d * 10 / 5000, by_planes = split + z + (dx + dw) * p.pieces;
     Plan q = p;
     rows_of((int)((grad ? p.lde : ceil_div(V, 64) * 64) >> kBlockLogF), 4);
     int64_t fx = 0, fw = 0;
-    const int64_t fz = cost_of(kCostF, ceil_div(V, 64) * ceil_div(p.R < T ? p.R : T, 64), ceil_div(d, 32));
+    const int64_t fz = cost_of(kCostF, ceil_div(V, 64) * ceil_div(T, 64), ceil_div(d, 32));
     if (grad) {
       split_dx(kCostF, 64, 64, p.R, 1, fx, kSmall);
       split_dw(kCostF, 64, 64, p.R, 1, fw, kSmall);
     }
-    p.plain = (fz + fx + fw) * p.pieces < by_planes;
+    p.plain = fz + (fx + fw) * p.pieces < by_planes;
     if (!p.plain) p = q;
   }
   size_t at = 256;                                        // n_act
@@ -777,6 +787,11 @@ template <typename F> hipError_t with_tiles(int c, F &&f) {
   return c == kSmall ? f(Tiles<kSmall>()) : f(Tiles<kLarge>());
 }
 
+// and for the logits
+template <typename F> hipError_t with_logits(int c, F &&f) {
+  return c == kMid ? f(Tiles<kMid>()) : c == kStream ? f(Tiles<kStream>()) : with_tiles(c, f);
+}
+
 // T: type of the operands and results; ET: of e
 template <typename T, typename ET, int NP>
 hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
@@ -803,7 +818,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
             zt);
         return hipGetLastError();
       };
-      TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
+      TW_TRY_HIP(with_logits(p.zc, logits));
       k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
                                                        nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse);
       return hipGetLastError();
@@ -834,7 +849,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       return hipGetLastError();
     };
     if constexpr (NP == 0) TW_TRY_HIP(logits(TilesF()));
-    else TW_TRY_HIP(p.zc == kMid ? logits(Tiles<kMid>()) : with_tiles(p.zc, logits));
+    else TW_TRY_HIP(with_logits(p.zc, logits));
     // a row's columns go to several workgroups where rows alone would leave CUs idle
     int split = 1;
     while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;

@@ -346,3 +346,14 @@ def test_many_tokens_of_a_small_head(T, d, V, dtype):
         assert torch.equal(a, b)
     fwd = tw.linear_xent_fwd(x, w, y)
     check(x, w, y, dl, fwd)
+
+
+@pytest.mark.parametrize("T,d,V", [(1, 72, 40001), (20, 64, 33000), (32, 136, 36003), (33, 64, 36003)])
+def test_few_tokens_of_a_large_vocabulary(T, d, V):
+    say("xent few", T, d, V)
+    x, w, y, dl = problem(T + V, T, d, V, BF16, ignored=T // 5)
+    check(x, w, y, dl, tw.linear_xent_fwd(x, w, y))
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, w, y, dl, got)
+    for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
+        assert torch.equal(a, b)
