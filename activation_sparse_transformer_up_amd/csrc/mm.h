@@ -386,17 +386,20 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
 
 // fp32 operands as they lie, on v_mfma_f32_16x16x4_f32 (157 TFLOP/s, below six bf16 products, but each
 // element is read once, as 4 bytes, where the planes take 10 to be made and 12 to be read): for few
-// rows and small products. A workgroup computes 64 x 64, a wave 32 x 32; a stage holds 32 k (16 KB),
+// rows and small products. A workgroup of four waves computes BM x BN (64 where an operand lies across
+// k), a wave 32 x 32, of which 16-column parts of B that do not exist are left out; a stage holds 32 k,
 // four stages in a ring. The k of the four lane groups g of an instruction may be any four, the same
 // for both operands: instruction j of half h takes k = 16 h + 4 g + j, so that along k a lane reads its
 // four j in one load. In LDS, without bank conflicts:
 //   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
 //   across k:  k row j at 256 j, its 64-byte chunk c at c ^ ((j >> 2) & 3)
-template <bool ATR_, bool BTR_> struct MMF {
-  static constexpr int BM = 64, BN = 64, WM = 32, WN = 32, NS = 4;
+template <int BM_, int BN_, bool ATR_, bool BTR_> struct MMF {
+  static constexpr int BM = BM_, BN = BN_, WM = 32, WN = 32, NS = 4;
   static constexpr bool ATR = ATR_, BTR = BTR_;
-  static constexpr int NWM = 2, NWN = 2, NW = 4, NT = 256, FM = 2, FN = 2;
-  static constexpr int STAGE = 16384, SMEM = NS * STAGE;
+  static constexpr int NWM = BM / WM, NWN = BN / WN, NW = 4, NT = 256, FM = 2, FN = 2;
+  static constexpr int LA = BM / 32, LB = BN / 32, NL = LA + LB;      // 1 KB wave-loads per wave and stage
+  static constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128, SMEM = NS * STAGE;
+  static_assert(NWM * NWN == NW && (!ATR || BM == 64) && (!BTR || BN == 64), "tile");
 };
 struct MmfOperand {                                       // as MmOperand; n a multiple of 4 across k
   const float *p;
@@ -424,13 +427,14 @@ template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / G::NWN, wn = wave % G::NWN;
-  uint32_t voff[4];                                       // A's two 1 KB blocks of this wave, then B's
-  int kof[4];
+  const bool half = B.n - wn * 32 <= 16, none = B.n <= wn * 32;       // columns of this wave that exist
+  uint32_t voff[G::NL];                                   // A's 1 KB blocks of this wave, then B's
+  int kof[G::NL];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const MmfOperand &o = i < 2 ? A : B;
-    const int blk = wave + 4 * (i & 1);
-    if (i < 2 ? G::ATR : G::BTR) {                        // 4 k rows
+  for (int i = 0; i < G::NL; ++i) {
+    const MmfOperand &o = i < G::LA ? A : B;
+    const int blk = wave + 4 * (i < G::LA ? i : i - G::LA);
+    if (i < G::LA ? G::ATR : G::BTR) {                     // 4 k rows
       const int col = (((lane >> 2 & 3) ^ (blk & 3)) << 4) + (lane & 3) * 4;
       kof[i] = blk * 4 + (lane >> 4);
       voff[i] = col < o.n ? (uint32_t)(kof[i] * o.ld + col) * 4 : OOB;
@@ -445,33 +449,38 @@ template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B
   auto issue = [&](int kt) {                              // zeros past the last stage
     const int lk = kt * 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      char *at = smem + kt % G::NS * G::STAGE + (i < 2 ? 0 : G::STAGE / 2) + (wave + 4 * (i & 1)) * 1024;
-      const float *base = i < 2 ? A.p + (G::ATR ? lk * A.ld : lk) : B.p + (G::BTR ? lk * B.ld : lk);
+    for (int i = 0; i < G::NL; ++i) {
+      const bool isA = i < G::LA;
+      char *at = smem + kt % G::NS * G::STAGE + (isA ? 0 : G::A_BYTES) + (wave + 4 * (isA ? i : i - G::LA)) * 1024;
+      const float *base = isA ? A.p + (G::ATR ? lk * A.ld : lk) : B.p + (G::BTR ? lk * B.ld : lk);
       const uint32_t vo = lk + kof[i] < K ? voff[i] : OOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)at, 16, vo, 0, 0, 0);
     }
   };
   for (int st = 0; st < G::NS - 1; ++st) issue(st);
   for (int kt = 0; kt < nk; ++kt) {
-    wait_vmcnt<(G::NS - 2) * 4>();                        // stage kt has landed
+    wait_vmcnt<(G::NS - 2) * G::NL>();                    // stage kt has landed
     block_barrier_lds();                                  // for all waves, which have read stage kt - 1
     issue(kt + G::NS - 1);
     const char *st = smem + kt % G::NS * G::STAGE;
+    if (none) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f32x4_t a[2], b[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         a[i] = mmf_frag<G::ATR>(st, wm * 32 + i * 16, h, lane);
-        b[i] = mmf_frag<G::BTR>(st + G::STAGE / 2, wn * 32 + i * 16, h, lane);
+        b[i] = mmf_frag<G::BTR>(st + G::A_BYTES, wn * 32 + i * 16, h, lane);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int n = 0; n < 2; ++n) {
+        if (n == 1 && half) break;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][j], b[n][j], acc[m][n], 0, 0, 0);
+          for (int m = 0; m < 2; ++m)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][j], b[n][j], acc[m][n], 0, 0, 0);
+      }
     }
   }
   wait_vmcnt<0>();                                        // no load into LDS outlives the loop

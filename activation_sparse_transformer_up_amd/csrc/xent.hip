@@ -627,9 +627,16 @@ template <> struct Tiles<kStream> {
   typedef MM64<128, 32, 32, 32, 4, 4> Z;
 };
 struct TilesF {                                           // fp32 as it is
-  typedef MMF<false, false> Z;
-  typedef MMF<true, false> X;
-  typedef MMF<true, true> W;
+  typedef MMF<64, 64, false, false> Z;
+  // logits of at most 32 tokens: T = 1, d = 2136, V = 80008 145 us, with 64 x 64 228; T = 16, d = 4096, V = 8000
+  // 62 and 86
+  typedef MMF<128, 32, false, false> ZFew;
+  typedef MMF<64, 64, true, false> X;
+  typedef MMF<64, 64, true, true> W;
+};
+
+struct TilesFew {
+  typedef TilesF::ZFew Z;
 };
 
 constexpr int kCUs = 256;
@@ -665,7 +672,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int block_m(int c) { return c == kStream ? Tiles<kStream>::Z::BM : 64 << c; }
 int block_log(int c) { return c == kSmall ? 4 : c == kMid ? 6 : c == kStream ? 5 : 7; }
 constexpr int kBlockLogF = 5;
-static_assert(TilesF::Z::WM == 32 && Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 &&
+static_assert(TilesF::Z::WM == 32 && TilesF::ZFew::WM == 32 && Tiles<kSmall>::Z::WM == 16 && Tiles<kMid>::Z::WM == 64 &&
                   Tiles<kLarge>::Z::WM == 128 && Tiles<kStream>::Z::WM == 32,
               "block_log");
 
@@ -747,9 +754,11 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
     // the planes of w are written and read again
     const int64_t split = (int64_t)V * d * 10 / 5000, by_planes = split + z + (dx + dw) * p.pieces;
     Plan q = p;
-    rows_of((int)((grad ? p.lde : ceil_div(V, 64) * 64) >> kBlockLogF), 4);
+    p.zc = T <= 32 ? kStream : kSmall;
+    const int b = T <= 32 ? TilesF::ZFew::BM : TilesF::Z::BM;
+    rows_of((int)((grad ? p.lde : ceil_div(V, b) * b) >> kBlockLogF), 4);
     int64_t fx = 0, fw = 0;
-    const int64_t fz = cost_of(kCostF, ceil_div(V, 64) * ceil_div(T, 64), ceil_div(d, 32));
+    const int64_t fz = cost_of(kCostF, ceil_div(V, b) * ceil_div(T, 64), ceil_div(d, 32));
     if (grad) {
       split_dx(kCostF, 64, 64, p.R, 1, fx, kSmall);
       split_dw(kCostF, 64, 64, p.R, 1, fw, kSmall);
@@ -848,7 +857,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       else go(std::integral_constant<bool, false>());
       return hipGetLastError();
     };
-    if constexpr (NP == 0) TW_TRY_HIP(logits(TilesF()));
+    if constexpr (NP == 0) TW_TRY_HIP(p.zc == kStream ? logits(TilesFew()) : logits(TilesF()));
     else TW_TRY_HIP(with_logits(p.zc, logits));
     // a row's columns go to several workgroups where rows alone would leave CUs idle
     int split = 1;
