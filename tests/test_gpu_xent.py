@@ -357,3 +357,41 @@ def test_few_tokens_of_a_large_vocabulary(T, d, V):
     check(x, w, y, dl, got)
     for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
         assert torch.equal(a, b)
+
+
+def test_pieces_in_planes():
+    """Two pieces of rows (768 fp32 rows at this vocabulary) of products that run in bf16 planes."""
+    T, d, V = 1500, 520, 100003
+    say("xent planes, pieces", T, d, V)
+    x, w, y, dl = problem(23, T, d, V, F32, ignored=200)
+    check(x, w, y, dl, tw.linear_xent_fwd_bwd(x, w, y, dl))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pieces_of_split_tokens(dtype):
+    """More than a million tokens of a small head: dw in splits of the tokens and sums over pieces."""
+    T, d, V = 1150000, 16, 500
+    say("xent many tokens", T, d, V, dtype)
+    x, w, y, dl = problem(29, T, d, V, dtype, ignored=1000, lean=4.0)
+    dl = dl / T
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    rest = torch.randperm(T, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))[:4000]
+    act = rest[y[rest] >= 0]
+    xs, ws = x[act].double(), w.double()
+    z = xs @ ws.t()
+    lse = torch.logsumexp(z, 1)
+    assert ((got[1][act].double() - lse).abs() <= 1024 * E * (1 + z.abs().amax(1))).all()
+    # dw in 64 bits, in parts; its error: 2 H (bf16) or 1024 E of every term, and the output's rounding
+    ref = torch.zeros(V, d, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(ref)
+    for at in range(0, T, 100000):
+        yy = y[at:at + 100000]
+        a = yy >= 0
+        xx = x[at:at + 100000][a].double()
+        p = torch.softmax(xx @ ws.t(), 1)
+        p[torch.arange(len(p), device="cuda"), yy[a]] -= 1
+        G = p * dl[at:at + 100000][a].double()[:, None]
+        ref += G.t() @ xx
+        tol += G.abs().t() @ xx.abs()
+    tol = tol * ((2 * H if dtype == BF16 else 0) + 1024 * E) + (H if dtype == BF16 else E) * ref.abs()
+    assert ((got[3].double() - ref).abs() <= tol).all()
