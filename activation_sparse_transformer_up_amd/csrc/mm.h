@@ -296,7 +296,8 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
     const int o = isB ? 0 : 1, blk = wave + G::NW * (isB ? i : i - G::LB);
     char *at = smem + (isB ? G::NSA * G::A_STAGE + lp[0] * G::B_STAGE : lp[1] * G::A_STAGE) + blk * 1024;
     const uint32_t vo = lk[o] + kof[i] < K && (NP == 1 || lt[o] < NP) ? voff[i] : OOB;
-    const uint16_t *base = isB ? B.p + (NP > 1 ? mm_plane_b(lt[0]) * B.plane : 0) : A.p + (NP > 1 ? mm_plane_a(lt[1]) * A.plane : 0);
+    const int64_t pb = NP > 1 ? mm_plane_b(lt[0]) * B.plane : 0, pa = NP > 1 ? mm_plane_a(lt[1]) * A.plane : 0;
+    const uint16_t *base = isB ? B.p + pb : A.p + pa;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base + lk[o]), (lds_void_t *)at, 16, vo, 0, 0, 0);
     if (i != G::LB - 1 && i != NL - 1) return;            // the operand's last load of the stage
     lk[o] += 64;

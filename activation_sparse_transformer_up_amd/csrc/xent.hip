@@ -796,9 +796,11 @@ template <typename F> hipError_t with_tiles(int c, F &&f) {
   return c == kSmall ? f(Tiles<kSmall>()) : f(Tiles<kLarge>());
 }
 
-// and for the logits
-template <typename F> hipError_t with_logits(int c, F &&f) {
-  return c == kMid ? f(Tiles<kMid>()) : c == kStream ? f(Tiles<kStream>()) : with_tiles(c, f);
+// and for the logits (kStream: bf16 only)
+template <int NP, typename F> hipError_t with_logits(int c, F &&f) {
+  if constexpr (NP == 1)
+    if (c == kStream) return f(Tiles<kStream>());
+  return c == kMid ? f(Tiles<kMid>()) : with_tiles(c, f);
 }
 
 // T: type of the operands and results; ET: of e
@@ -827,7 +829,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
             zt);
         return hipGetLastError();
       };
-      TW_TRY_HIP(with_logits(p.zc, logits));
+      TW_TRY_HIP(with_logits<NP>(p.zc, logits));
       k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
                                                        nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse);
       return hipGetLastError();
@@ -858,14 +860,15 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       return hipGetLastError();
     };
     if constexpr (NP == 0) TW_TRY_HIP(p.zc == kStream ? logits(TilesFew()) : logits(TilesF()));
-    else TW_TRY_HIP(with_logits(p.zc, logits));
+    else TW_TRY_HIP(with_logits<NP>(p.zc, logits));
     // a row's columns go to several workgroups where rows alone would leave CUs idle
     int split = 1;
     while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;
     auto join = [&](auto G) {
       k_xent_join<ET, decltype(G)::value, false><<<R * split, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
-                                                                           row0, R, a.V, a.dloss, e, p.lde, NP > 1 ? g : nullptr, gplane, split,
-                                                                           a.loss, a.lse);
+                                                                           row0, R, a.V, a.dloss, e, p.lde,
+                                                                           NP > 1 ? g : nullptr, gplane, split, a.loss,
+                                                                           a.lse);
     };
     if (grad) join(std::integral_constant<bool, true>());
     else join(std::integral_constant<bool, false>());
