@@ -10,7 +10,7 @@
 // costs no more accuracy than rounding G itself for the next product (a bf16 e is off by 2^-9
 // of itself whatever the size of z, where a bf16 z would be off by 2^-9 |z|). Once a row's
 // blocks are joined, one pass turns e into G in place; the target's element is formed from the
-// fp32 logit instead, so that p - 1 of a token the model is sure of keeps its digits.
+// sum without the target instead, so that p - 1 of a token the model is sure of keeps its digits.
 //
 // Tokens without a target (negative) take no part: the rows with one are gathered first, in
 // order, and all products run over that list (its length stays on the device; workgroups beyond

@@ -492,7 +492,8 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
  *
  * The workspace (linear_xent_workspace_bytes; contents need not be initialised) holds the
  * exponentials of one piece of tokens, about 1 GiB at most (bf16: up to 1 GiB + 4 V d bytes, the
- * size of dw's fp32 sums that several pieces need), a copy of x's rows and, for fp32, the parts of w.
+ * size of dw's fp32 sums that several pieces need), a copy of x's rows, for fp32
+ * the parts of w, and up to 200 MB of partial sums.
  * T == 0 writes zeros to dw (linear_xent_fwd: nothing).
  * Errors: TWELL_ERR_ARG (null, dtype), TWELL_ERR_SHAPE (T < 0, d or V <= 0, ldx < d),
  * TWELL_ERR_ALIGN (d % 8, ldx % 8, pointers), TWELL_ERR_WORKSPACE, TWELL_ERR_UNSUPPORTED
