@@ -53,7 +53,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const T *__restrict__ x, int6
   __shared__ float red[32];
   int turn = 0;
   const int units = d / kU, nt = blockDim.x;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {        // beyond 2^31 in its last step
     float v[VPT][kU];
     float sum[1] = {0.f};
 #pragma unroll
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const T *__restrict__ x, int6
         load8(res + row * ldr + (size_t)u * kU, r);
 #pragma unroll
         for (int k = 0; k < kU; ++k) v[i][k] = rounded<T>(v[i][k] + r[k]);
-        store8(s + (size_t)row * d + (size_t)u * kU, v[i]);
+        store8(s + row * d + (size_t)u * kU, v[i]);
       }
 #pragma unroll
       for (int k = 0; k < kU; ++k) sum[0] += v[i][k];
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const T *__restrict__ x, int6
       if (b) load8(b + u * kU, bv);
 #pragma unroll
       for (int k = 0; k < kU; ++k) o[k] = v[i][k] * rs * wv[k] + (b ? bv[k] : 0.f);
-      store8(y + (size_t)row * d + (size_t)u * kU, o);
+      store8(y + row * d + (size_t)u * kU, o);
     }
   }
 }
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const DYT *__restrict__ dy, i
     if (kAhead && u < units) load8(w + u * kU, wv[i]);
   }
   typedef BwdRow<T, DYT, DXT, VPT> Row;
-  auto fetch = [&](int row, Row &r) {
+  auto fetch = [&](int64_t row, Row &r) {
     r.mu = mean[row];
     r.rs = rstd[row];
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const DYT *__restrict__ dy, i
     }
   };
   Row cur, next;
-  int row = blockIdx.x;
+  int64_t row = blockIdx.x;                               // beyond 2^31 in its last step
   if (kAhead && row < rows) fetch(row, cur);
   for (; row < rows; row += gridDim.x) {
     if (!kAhead) fetch(row, cur);
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const DYT *__restrict__ dy, i
 #pragma unroll
         for (int k = 0; k < kU; ++k) o[k] += r[k];
       }
-      store8(dx + (size_t)row * d + (size_t)u * kU, o);
+      store8(dx + row * d + (size_t)u * kU, o);
     }
     if (kAhead) cur = next;
   }
