@@ -671,7 +671,8 @@ def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor |
 def grad_clip(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
               workspace: torch.Tensor | None = None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), norm over all of them: in place,
-    or into ``out`` (tensors of the same shapes, fp32 or bf16). Returns (norm, out)."""
+    or into ``out`` (tensors of the same shapes, fp32 or bf16). Returns (norm, out). In place a tensor may
+    be listed once only, and outputs may not overlap (TwellError)."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     return _grad_call(grads, outs, max_norm, norm, workspace), outs

@@ -2,7 +2,9 @@
 // Declarations, layouts and error contract: include/twell.h.
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
+#include <new>
 
 #include "../../include/twell.h"
 #include "launch.h"
@@ -740,6 +742,36 @@ int linear_xent_fwd_bwd(const void *x, int64_t ldx, const void *w, const int64_t
 
 size_t grad_norm_workspace_bytes(int32_t n) { return n > 0 ? grad_workspace_bytes(n) : 0; }
 
+// Whether every output lies apart from all other outputs and from all gradients but its own, which it
+// may replace: the scaling's workgroups run in no order, so an element that two of them write, or one
+// writes and another reads, would come out scaled once or twice. n log n on the host (1000 tensors
+// in no order: 12 us; 41: 0.3).
+static int grad_outs_apart(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *dtypes,
+                           const int32_t *out_dtypes, int32_t n) {
+  struct Span {
+    uintptr_t at, end;
+  } few[64], *span = n <= 64 ? few : new (std::nothrow) Span[n];
+  if (!span) return TWELL_ERR_HIP;          // no host memory
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    const uintptr_t at = (uintptr_t)outs[i];
+    span[m++] = {at, at + (uintptr_t)sizes[i] * (out_dtypes[i] == TWELL_BF16 ? 2 : 4)};
+  }
+  std::sort(span, span + m, [](const Span &a, const Span &b) { return a.at < b.at; });
+  bool ok = true;
+  for (int k = 1; k < m; ++k) ok = ok && span[k - 1].end <= span[k].at;
+  // the outputs are apart, so of those that begin before a gradient's end the last reaches furthest
+  for (int i = 0; ok && i < n; ++i) {
+    if (sizes[i] == 0 || outs[i] == grads[i]) continue;
+    const uintptr_t at = (uintptr_t)grads[i], end = at + (uintptr_t)sizes[i] * (dtypes[i] == TWELL_BF16 ? 2 : 4);
+    const Span *s = std::lower_bound(span, span + m, end, [](const Span &a, uintptr_t e) { return a.at < e; });
+    ok = s == span || s[-1].end <= at;
+  }
+  if (span != few) delete[] span;
+  return ok ? TWELL_OK : TWELL_ERR_ARG;
+}
+
 // Shared checks of grad_norm and grad_clip (outs == NULL: the norm only).
 static int grad_run(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *dtypes,
                     const int32_t *out_dtypes, int32_t n, float max_norm, float *norm, void *workspace,
@@ -758,6 +790,10 @@ static int grad_run(const void *const *grads, void *const *outs, const int64_t *
     if (outs && (uintptr_t)outs[i] % (out_dtypes[i] == TWELL_BF16 ? 2 : 4)) return TWELL_ERR_ALIGN;
     // chunks of the whole set are counted in 32 bits
     if (sizes[i] > ((int64_t)1 << 40) || (total += sizes[i]) > ((int64_t)1 << 40)) return TWELL_ERR_UNSUPPORTED;
+  }
+  if (outs) {
+    const int st = grad_outs_apart(grads, outs, sizes, dtypes, out_dtypes, n);
+    if (st) return st;
   }
   if (n > 0 && (!workspace || workspace_bytes < grad_workspace_bytes(n))) return TWELL_ERR_WORKSPACE;
   if (n > 0 && !al16(workspace)) return TWELL_ERR_ALIGN;

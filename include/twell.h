@@ -519,9 +519,10 @@ int linear_xent_fwd_bwd(const void *x, int64_t ldx, const void *w, const int64_t
  * fixed order (the same bits on every call). Infinities and NaN reach the norm.
  * grad_clip — the same, then out_i = c g_i with c = min(1, max_norm / (norm + 1e-6)) in fp32,
  * rounded to out_dtype. outs[i] may be grads[i] (in place, same dtype; nothing is then written
- * where c is 1), or must not overlap any gradient. A NaN or infinite norm makes c NaN or 0, and
- * the outputs follow from the products. max_norm >= 0.
- * Errors: TWELL_ERR_ARG (null, dtype, max_norm negative or NaN), TWELL_ERR_SHAPE (negative n or
+ * where c is 1). Otherwise no output may overlap another or a gradient: a tensor that is clipped in
+ * place stands in the list once (tied weights share one gradient). A NaN or infinite norm makes c NaN
+ * or 0, and the outputs follow from the products. max_norm >= 0.
+ * Errors: TWELL_ERR_ARG (null, dtype, overlap, max_norm negative or NaN), TWELL_ERR_SHAPE (negative n or
  * size), TWELL_ERR_ALIGN, TWELL_ERR_WORKSPACE (grad_norm_workspace_bytes; contents need not be
  * initialised), TWELL_ERR_UNSUPPORTED (more than 2^40 elements in all).
  */
