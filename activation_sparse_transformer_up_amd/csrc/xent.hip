@@ -31,6 +31,7 @@ namespace {
 
 typedef uint16_t bf16_t;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kFarLogit = 1024.f;                       // up to it the exponent is off by 2^-14 at most
 
 // ------------------------------------------------------------------------------ rows, planes
 
@@ -276,7 +277,21 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
     mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
     const float ref = mx == -INFINITY ? 0.f : mx;         // a block past the vocabulary: e = 0
-    const float refl = ref * kLog2e;
+    float refl = ref * kLog2e;
+    if constexpr (NP == 1) {
+      // The fused product below rounds ref log2 e, which puts 2^-24 |ref| log2 e in the exponent: as much
+      // as the logits' own rounding near them, but a block that a mask of 1e30 or the type's lowest value
+      // fills would come to infinity. Rare: rows far from zero take their reference off first.
+      const bool far = fabsf(ref) > kFarLogit;
+      if (ballot64(far)) {
+        const float off = far ? ref : 0.f;
+#pragma unroll
+        for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[fm][fn][i] -= off;
+        refl = far ? 0.f : refl;
+      }
+    }
     auto ex = [&](float z) {
       if constexpr (NP == 1) return __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -refl));
       else return expf(z - ref);
