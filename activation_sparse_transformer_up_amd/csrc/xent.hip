@@ -66,12 +66,14 @@ __global__ __launch_bounds__(1024) void k_xent_rows(const int64_t *__restrict__ 
 }
 
 // Splits 8 fp32 values into three bf16 planes, hi + mid + lo = v (24 bits; rounded to nearest,
-// so mid and lo are at most 2^-9 and 2^-18 of v).
+// so mid and lo are at most 2^-8 and 2^-17 of v). The largest finite values would round to infinity
+// and leave inf - inf: their hi is cut off instead. An infinite v has NaN in mid and lo.
 TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
   float h[8], r[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     h[k] = rounded<bf16_t>(v[k]);
+    if (__builtin_isinf(h[k])) h[k] = __uint_as_float(__float_as_uint(v[k]) & 0xFFFF0000u);
     r[k] = v[k] - h[k];
   }
   store8(p, h);

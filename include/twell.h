@@ -484,6 +484,9 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
  * A negative target takes its token out: loss, lse and its row of dx are 0, and its x and dloss,
  * whatever they hold, reach nothing (the products run over the other tokens only). A target of V
  * or more gives a NaN loss and, with gradients, NaN in its row of dx and in dw.
+ * Vocabulary entries are masked by a large finite negative logit (their p is 0; any value down to the
+ * type's lowest). An infinity in w may make all losses NaN where the formula still has values: large
+ * fp32 products take it in parts.
  *
  * linear_xent_fwd — loss and lse only (scoring). linear_xent_fwd_bwd — with both gradients.
  * bf16: G is held in bf16 (two roundings per element off the target, one on it), the sums are

@@ -53,3 +53,19 @@ def test_masked_vocabulary_bf16(T, d, V, value):
     loss, lse, dx, dw = tw.linear_xent_fwd_bwd(x, w, y, dl)
     check(x, wk, yk, dl, (loss, lse, dx, dw[keep]))
     assert not dw[~keep].any()
+
+
+# fp32 as it is and in planes, with gradients and without
+F32_SHAPES = [(1, 64, 1000), (40, 128, 700), (1300, 1032, 2503), (2049, 328, 2500), (2100, 1544, 4099)]
+
+
+@pytest.mark.parametrize("value", [torch.finfo(F32).min, LOWEST, -2.0e38, -1e30, -1e4])
+@pytest.mark.parametrize("T,d,V", F32_SHAPES)
+def test_masked_vocabulary_f32(T, d, V, value):
+    say("xent mask f32", T, d, V, value)
+    x, w, y, dl, keep, yk = masked(T, d, V, F32, value)
+    wk = w[keep]
+    check(x, wk, yk, dl, tw.linear_xent_fwd(x, w, y))
+    loss, lse, dx, dw = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, wk, yk, dl, (loss, lse, dx, dw[keep]))
+    assert not dw[~keep].any()
