@@ -401,7 +401,8 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
     loss[t] = et > 0.5f ? log1pf(rest / et) : (ref - z) + ls;
   }
   if constexpr (GRAD) {
-    const float dl = bad ? NAN : dloss[t], at_target = -rest / all * dl;
+    // exp(z - lse) as exp(z - max) / sum: lse itself has lost the sum's digits in a row far from zero
+    const float dl = bad ? NAN : dloss[t], at_target = -rest / all * dl, scale = dl / all;
     constexpr int kAt = 4;                                // units in flight: loads before any store
     const int step = split * 256 * 8;
     for (int i0 = (part_of * 256 + threadIdx.x) * 8; i0 < lde; i0 += kAt * step) {
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
       for (int q = 0; q < kAt; ++q) {
         const int i = i0 + q * step;
         if (i >= lde) break;
-        f[q] = expf(f[q] - l) * dl;
+        f[q] = expf(f[q] - ref) * scale;
         float v[8];
         raw[q].to(v);
 #pragma unroll

@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import activation_sparse_transformer_up_amd as tw  # noqa: E402
-from test_gpu_xent import BF16, F32, check, problem  # noqa: E402
+from test_gpu_xent import BF16, E, F32, FLUSH, H, check, problem  # noqa: E402
 
 
 def say(*a):
@@ -69,3 +69,43 @@ def test_masked_vocabulary_f32(T, d, V, value):
     loss, lse, dx, dw = tw.linear_xent_fwd_bwd(x, w, y, dl)
     check(x, wk, yk, dl, (loss, lse, dx, dw[keep]))
     assert not dw[~keep].any()
+
+
+@pytest.mark.parametrize("offset", [2.0 ** 20, -2.0 ** 20, "lowest"])
+@pytest.mark.parametrize("T,d,V,dtype", [(40, 128, 700, BF16), (600, 1024, 5000, BF16), (2049, 328, 2500, BF16),
+                                         (40, 128, 700, F32), (1300, 1032, 2503, F32)])
+def test_rows_far_from_zero_keep_their_softmax(T, d, V, dtype, offset):
+    """All logits of a token carry one offset. Small integers make them exact in fp32 (below 2^24) at an
+    offset of 2^20, where lse has four bits behind the point left: softmax and loss have all theirs. An
+    offset of the type's lowest value swallows the rest: p = 1 / V. Tolerances: 256 E for exponentials,
+    the sum and the logarithm, 2 H per element of G in bf16 and 8 E in fp32, as without an offset."""
+    say("xent offset", T, d, V, dtype, offset)
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    kw = dict(generator=g, device="cuda")
+    offset = torch.finfo(dtype).min if offset == "lowest" else offset
+    x = torch.randint(-1, 2, (T, d), **kw).to(dtype)
+    w = (torch.randint(-1, 2, (V, d), **kw) * (torch.rand(V, d, **kw) < 32 / d)).to(dtype)
+    y = torch.randint(0, V, (T,), **kw)
+    dl = torch.rand(T, **kw) + 0.5
+    x[:, 0], w[:, 0] = 1, offset
+    z = x[:, 1:].double() @ w[:, 1:].double().t()
+    if abs(offset) > 2.0 ** 24:
+        z = torch.zeros_like(z)
+    logp = torch.log_softmax(z, 1)
+    zt = logp.gather(1, y[:, None])
+    loss, lse, dx, dw = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    assert ((loss.double() + zt[:, 0]).abs() <= 256 * E * (1 + zt[:, 0].abs())).all()
+    assert ((lse.double() - (offset + torch.logsumexp(z, 1))).abs() <= 2 * E * lse.double().abs()).all()
+    fwd = tw.linear_xent_fwd(x, w, y)
+    assert ((fwd[0].double() + zt[:, 0]).abs() <= 256 * E * (1 + zt[:, 0].abs())).all()
+    p, d64 = torch.exp(logp), dl.double()[:, None]
+    G = (p * d64).scatter_(1, y[:, None], torch.expm1(zt) * d64)
+    tg = G.abs() * (2 * H if dtype == BF16 else 8 * E) + p * d64 * 256 * E + FLUSH * (1 + d64)
+    out = H if dtype == BF16 else E
+    x64, w64 = x.double(), w.double()
+    ref = G.t() @ x64
+    tol = tg.t() @ x64.abs() + (T + 8) * E * (G.abs().t() @ x64.abs())
+    assert ((dw.double() - ref).abs() <= tol + out * (ref.abs() + tol) + FLUSH).all()
+    ref = G @ w64[:, 1:]                    # the offset's own column sums G to 0 times the offset
+    tol = tg @ w64[:, 1:].abs() + V * E * (G.abs() @ w64[:, 1:].abs())
+    assert ((dx[:, 1:].double() - ref).abs() <= tol + out * (ref.abs() + tol) + FLUSH).all()
