@@ -86,8 +86,8 @@ TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
   store8(p + 2 * plane, r);
 }
 
-// Token blockIdx.x < T: with a target, its row of x into the gathered operand (three planes or as it is);
-// without, zeros to its loss, lse and row of dx. pos == NULL: the token's place is counted here (and
+// Workgroup t = first + blockIdx.x, token t < T: with a target, its row of x into the gathered operand
+// (three planes or as it is); without, zeros to its loss, lse and row of dx. pos == NULL: the token's place is counted here (and
 // list, tgt and n_act written), which for few tokens costs less than the launch of k_xent_rows.
 // fp32 planes: the workgroups past T split w (wp == NULL: x is only gathered, as fp32).
 template <typename T, typename DXT>
@@ -97,10 +97,11 @@ __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int
                                                     int32_t *__restrict__ n_act, bf16_t *__restrict__ xc, int64_t plane,
                                                     float *__restrict__ loss, float *__restrict__ lse,
                                                     DXT *__restrict__ dx, const T *__restrict__ w, size_t wn,
-                                                    bf16_t *__restrict__ wp) {
+                                                    bf16_t *__restrict__ wp, int first) {
+  const int t = first + (int)blockIdx.x;
   if constexpr (std::is_same<T, float>::value) {
-    if ((int)blockIdx.x >= tokens) {
-      const size_t i = ((size_t)(blockIdx.x - tokens) * 256 + threadIdx.x) * 8;
+    if (t >= tokens) {
+      const size_t i = ((size_t)(t - tokens) * 256 + threadIdx.x) * 8;
       if (i >= wn) return;
       float v[8];
       load8(w + i, v);
@@ -108,7 +109,6 @@ __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int
       return;
     }
   }
-  const int t = blockIdx.x;
   int p;
   if (pos) {
     p = pos[t];
@@ -333,7 +333,8 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 // and E the target's: loss = log(1 + R / E) and p - 1 = -R / (R + E), which keep the digits of a token
 // that the model is sure of (R << E), where lse - z and exp(z - lse) - 1 have none left. A target
 // beyond the vocabulary makes loss and G NaN.
-// GRAD: `split` workgroups per row share its columns (each joins the blocks by itself).
+// Workgroup first + blockIdx.x: one per row; GRAD: `split` per row share its columns (each joins the
+// blocks by itself).
 // DIRECT: a workgroup per token of y instead, zeros for one without a target.
 template <typename ET, bool GRAD, bool DIRECT>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, int pw,
@@ -342,11 +343,12 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
                                                    const int32_t *__restrict__ n_act, int row0, int R, int V,
                                                    const float *__restrict__ dloss, ET *__restrict__ e, int64_t lde,
                                                    bf16_t *__restrict__ g, int64_t gplane, int split,
-                                                   float *__restrict__ loss, float *__restrict__ lse) {
+                                                   float *__restrict__ loss, float *__restrict__ lse, int first) {
   __shared__ float red[8];
   const int wave = threadIdx.x >> 6;
-  const int part_of = GRAD ? blockIdx.x % split : 0;
-  int r = GRAD ? blockIdx.x / split : blockIdx.x, t, tgt;
+  const uint32_t wg = first + blockIdx.x;
+  const int part_of = GRAD ? wg % split : 0;
+  int r = GRAD ? wg / split : wg, t, tgt;
   if constexpr (DIRECT) {
     t = r;
     const int64_t v = y[t];
@@ -807,6 +809,17 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
   return p;
 }
 
+// f(first, workgroups) over `total` workgroups of 256 threads, in as many launches as it takes: HIP
+// counts the threads of one in 32 bits, which 2^24 tokens reach.
+constexpr int64_t kLaunch = 1 << 23;
+template <typename F> hipError_t in_launches(int64_t total, F &&f) {
+  for (int64_t first = 0; first < total; first += kLaunch) {
+    f(first, (unsigned)(total - first < kLaunch ? total - first : kLaunch));
+    TW_TRY_HIP(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
 int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 
 // f(Tiles<c>()) for dx and dw
@@ -849,7 +862,7 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
       };
       TW_TRY_HIP(with_logits<NP>(p.zc, logits));
       k_xent_join<ET, false, true><<<a.T, 256, 0, s>>>(part, p.nblk, pw, zt, a.y, nullptr, nullptr, nullptr, 0, a.T, a.V,
-                                                       nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse);
+                                                       nullptr, nullptr, 0, nullptr, 0, 1, a.loss, a.lse, 0);
       return hipGetLastError();
     }
   }
@@ -858,11 +871,11 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     TW_TRY_HIP(hipGetLastError());
   }
   const int64_t split = NP <= 1 ? 0 : ceil_div(wplane, 256 * 8);
-  k_xent_stage<T, T><<<(unsigned)(a.T + split), 256, 0, s>>>((const T *)a.x, a.ldx, a.T, a.d, a.V, a.y,
-                                                             a.T > kCountT ? pos : nullptr, list, tgt, n_act, xc, xplane,
-                                                             a.loss, a.lse, (T *)a.dx, (const T *)a.w, (size_t)wplane,
-                                                             wp);
-  TW_TRY_HIP(hipGetLastError());
+  TW_TRY_HIP(in_launches(a.T + split, [&](int64_t first, unsigned n) {
+    k_xent_stage<T, T><<<n, 256, 0, s>>>((const T *)a.x, a.ldx, a.T, a.d, a.V, a.y, a.T > kCountT ? pos : nullptr, list,
+                                         tgt, n_act, xc, xplane, a.loss, a.lse, (T *)a.dx, (const T *)a.w,
+                                         (size_t)wplane, wp, (int)first);
+  }));
   for (int q = 0; q < p.pieces; ++q) {
     const int row0 = q * p.R, R = a.T - row0 < p.R ? a.T - row0 : p.R;
     auto logits = [&](auto C) {
@@ -883,14 +896,14 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     int split = 1;
     while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;
     auto join = [&](auto G) {
-      k_xent_join<ET, decltype(G)::value, false><<<R * split, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
-                                                                           row0, R, a.V, a.dloss, e, p.lde,
-                                                                           NP > 1 ? g : nullptr, gplane, split, a.loss,
-                                                                           a.lse);
+      return in_launches((int64_t)R * split, [&](int64_t first, unsigned n) {
+        k_xent_join<ET, decltype(G)::value, false><<<n, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
+                                                                     row0, R, a.V, a.dloss, e, p.lde,
+                                                                     NP > 1 ? g : nullptr, gplane, split, a.loss, a.lse,
+                                                                     (int)first);
+      });
     };
-    if (grad) join(std::integral_constant<bool, true>());
-    else join(std::integral_constant<bool, false>());
-    TW_TRY_HIP(hipGetLastError());
+    TW_TRY_HIP(grad ? join(std::integral_constant<bool, true>()) : join(std::integral_constant<bool, false>()));
     if (!grad) continue;
     const bool last = q + 1 == p.pieces, f32 = NP != 1;
     GradPiece<T> gp;
@@ -947,8 +960,9 @@ size_t xent_workspace_bytes(int T, int d, int V, int bf16, bool grad) { return p
 hipError_t launch_xent(const XentArgs &a, hipStream_t s) {
   if (a.T == 0) {                           // no tokens: dw is zero
     const size_t n16 = (size_t)a.V * a.d * (a.bf16 ? 2 : 4) / 16;
-    k_xent_zero<<<(unsigned)((n16 + 255) / 256), 256, 0, s>>>((uint4 *)a.dw, n16);
-    return hipGetLastError();
+    return in_launches((n16 + 255) / 256, [&](int64_t first, unsigned n) {
+      k_xent_zero<<<n, 256, 0, s>>>((uint4 *)a.dw + first * 256, n16 - first * 256);
+    });
   }
   const Plan p = plan_of(a.T, a.d, a.V, a.bf16, a.dw != nullptr);
   if (a.bf16) return xent_run<bf16_t, bf16_t, 1>(a, p, s);

@@ -1,0 +1,82 @@
+"""The cross entropy at the largest number of tokens that its header allows, where one workgroup per token
+is one thread more than a launch counts."""
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import activation_sparse_transformer_up_amd as tw  # noqa: E402
+from test_gpu_xent import BF16, E, F32, FLUSH, H  # noqa: E402
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1 << 24, (1 << 24) - 77, (1 << 23) + 1])
+def test_most_tokens(T, dtype):
+    """Positive x and targets that are mostly 0: no term of dw cancels, so that a piece, a split or a
+    launch left out shows. Logits of 8 products: 12 E of sum |x w| <= 8, and 256 E for the rest; a
+    split of at most 2^15 tokens adds dw with 2^15 E."""
+    say("xent most tokens", T, dtype)
+    d, V = 8, 7
+    g = torch.Generator(device="cuda").manual_seed(T)
+    kw = dict(generator=g, device="cuda")
+    x = (0.5 + torch.rand(T, d, **kw)).to(dtype)
+    w = (torch.rand(V, d, **kw) - 0.5).to(dtype)
+    y = torch.where(torch.rand(T, **kw) < 0.9, 0, torch.randint(0, V, (T,), **kw))
+    y[::5] = -1
+    y[T - 1], y[0] = 3, 2
+    dl = torch.rand(T, **kw) + 0.5
+    act = y >= 0
+    w64 = w.double()
+    dw_ref, dw_abs = torch.zeros(V, d, dtype=torch.float64, device="cuda"), 0
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    fwd = tw.linear_xent_fwd(x, w, y)
+    assert torch.equal(fwd[0], got[0]) and torch.equal(fwd[1], got[1])
+    out = H if dtype == BF16 else E
+    for at in range(0, T, 1 << 22):
+        p = slice(at, min(T, at + (1 << 22)))
+        a, x64 = act[p], x[p].double()
+        logp = torch.log_softmax(x64 @ w64.t(), 1)
+        lt = logp.gather(1, y[p].clamp(min=0)[:, None])
+        loss = torch.where(a, -lt[:, 0], 0.0)
+        assert ((got[0][p].double() - loss).abs() <= 512 * E * (1 + loss)).all()
+        G = logp.exp() * dl[p].double()[:, None]
+        G.scatter_(1, y[p].clamp(min=0)[:, None], torch.expm1(lt) * dl[p].double()[:, None])
+        G *= a[:, None]
+        tg = G.abs() * (2 * H if dtype == BF16 else 8 * E) + 512 * E * dl[p].double()[:, None] + FLUSH
+        dx = G @ w64
+        tol = tg @ w64.abs()
+        assert ((got[2][p].double() - dx).abs() <= tol + out * (dx.abs() + tol)).all()
+        assert not got[2][p][~a].any()
+        dw_ref += G.t() @ x64
+        dw_abs = dw_abs + tg.t() @ x64 + 2 ** 15 * E * (G.abs().t() @ x64)
+    assert ((got[3].double() - dw_ref).abs() <= dw_abs + out * (dw_ref.abs() + dw_abs)).all()
+    assert (dw_abs[0] < 0.02 * dw_ref[0].abs()).all()
+
+
+def test_dw_of_no_tokens_of_a_head_beyond_64_gib():
+    """T = 0 clears all of dw."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 200 << 30:
+        pytest.skip("needs 200 GiB of free GPU memory")
+    V, d = (1 << 20) + 3, 1 << 15
+    say("xent no tokens", V, d)
+    w = torch.empty(V, d, dtype=BF16, device="cuda")
+    old = torch.full((V, d), 1.0, dtype=BF16, device="cuda")
+    del old                                 # dw takes its place
+    x, y, dl = torch.empty(0, d, dtype=BF16).cuda(), torch.empty(0, dtype=torch.int64).cuda(), torch.empty(0).cuda()
+    dw = tw.linear_xent_fwd_bwd(x, w, y, dl)[3]
+    assert dw.shape == (V, d)
+    for at in range(0, V, 1 << 15):
+        assert not dw[at:at + (1 << 15)].any(), at
+    del w, dw
+    torch.cuda.empty_cache()
