@@ -139,6 +139,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _i32(*sizes):
+    """The sizes, checked: ctypes would cut them to the 32 bits that the library takes."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"a size of {n} does not fit 32 bits")
+    return sizes
+
+
 def _rows(t, d: int):
     """(pointer, row stride) of a [T][d] tensor whose rows are contiguous."""
     if t is None:
@@ -532,7 +540,7 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, y_dty
     (y, s, mean, rstd), mean and rstd fp32 [T] (None unless want_stats). weight and bias are
     fp32; y has x's dtype unless y_dtype is given; s is x itself where there is no residual. x and
     residual may have a row stride (a multiple of 8 elements)."""
-    T, d = x.shape
+    T, d = _i32(*x.shape)
     if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
         raise TypeError("residual must have x's dtype and shape")
     y = _rows_like(x, y_dtype)
@@ -547,7 +555,7 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, y_dty
 
 
 def layer_norm_bwd_workspace_bytes(T: int, d: int) -> int:
-    return lib().layer_norm_bwd_workspace_bytes(T, d)
+    return lib().layer_norm_bwd_workspace_bytes(*_i32(T, d))
 
 
 def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype | None = None,
@@ -555,7 +563,7 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype |
     """Gradients (dx, dweight, dbias) of layer_norm_fwd for dy [T][d] (fp32 or bf16, whatever s
     is); dres: the gradient that reaches s past the norm, in dx's dtype (default s's), added to
     dx. dweight and dbias are fp32; dbias is None unless want_bias."""
-    T, d = s.shape
+    T, d = _i32(*s.shape)
     dx = _rows_like(s, dx_dtype)
     if dy.shape != s.shape or (dres is not None and dres.shape != s.shape):
         raise ValueError("dy and dres must have s's shape")
@@ -576,12 +584,13 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dres=None, dx_dtype: torch.dtype |
 
 
 def linear_xent_workspace_bytes(T: int, d: int, V: int, dtype=torch.bfloat16, want_grad: bool = True) -> int:
-    return lib().linear_xent_workspace_bytes(T, d, V, _dt(dtype), int(want_grad))
+    return lib().linear_xent_workspace_bytes(*_i32(T, d, V), _dt(dtype), int(want_grad))
 
 
 def _xent_io(x, w, targets, workspace, want_grad):
     T, d = x.shape
     V = w.shape[0]
+    _i32(T, d, V)
     if w.dtype != x.dtype:
         raise TypeError("x and w must share a dtype")
     if w.dim() != 2 or w.shape[1] != d:
@@ -619,7 +628,7 @@ def linear_xent_fwd_bwd(x, w, targets, dloss, workspace: torch.Tensor | None = N
 
 
 def grad_norm_workspace_bytes(n: int) -> int:
-    return lib().grad_norm_workspace_bytes(n)
+    return lib().grad_norm_workspace_bytes(*_i32(n))
 
 
 def _addresses(tensors, dev):
