@@ -58,8 +58,9 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> str
 
 // p: element (first row of the tile, k = 0) for an operand along k, (k = 0, first column of the
 // tile) for one across k; ld: elements between rows; n: rows (columns) of the tile that exist (a
-// multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand; rows: where
-// the tile's rows are not consecutive, their numbers (n of them, in LDS; mm_loop64: may lie in smem).
+// multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand; rows (B of
+// mm_loop64 only): where the tile's rows are not consecutive, their numbers (n of them, in LDS, may
+// lie in smem).
 struct MmOperand {
   const uint16_t *p;
   int64_t ld, plane;
@@ -133,7 +134,7 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
       if constexpr (!decltype(tr)::value) {
         const int r = blk * 16 + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
         kof[i] = c * 8;
-        voff[i] = r < o.n ? (uint32_t)((o.rows ? o.rows[r] : r) * o.ld + c * 8) * 2 : OOB;
+        voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 8) * 2 : OOB;
       } else {
         constexpr int BX = decltype(bx)::value, LR = BX / 8;          // lanes per k row
         const int j = blk * MmTr<BX>::RPB + lane / LR;
