@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import activation_sparse_transformer_up_amd as tw  # noqa: E402
-from test_gpu_xent import BF16, E, F32, FLUSH, H  # noqa: E402
+from test_gpu_xent import BF16, E, F32, FLUSH, H, check, problem  # noqa: E402
 
 
 def say(*a):
@@ -80,3 +80,20 @@ def test_dw_of_no_tokens_of_a_head_beyond_64_gib():
         assert not dw[at:at + (1 << 15)].any(), at
     del w, dw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,d,V,ignored", [(1500, 768, 100003, 200), (1500, 1024, 100003, 600), (3000, 512, 100003, 7),
+                                           (2600, 1024, 60001, 0)])
+def test_pieces_in_planes(T, d, V, ignored):
+    """Several pieces of rows of fp32 products that run in bf16 planes (pieces of 1024, 1024, 1024 and 1536
+    rows); the last piece of the second case is empty. The workspace tells the path: as it is, fp32 takes
+    no more than a piece of 1 GiB, x's copy, the lists and 200 MB of partial sums."""
+    say("xent planes, pieces", T, d, V, ignored)
+    need = tw.linear_xent_workspace_bytes(T, d, V, F32)
+    assert need > (1 << 30) + T * d * 4 + 12 * T + 200_000_000, "not in planes"
+    assert T * V * 10 > 1 << 30, "one piece"
+    x, w, y, dl = problem(T + d, T, d, V, F32, ignored=ignored)
+    got = tw.linear_xent_fwd_bwd(x, w, y, dl)
+    check(x, w, y, dl, got)
+    for a, b in zip(got, tw.linear_xent_fwd_bwd(x, w, y, dl)):
+        assert torch.equal(a, b)
