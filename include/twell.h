@@ -493,10 +493,14 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
  * fp32. fp32: large products split operands and G into three bf16 parts, which carry all 24 bits,
  * small ones are fp32 matrix instructions. The same bits on every call.
  *
- * The workspace (linear_xent_workspace_bytes; contents need not be initialised) holds the
- * exponentials of one piece of tokens, about 1 GiB at most (bf16: up to 1 GiB + 4 V d bytes, the
- * size of dw's fp32 sums that several pieces need), a copy of x's rows, for fp32
- * the parts of w, and up to 200 MB of partial sums.
+ * The workspace (linear_xent_workspace_bytes; contents need not be initialised) holds
+ *   one piece of tokens: 1 GiB at most, or what 256 tokens take where that is more. A token takes 8
+ *     bytes per 16 to 128 columns and, for gradients, its exponentials: 2 bytes per column in bf16, 4
+ *     or 10 in fp32 (5.5 GB at V = 2^21). bf16 gradients add up to 4 V d bytes, the size of dw's fp32
+ *     sums that several pieces need: they take all tokens in one piece where its exponentials are no
+ *     more than that and 1 GiB;
+ *   a copy of x's rows (6 bytes per element of large fp32 products), for those the parts of w (6
+ *     bytes per element), up to 200 MB of partial sums, and lists of 12 bytes per token.
  * T == 0 writes zeros to dw (linear_xent_fwd: nothing).
  * Errors: TWELL_ERR_ARG (null, dtype), TWELL_ERR_SHAPE (T < 0, d or V <= 0, ldx < d),
  * TWELL_ERR_ALIGN (d % 8, ldx % 8, pointers), TWELL_ERR_WORKSPACE, TWELL_ERR_UNSUPPORTED
