@@ -475,8 +475,9 @@ int layer_norm_bwd(const void *dy, int64_t lddy, int32_t dy_dtype, const void *s
                    size_t workspace_bytes, void *stream);
 
 /*
- * Softmax cross entropy of a vocabulary of V, straight from hidden states and head weights; the
- * [T][V] logits are never written.
+ * Softmax cross entropy of a vocabulary of V, straight from hidden states and head weights. The fp32
+ * [T][V] logits are never written; for gradients, a piece of tokens' exponentials are, in the
+ * operands' type.
  *   z = x w^T (fp32 sums);  lse = log sum_j exp z_j;  loss = lse - z_target          [T] fp32
  *   G = (exp(z - lse) - onehot(target)) dloss;  dx = G w [T][d];  dw = G^T x [V][d]
  * x [T][d] (rows ldx elements apart, as for layer_norm_fwd) and w [V][d], dx and dw in dtype;
