@@ -462,7 +462,7 @@ int twell_choose_row_ell_width(const int32_t *hist, int32_t nbins, int32_t rows,
  * Errors of both: TWELL_ERR_ARG (null, dtype, eps), TWELL_ERR_SHAPE (T < 0, d <= 0, ld < d),
  * TWELL_ERR_ALIGN (d % 8, ld % 8, pointers), TWELL_ERR_WORKSPACE, TWELL_ERR_UNSUPPORTED
  * (d > 16384: a workgroup holds a whole row). Infinities and NaN stay in their own row of y and
- * dx; they reach all of dw and db.
+ * dx. One in s (or its statistics) reaches all of dw and nothing of db; one in dy its column of both.
  */
 int layer_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, const float *w,
                    const float *b, int32_t x_dtype, int32_t T, int32_t d, float eps, void *y,
