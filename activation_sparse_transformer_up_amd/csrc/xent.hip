@@ -333,8 +333,8 @@ __global__ __launch_bounds__(G::NT) void k_xent_logits(const bf16_t *__restrict_
 // and E the target's: loss = log(1 + R / E) and p - 1 = -R / (R + E), which keep the digits of a token
 // that the model is sure of (R << E), where lse - z and exp(z - lse) - 1 have none left. A target
 // beyond the vocabulary makes loss and G NaN.
-// Workgroup first + blockIdx.x: one per row; GRAD: `split` per row share its columns (each joins the
-// blocks by itself).
+// GRAD: `split` workgroups per row share its columns (each joins the blocks by itself); without, row
+// first + blockIdx.x.
 // DIRECT: a workgroup per token of y instead, zeros for one without a target.
 template <typename ET, bool GRAD, bool DIRECT>
 __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int nblk, int pw,
@@ -346,9 +346,8 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
                                                    float *__restrict__ loss, float *__restrict__ lse, int first) {
   __shared__ float red[8];
   const int wave = threadIdx.x >> 6;
-  const uint32_t wg = first + blockIdx.x;
-  const int part_of = GRAD ? wg % split : 0;
-  int r = GRAD ? wg / split : wg, t, tgt;
+  const int part_of = GRAD ? blockIdx.x % split : 0;
+  int r = GRAD ? blockIdx.x / split : first + blockIdx.x, t, tgt;
   if constexpr (DIRECT) {
     t = r;
     const int64_t v = y[t];
@@ -895,15 +894,17 @@ hipError_t xent_run(const XentArgs &a, const Plan &p, hipStream_t s) {
     // a row's columns go to several workgroups where rows alone would leave CUs idle
     int split = 1;
     while (grad && R * split < 4 * kCUs && split * 8192 < p.lde) split *= 2;
-    auto join = [&](auto G) {
-      return in_launches((int64_t)R * split, [&](int64_t first, unsigned n) {
-        k_xent_join<ET, decltype(G)::value, false><<<n, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act,
-                                                                     row0, R, a.V, a.dloss, e, p.lde,
-                                                                     NP > 1 ? g : nullptr, gplane, split, a.loss, a.lse,
-                                                                     (int)first);
-      });
+    auto join = [&](auto G, int64_t first, unsigned n) {
+      k_xent_join<ET, decltype(G)::value, false><<<n, 256, 0, s>>>(part, p.nblk, pw, zt, nullptr, tgt, list, n_act, row0,
+                                                                   R, a.V, a.dloss, e, p.lde, NP > 1 ? g : nullptr,
+                                                                   gplane, split, a.loss, a.lse, (int)first);
     };
-    TW_TRY_HIP(grad ? join(std::integral_constant<bool, true>()) : join(std::integral_constant<bool, false>()));
+    if (grad) {                             // R < 2^22: a row keeps 512 bytes or more
+      join(std::integral_constant<bool, true>(), 0, R * split);
+      TW_TRY_HIP(hipGetLastError());
+    } else {
+      TW_TRY_HIP(in_launches(R, [&](int64_t first, unsigned n) { join(std::integral_constant<bool, false>(), first, n); }));
+    }
     if (!grad) continue;
     const bool last = q + 1 == p.pieces, f32 = NP != 1;
     GradPiece<T> gp;
