@@ -6,11 +6,13 @@
 //
 // The three products (2 T V d operations each) bound it. The logits live in accumulators only:
 // the first product's epilogue reduces a tile's block of PW vocabulary columns to (max, sum of
-// exp) per token, and for a gradient leaves e = exp(z - block max) in the operand type, which
-// costs no more accuracy than rounding G itself for the next product (a bf16 e is off by 2^-9
-// of itself whatever the size of z, where a bf16 z would be off by 2^-9 |z|). Once a row's
-// blocks are joined, one pass turns e into G in place; the target's element is formed from the
-// sum without the target instead, so that p - 1 of a token the model is sure of keeps its digits.
+// exp) per token, and for a gradient leaves e = exp(z - block max) in the operand type. In bf16 that
+// and G, which the next products need in bf16, are two roundings of up to 2^-8 each, whatever the size
+// of z (a bf16 z would be off by 2^-8 |z|); dx and dw are then off by 1.4 times what rounding them to
+// bf16 leaves by itself (in the norm, 0.0024 against 0.0017). G in two bf16 parts would double those
+// products. fp32 operands keep 24 bits of both. Once a row's blocks are joined, one pass turns e into
+// G in place; the target's element is formed from the sum without the target instead, so that p - 1 of
+// a token the model is sure of keeps its digits.
 //
 // Tokens without a target (negative) take no part: the rows with one are gathered first, in
 // order, and all products run over that list (its length stays on the device; workgroups beyond
@@ -18,8 +20,9 @@
 // bf16 tokens makes the list in every workgroup instead and reads the rows of x where they lie,
 // which saves a launch (one pass alone, T = 333, d = 2048, V = 50021: 85 -> 82 us).
 //
-// Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is; dw is summed
-// over the pieces in fp32. fp32 operands are split into three bf16 planes (mm.h) where the products are
+// Tokens are taken in pieces of R rows, so that e needs R x V elements whatever T is (one piece as long
+// as that costs no more memory than dw's sums over pieces would, see rows_of); dw is summed over the
+// pieces in fp32. fp32 operands are split into three bf16 planes (mm.h) where the products are
 // large, and multiplied as they are where they are small or few rows make them a stream of w; in the
 // kernels' NP, the products of planes, these are 6 and 0, and bf16 is 1.
 #include "launch.h"
@@ -717,6 +720,8 @@ Plan plan_of(int T, int d, int V, int bf16, bool grad) {
     }
   }
   if (bf16 && T <= 32 && ceil_div(V, block_m(kStream)) > kCUs) p.zc = kStream;
+  // (both splits are chosen for all R rows; where most tokens have no target, dx's remaining tiles each walk
+  // a long range of the vocabulary on few CUs)
   // dx in R rows by tiles of m columns of d and b tokens: the vocabulary split 1, 2, 4, .. 64 times; the
   // partial sums cost their traffic (about 5 bytes per ps)
   auto split_dx = [&](const Cost &c, int m, int b, int R, int products, int64_t &best, int cls) {
