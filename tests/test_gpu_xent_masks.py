@@ -109,3 +109,27 @@ def test_rows_far_from_zero_keep_their_softmax(T, d, V, dtype, offset):
     ref = G @ w64[:, 1:]                    # the offset's own column sums G to 0 times the offset
     tol = tg @ w64[:, 1:].abs() + V * E * (G.abs() @ w64[:, 1:].abs())
     assert ((dx[:, 1:].double() - ref).abs() <= tol + out * (ref.abs() + tol) + FLUSH).all()
+
+
+@pytest.mark.parametrize("T,d,V,dtype", [(1, 64, 1000, BF16), (300, 200, 2049, BF16), (600, 1024, 5000, BF16),
+                                         (2049, 328, 2500, BF16), (20, 64, 33000, F32), (40, 128, 700, F32),
+                                         (1300, 1032, 2503, F32)])
+def test_infinite_mask(T, d, V, dtype):
+    """A bias of minus infinity masks as well, in scoring by bf16 products and by fp32 ones as they are. A
+    masked target's loss is infinite. The gradients of the other columns are those without the masked
+    entries; the bias column of dx is 0 times infinity."""
+    say("xent infinite mask", T, d, V, dtype)
+    x, w, y, dl, keep, yk = masked(T, d, V, dtype, -float("inf"))
+    check(x, w[keep], yk, dl, tw.linear_xent_fwd(x, w, y))
+    if dtype == BF16:
+        loss, lse, dx, dw = tw.linear_xent_fwd_bwd(x, w, y, dl)
+        act = y >= 0
+        assert torch.isnan(dx[act][:, 0].float()).all()
+        dx = dx.clone()
+        want = tw.linear_xent_fwd_bwd(x, w[keep].contiguous(), yk, dl)[2]
+        dx[:, 0] = want[:, 0]
+        check(x, w[keep], yk, dl, (loss, lse, dx, dw[keep]))
+        assert not dw[~keep].any()
+    y[T - 1] = int(torch.nonzero(~keep)[3])
+    loss, lse = tw.linear_xent_fwd(x, w, y)
+    assert loss[T - 1] == float("inf") and torch.isfinite(lse).all() and torch.isfinite(loss[:-1]).all()
