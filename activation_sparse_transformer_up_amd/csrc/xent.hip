@@ -90,9 +90,10 @@ TW_DEV void split8(const float (&v)[8], bf16_t *p, int64_t plane) {
 }
 
 // Workgroup t = first + blockIdx.x, token t < T: with a target, its row of x into the gathered operand
-// (three planes or as it is); without, zeros to its loss, lse and row of dx. pos == NULL: the token's place is counted here (and
-// list, tgt and n_act written), which for few tokens costs less than the launch of k_xent_rows.
-// fp32 planes: the workgroups past T split w (wp == NULL: x is only gathered, as fp32).
+// (three planes or as it is); without, zeros to its loss, lse and row of dx. pos == NULL: the token's
+// place is counted here (and list, tgt and n_act written), which for few tokens costs less than the
+// launch of k_xent_rows. fp32 planes: the workgroups past T split w (wp == NULL: x is only gathered, as
+// fp32).
 template <typename T, typename DXT>
 __global__ __launch_bounds__(256) void k_xent_stage(const T *__restrict__ x, int64_t ldx, int tokens, int d, int V,
                                                     const int64_t *__restrict__ y, const int32_t *__restrict__ pos,
