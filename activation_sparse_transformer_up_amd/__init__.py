@@ -23,7 +23,11 @@ __all__ = [
     "twell_stash_bytes", "twell_choose_slots", "twell_to_row_ell", "twell_row_nnz_histogram",
     "twell_choose_row_ell_width", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
     "linear_xent_fwd", "linear_xent_fwd_bwd", "linear_xent_workspace_bytes",
-    "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "F32", "BF16",
+    "grad_norm", "grad_clip", "grad_norm_workspace_bytes",
+    "linear_fwd", "linear_fwd_workspace_bytes", "linear_bwd", "linear_bwd_workspace_bytes",
+    "ffn_gated_dense_fwd", "ffn_gated_dense_fwd_workspace_bytes", "ffn_gated_dense_bwd",
+    "ffn_gated_dense_bwd_workspace_bytes", "adamw_step", "adamw8_states", "adamw8_values", "ADAMW_BLOCK",
+    "ACTS", "F32", "BF16",
 ]
 
 F32, BF16 = 0, 1
@@ -36,7 +40,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtwell.so
 
 _c = ctypes
 _P, _I, _F, _Z = _c.c_void_p, _c.c_int32, _c.c_float, _c.c_size_t
-_L = _c.c_int64
+_L, _D = _c.c_int64, _c.c_double
 
 
 class TwellError(RuntimeError):
@@ -91,6 +95,17 @@ _SIGS = {
     "grad_norm_workspace_bytes": ([_I], _Z),
     "grad_norm": ([_P, _P, _P, _I, _P, _P, _Z, _P], _I),
     "grad_clip": ([_P, _P, _P, _P, _P, _I, _F, _P, _P, _Z, _P], _I),
+    "linear_fwd_workspace_bytes": ([_I, _I, _I, _I, _I], _Z),
+    "linear_fwd": ([_P, _L, _P, _I, _P, _P, _L, _I, _I, _I, _I, _I, _P, _I, _P, _P, _Z, _P], _I),
+    "linear_bwd_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I, _I, _I], _Z),
+    "linear_bwd": ([_P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P], _I),
+    "ffn_gated_dense_fwd_workspace_bytes": ([_I, _I, _I, _I], _Z),
+    "ffn_gated_dense_fwd": ([_P, _L, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _Z, _P], _I),
+    "ffn_gated_dense_bwd_workspace_bytes": ([_I, _I, _I, _I, _I], _Z),
+    "ffn_gated_dense_bwd": ([_P, _L, _P, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P],
+                            _I),
+    "adamw_step": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _D, _P, _D, _D, _D, _L, _P, _P, _F, _P], _I),
+    "adamw8_values": ([_P, _P, _P, _P, _I, _P, _I, _P], _I),
 }
 
 _LIB = None
@@ -685,3 +700,280 @@ def grad_clip(grads, max_norm: float, out=None, norm: torch.Tensor | None = None
     grads = list(grads)
     outs = grads if out is None else list(out)
     return _grad_call(grads, outs, max_norm, norm, workspace), outs
+
+
+# activations of the dense layers (twell_act_t) and layouts of a linear layer's weights
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_LAYOUTS = {"nk": 0, "kn": 1}
+
+
+def _choice(value, table, name):
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, not {value!r}")
+    return code
+
+
+def _operand(t, name, dtype, shape, dev):
+    """Pointer of a contiguous operand, its dtype, shape and device checked (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}")
+    return _ptr(t)
+
+
+def _row_operand(t, name, dtype, T, d, dev):
+    """(pointer, row stride) of a [T][d] operand, checked likewise."""
+    if t is None:
+        return None, d
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 2 or t.shape[0] != T:
+        raise ValueError(f"{name}: expected {[T, d]}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}")
+    return _rows(t, d)
+
+
+def _enqueue(name, dev, *args):
+    """Calls the library on dev's current stream, with dev as the current device."""
+    if not dev.type == "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+        _check(getattr(lib(), name)(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(lib(), name)(*args, _stream(dev)), name)
+
+
+def _workspace(need, given, like):
+    """(tensor to keep alive, pointer, bytes): the given workspace, or a new one where one is needed."""
+    if given is None and need:
+        given = like.new_empty((need,), dtype=torch.uint8)
+    if given is None:
+        return None, None, 0
+    if given.device != like.device:
+        raise ValueError(f"workspace must live on {like.device}")
+    return given, _ptr(given), given.numel() * given.element_size()
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {list(t.shape)}")
+    return _i32(*t.shape)
+
+
+def _layer_shape(x, w, w_layout):
+    """(T, d_in, d_out, code of the layout) of a linear layer."""
+    T, K = _matrix(x, "x")
+    rows, cols = _matrix(w, "w")
+    code = _choice(w_layout, _LAYOUTS, "w_layout")
+    N, k = (rows, cols) if code == 0 else (cols, rows)
+    if k != K:
+        raise ValueError(f"w ({w_layout}): expected {K} inputs, got {list(w.shape)}")
+    return T, K, N, code
+
+
+def linear_fwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype=torch.bfloat16, w_layout: str = "nk") -> int:
+    return lib().linear_fwd_workspace_bytes(*_i32(T, d_in, d_out), _dt(dtype), _choice(w_layout, _LAYOUTS, "w_layout"))
+
+
+def linear_fwd(x, w, bias=None, residual=None, act: str = "none", w_layout: str = "nk", y_dtype: torch.dtype | None = None,
+               want_pre: bool = False, workspace: torch.Tensor | None = None):
+    """act(x w^T + bias) + residual for x [T][d_in] and w [d_out][d_in] (w_layout "nk"), or x w for w
+    [d_in][d_out] ("kn"): (y, pre). bias fp32 [d_out]; y and residual in y_dtype (default x's dtype);
+    pre, the activation's argument in x's dtype, is None unless want_pre. x and residual may have a row
+    stride (a multiple of 8 elements)."""
+    T, K, N, layout = _layer_shape(x, w, w_layout)
+    dev, dt = x.device, x.dtype
+    y = x.new_empty((T, N), dtype=y_dtype)
+    pre = x.new_empty((T, N)) if want_pre else None
+    (xp, ldx), (rp, ldr) = _row_operand(x, "x", dt, T, K, dev), _row_operand(residual, "residual", y.dtype, T, N, dev)
+    wp, bp = _operand(w, "w", dt, w.shape, dev), _operand(bias, "bias", torch.float32, (N,), dev)
+    code = _dt(dt)
+    keep, ws, nbytes = _workspace(lib().linear_fwd_workspace_bytes(T, K, N, code, layout), workspace, x)
+    _enqueue("linear_fwd", dev, xp, ldx, wp, layout, bp, rp, ldr, code, T, K, N, _choice(act, ACTS, "act"), y.data_ptr(),
+             _dt(y.dtype), pre.data_ptr() if want_pre else None, ws, nbytes)
+    return y, pre
+
+
+def linear_bwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype=torch.bfloat16, w_layout: str = "nk", act: str = "none",
+                               want_dx: bool = True, want_dw: bool = True, want_bias: bool = False) -> int:
+    return lib().linear_bwd_workspace_bytes(*_i32(T, d_in, d_out), _dt(dtype), _choice(w_layout, _LAYOUTS, "w_layout"),
+                                            _choice(act, ACTS, "act"), int(want_dx), int(want_dw), int(want_bias))
+
+
+def linear_bwd(dy, x, w, pre=None, act: str = "none", w_layout: str = "nk", want_dx: bool = True, want_dw: bool = True,
+               want_bias: bool = False, workspace: torch.Tensor | None = None):
+    """Gradients (dx, dw, dbias) of linear_fwd for dy [T][d_out] in x's dtype (the residual's gradient is dy
+    itself). pre: the forward's, needed with an activation. dx and dw have x's dtype, dbias fp32; those
+    not wanted are None. dy and x may have a row stride."""
+    T, K, N, layout = _layer_shape(x, w, w_layout)
+    dev, dt, code, acode = x.device, x.dtype, _dt(x.dtype), _choice(act, ACTS, "act")
+    (yp, lddy), (xp, ldx) = _row_operand(dy, "dy", dt, T, N, dev), _row_operand(x, "x", dt, T, K, dev)
+    wp, pp = _operand(w, "w", dt, w.shape, dev), _operand(pre, "pre", dt, (T, N), dev)
+    dx = x.new_empty((T, K)) if want_dx else None
+    dw = torch.empty_like(w) if want_dw else None
+    db = x.new_empty((N,), dtype=torch.float32) if want_bias else None
+    need = lib().linear_bwd_workspace_bytes(T, K, N, code, layout, acode, want_dx, want_dw, want_bias)
+    keep, ws, nbytes = _workspace(need, workspace, x)
+    _enqueue("linear_bwd", dev, yp, lddy, xp, ldx, wp, layout, pp, code, T, K, N, acode, dx.data_ptr() if want_dx else None,
+             dw.data_ptr() if want_dw else None, db.data_ptr() if want_bias else None, ws, nbytes)
+    return dx, dw, db
+
+
+def ffn_gated_dense_fwd_workspace_bytes(T: int, d: int, f: int, dtype=torch.bfloat16) -> int:
+    return lib().ffn_gated_dense_fwd_workspace_bytes(*_i32(T, d, f), _dt(dtype))
+
+
+def ffn_gated_dense_fwd(x, wgt, wut, w2, bg=None, bu=None, residual=None, act: str = "silu",
+                        y_dtype: torch.dtype | None = None, want_saved: bool = False,
+                        workspace: torch.Tensor | None = None):
+    """The dense gated block y = (act(x wgt^T + bg) * (x wut^T + bu)) w2 + residual: (y, g, u), g and u
+    the two products with their biases in x's dtype, which the backward needs (None unless want_saved).
+    x [T][d]; wgt, wut, w2 [f][d] in x's dtype; bg, bu fp32 [f]; y and residual in y_dtype (default x's). x
+    and residual may have a row stride."""
+    T, d = _matrix(x, "x")
+    f, _ = _matrix(wgt, "wgt")
+    dev, dt, code = x.device, x.dtype, _dt(x.dtype)
+    y = x.new_empty((T, d), dtype=y_dtype)
+    g, u = (x.new_empty((T, f)), x.new_empty((T, f))) if want_saved else (None, None)
+    (xp, ldx), (rp, ldr) = _row_operand(x, "x", dt, T, d, dev), _row_operand(residual, "residual", y.dtype, T, d, dev)
+    gp, up, dp = (_operand(t, n, dt, (f, d), dev) for t, n in ((wgt, "wgt"), (wut, "wut"), (w2, "w2")))
+    bgp, bup = _operand(bg, "bg", torch.float32, (f,), dev), _operand(bu, "bu", torch.float32, (f,), dev)
+    keep, ws, nbytes = _workspace(lib().ffn_gated_dense_fwd_workspace_bytes(T, d, f, code), workspace, x)
+    _enqueue("ffn_gated_dense_fwd", dev, xp, ldx, gp, up, dp, bgp, bup, rp, ldr, code, T, d, f, _choice(act, ACTS, "act"),
+             y.data_ptr(), _dt(y.dtype), g.data_ptr() if want_saved else None, u.data_ptr() if want_saved else None, ws, nbytes)
+    return y, g, u
+
+
+def ffn_gated_dense_bwd_workspace_bytes(T: int, d: int, f: int, dtype=torch.bfloat16, want_bias: bool = False) -> int:
+    return lib().ffn_gated_dense_bwd_workspace_bytes(*_i32(T, d, f), _dt(dtype), int(want_bias))
+
+
+def ffn_gated_dense_bwd(dy, x, wgt, wut, w2, g, u, act: str = "silu", want_bias: bool = False,
+                        workspace: torch.Tensor | None = None):
+    """Gradients (dx, dwgt, dwut, dw2, dbg, dbu) of ffn_gated_dense_fwd for dy [T][d] in x's dtype, from
+    the forward's g and u (the residual's gradient is dy itself). dbg and dbu are fp32, None unless
+    want_bias; the others have x's dtype. dy and x may have a row stride."""
+    T, d = _matrix(x, "x")
+    f, _ = _matrix(wgt, "wgt")
+    dev, dt, code = x.device, x.dtype, _dt(x.dtype)
+    (yp, lddy), (xp, ldx) = _row_operand(dy, "dy", dt, T, d, dev), _row_operand(x, "x", dt, T, d, dev)
+    gp, up, dp = (_operand(t, n, dt, (f, d), dev) for t, n in ((wgt, "wgt"), (wut, "wut"), (w2, "w2")))
+    gs, us = _operand(g, "g", dt, (T, f), dev), _operand(u, "u", dt, (T, f), dev)
+    dx, dwg, dwu, dw2 = x.new_empty((T, d)), torch.empty_like(wgt), torch.empty_like(wgt), torch.empty_like(wgt)
+    dbg, dbu = x.new_empty((2, f), dtype=torch.float32).unbind() if want_bias else (None, None)
+    keep, ws, nbytes = _workspace(lib().ffn_gated_dense_bwd_workspace_bytes(T, d, f, code, want_bias), workspace, x)
+    _enqueue("ffn_gated_dense_bwd", dev, yp, lddy, xp, ldx, gp, up, dp, gs, us, code, T, d, f, _choice(act, ACTS, "act"),
+             dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dw2.data_ptr(), dbg.data_ptr() if want_bias else None,
+             dbu.data_ptr() if want_bias else None, ws, nbytes)
+    return dx, dwg, dwu, dw2, dbg, dbu
+
+
+# elements that share a scale of the 8-bit AdamW states (TWELL_ADAMW_BLOCK)
+ADAMW_BLOCK = 256
+
+
+def adamw8_states(param):
+    """The initial 8-bit states of a parameter, all zero: (m int8, m_scales, v uint8, v_scales), the codes in
+    its shape, the scales fp32, one per ADAMW_BLOCK elements."""
+    blocks = (param.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+    return (torch.zeros(param.shape, dtype=torch.int8, device=param.device), param.new_zeros((blocks,), dtype=torch.float32),
+            torch.zeros(param.shape, dtype=torch.uint8, device=param.device), param.new_zeros((blocks,), dtype=torch.float32))
+
+
+def _pointers(tensors, dtypes, sizes, name, dev):
+    """Host array of a list's pointers; every tensor contiguous, on dev, of one of the dtypes and its size."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(tensors)}")
+    ptrs = array.array("Q")
+    for t, n in zip(tensors, sizes):
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} elements, got {list(t.shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name}: all tensors must live on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _scalar(value, dtype, name, dev):
+    """(host value, device pointer) of a number or a one-element GPU tensor."""
+    if not isinstance(value, torch.Tensor):
+        return value, None
+    if value.dtype != dtype or value.numel() != 1:
+        raise TypeError(f"{name} must be a number or one {dtype}")
+    if value.device != dev:
+        raise ValueError(f"{name} must live on {dev}")
+    return 0, value.data_ptr()
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, norm=None,
+               max_norm: float = 1.0, copies=None, m_scales=None, v_scales=None) -> None:
+    """One AdamW step over lists of tensors, in place. params and grads fp32 or bf16; the states m and v fp32,
+    or 8-bit codes (int8 and uint8) with m_scales and v_scales (see adamw8_states); copies: bf16 tensors
+    that take the new values of fp32 params. step counts this step, from 1; weight_decay is a number or one
+    per tensor; lr and step may be GPU scalars (fp32, int64), which a captured step reads on every replay.
+    norm: grad_norm's result over all gradients; they are then scaled by min(1, max_norm / (norm + 1e-6)), and a
+    norm that is not finite skips the step. A tensor may be listed once only (TwellError)."""
+    params, grads = list(params), list(grads)
+    n = len(params)
+    if n == 0:
+        if len(grads) or len(m) or len(v):
+            raise ValueError("grads, m and v must match params")
+        return
+    dev = params[0].device
+    sizes = array.array("q", [p.numel() for p in params])
+    eight = m_scales is not None or v_scales is not None
+    blocks = [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes] if eight else None
+    if eight and (m_scales is None or v_scales is None):
+        raise ValueError("8-bit states need m_scales and v_scales")
+    f32 = (torch.float32,)
+    lists = [_pointers(params, _FLOATS, sizes, "params", dev), _pointers(grads, _FLOATS, sizes, "grads", dev),
+             _pointers(m, (torch.int8,) if eight else f32, sizes, "m", dev),
+             _pointers(v, (torch.uint8,) if eight else f32, sizes, "v", dev),
+             _pointers(m_scales, f32, blocks, "m_scales", dev) if eight else None,
+             _pointers(v_scales, f32, blocks, "v_scales", dev) if eight else None,
+             _pointers(copies, (torch.bfloat16,), sizes, "copies", dev) if copies is not None else None,
+             sizes, array.array("i", [_dt(p.dtype) for p in params]), array.array("i", [_dt(g.dtype) for g in grads]),
+             array.array("d", weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n)]
+    if len(lists[-1]) != n:
+        raise ValueError("weight_decay: expected a number or one per tensor")
+    lr, lr_dev = _scalar(lr, torch.float32, "lr", dev)
+    step, step_dev = _scalar(step, torch.int64, "step", dev)
+    norm_dev = None
+    if norm is not None:
+        if not isinstance(norm, torch.Tensor):
+            raise TypeError("norm must be a GPU tensor")
+        norm_dev = _scalar(norm, torch.float32, "norm", dev)[1]
+    _enqueue("adamw_step", dev, *(None if a is None else a.buffer_info()[0] for a in lists), n, 8 if eight else 32, lr, lr_dev,
+             betas[0], betas[1], eps, step, step_dev, norm_dev, max_norm)
+
+
+def adamw8_values(codes, scales, dtype: torch.dtype = torch.float32) -> list:
+    """The values of 8-bit AdamW states, for lists of codes (int8: of m, uint8: of v) and their scales: new
+    tensors of the codes' shapes in dtype."""
+    n = len(codes)
+    if n == 0:
+        return []
+    dev = codes[0].device
+    sizes = array.array("q", [c.numel() for c in codes])
+    cp = _pointers(codes, (torch.int8, torch.uint8), sizes, "codes", dev)
+    sp = _pointers(scales, (torch.float32,), [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes], "scales", dev)
+    outs = [torch.empty_like(c, dtype=dtype) for c in codes]
+    op = array.array("Q", [o.data_ptr() for o in outs])
+    second = array.array("i", [c.dtype == torch.uint8 for c in codes])
+    _enqueue("adamw8_values", dev, *(a.buffer_info()[0] for a in (cp, sp, second, sizes)), n, op.buffer_info()[0], _dt(dtype))
+    return outs

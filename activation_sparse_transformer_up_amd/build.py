@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtwell.so")
 SOURCES = ["abi.hip", "gemm.hip", "pack.hip", "down.hip", "decode.hip", "bwd.hip", "nm.hip", "gated.hip", "rell.hip",
-           "norm.hip", "grad.hip", "xent.hip"]
+           "norm.hip", "grad.hip", "xent.hip", "dense.hip", "adamw.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

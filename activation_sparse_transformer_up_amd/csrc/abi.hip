@@ -815,6 +815,280 @@ int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
   return grad_run(grads, outs, sizes, dtypes, out_dtypes, n, max_norm, norm, workspace, workspace_bytes, S(stream));
 }
 
+// ------------------------------------------------------------------------------ dense layers
+
+static bool act_ok(int32_t act) { return act >= TWELL_ACT_NONE && act <= TWELL_ACT_GELU_TANH; }
+static bool layout_ok(int32_t l) { return l == TWELL_W_NK || l == TWELL_W_KN; }
+
+// rows of a tile are addressed with 32-bit byte offsets
+static constexpr int kDenseMaxT = 1 << 24, kDenseMaxD = 1 << 20, kDenseMaxLd = 1 << 21;
+
+static int dense_shape(int32_t T, int32_t a, int32_t b) {
+  if (T < 0 || a <= 0 || b <= 0) return TWELL_ERR_SHAPE;
+  if (a % 8 || b % 8) return TWELL_ERR_ALIGN;
+  if (T > kDenseMaxT || a > kDenseMaxD || b > kDenseMaxD) return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+// The stride of an operand's T rows of d (p NULL: not used).
+static int dense_ld(const void *p, int64_t ld, int32_t T, int32_t d) {
+  if (!p || T <= 1) return TWELL_OK;
+  if (ld < d) return TWELL_ERR_SHAPE;
+  if (ld % 8) return TWELL_ERR_ALIGN;
+  return ld > kDenseMaxLd ? TWELL_ERR_UNSUPPORTED : TWELL_OK;
+}
+
+static int dense_ws(const void *ws, size_t bytes, size_t need) {
+  if (need && (!ws || bytes < need)) return TWELL_ERR_WORKSPACE;
+  return need && !al16(ws) ? TWELL_ERR_ALIGN : TWELL_OK;
+}
+
+size_t linear_fwd_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype, int32_t w_layout) {
+  if (T <= 0 || !dtype_ok(dtype) || !layout_ok(w_layout) || dense_shape(T, d_in, d_out) != TWELL_OK) return 0;
+  return linear_fwd_workspace(T, d_in, d_out, dtype == TWELL_BF16, w_layout == TWELL_W_KN);
+}
+
+int linear_fwd(const void *x, int64_t ldx, const void *w, int32_t w_layout, const float *bias, const void *residual,
+               int64_t ldr, int32_t dtype, int32_t T, int32_t d_in, int32_t d_out, int32_t act, void *y, int32_t y_dtype,
+               void *pre, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!w || (T > 0 && (!x || !y))) return TWELL_ERR_ARG;
+  if (!dtype_ok(dtype) || !dtype_ok(y_dtype) || !act_ok(act) || !layout_ok(w_layout)) return TWELL_ERR_ARG;
+  int st = dense_shape(T, d_in, d_out);
+  if (st || (st = dense_ld(x, ldx, T, d_in)) || (st = dense_ld(residual, ldr, T, d_out))) return st;
+  if (!al16(x) || !al16(w) || !al16(bias) || !al16(residual) || !al16(y) || !al16(pre)) return TWELL_ERR_ALIGN;
+  if (T == 0) return TWELL_OK;
+  st = dense_ws(workspace, workspace_bytes, linear_fwd_workspace_bytes(T, d_in, d_out, dtype, w_layout));
+  if (st) return st;
+  LinearArgs a = {};
+  a.x = x; a.w = w; a.res = residual; a.bias = bias;
+  a.ldx = T > 1 ? ldx : d_in; a.ldr = T > 1 ? ldr : d_out;
+  a.T = T; a.K = d_in; a.N = d_out;
+  a.bf16 = dtype == TWELL_BF16; a.y_bf16 = y_dtype == TWELL_BF16; a.kn = w_layout == TWELL_W_KN; a.act = act;
+  a.y = y; a.pre = pre; a.ws = workspace;
+  TW_TRY(launch_linear_fwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+size_t linear_bwd_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype, int32_t w_layout, int32_t act,
+                                  int32_t want_dx, int32_t want_dw, int32_t want_db) {
+  if (T <= 0 || !dtype_ok(dtype) || !layout_ok(w_layout) || !act_ok(act) || dense_shape(T, d_in, d_out) != TWELL_OK) return 0;
+  return linear_bwd_workspace(T, d_in, d_out, dtype == TWELL_BF16, w_layout == TWELL_W_KN, act, want_dx != 0, want_dw != 0,
+                              want_db != 0);
+}
+
+int linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w, int32_t w_layout, const void *pre,
+               int32_t dtype, int32_t T, int32_t d_in, int32_t d_out, int32_t act, void *dx, void *dw, float *db,
+               void *workspace, size_t workspace_bytes, void *stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || !layout_ok(w_layout)) return TWELL_ERR_ARG;
+  if (T > 0 && (dx || dw || db) && (!dy || (act != TWELL_ACT_NONE && !pre))) return TWELL_ERR_ARG;
+  if (T > 0 && ((dx && !w) || (dw && !x))) return TWELL_ERR_ARG;
+  int st = dense_shape(T, d_in, d_out);
+  if (st || (st = dense_ld(dy, lddy, T, d_out)) || (st = dense_ld(dw ? x : nullptr, ldx, T, d_in))) return st;
+  if (!al16(dy) || !al16(x) || !al16(w) || !al16(pre) || !al16(dx) || !al16(dw) || !al16(db)) return TWELL_ERR_ALIGN;
+  if (!dx && !dw && !db) return TWELL_OK;
+  if (T > 0) {
+    st = dense_ws(workspace, workspace_bytes,
+                  linear_bwd_workspace_bytes(T, d_in, d_out, dtype, w_layout, act, dx != nullptr, dw != nullptr, db != nullptr));
+    if (st) return st;
+  }
+  LinearBackArgs a = {};
+  a.dy = dy; a.x = x; a.w = w; a.pre = pre;
+  a.lddy = T > 1 ? lddy : d_out; a.ldx = T > 1 ? ldx : d_in;
+  a.T = T; a.K = d_in; a.N = d_out;
+  a.bf16 = dtype == TWELL_BF16; a.kn = w_layout == TWELL_W_KN; a.act = act;
+  a.dx = dx; a.dw = dw; a.db = db; a.ws = workspace;
+  TW_TRY(launch_linear_bwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+size_t ffn_gated_dense_fwd_workspace_bytes(int32_t T, int32_t d_model, int32_t d_ff, int32_t dtype) {
+  if (T <= 0 || !dtype_ok(dtype) || dense_shape(T, d_model, d_ff) != TWELL_OK) return 0;
+  return gated_fwd_workspace(T, d_model, d_ff, dtype == TWELL_BF16);
+}
+
+int ffn_gated_dense_fwd(const void *x, int64_t ldx, const void *wg, const void *wu, const void *w2, const float *bg,
+                        const float *bu, const void *residual, int64_t ldr, int32_t dtype, int32_t T, int32_t d_model,
+                        int32_t d_ff, int32_t act, void *y, int32_t y_dtype, void *g, void *u, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+  if (!wg || !wu || !w2 || (T > 0 && (!x || !y)) || (g == nullptr) != (u == nullptr)) return TWELL_ERR_ARG;
+  if (!dtype_ok(dtype) || !dtype_ok(y_dtype) || !act_ok(act)) return TWELL_ERR_ARG;
+  int st = dense_shape(T, d_model, d_ff);
+  if (st || (st = dense_ld(x, ldx, T, d_model)) || (st = dense_ld(residual, ldr, T, d_model))) return st;
+  if (!al16(x) || !al16(wg) || !al16(wu) || !al16(w2) || !al16(bg) || !al16(bu) || !al16(residual) || !al16(y) || !al16(g) ||
+      !al16(u))
+    return TWELL_ERR_ALIGN;
+  if (T == 0) return TWELL_OK;
+  st = dense_ws(workspace, workspace_bytes, ffn_gated_dense_fwd_workspace_bytes(T, d_model, d_ff, dtype));
+  if (st) return st;
+  GatedArgs a = {};
+  a.x = x; a.wg = wg; a.wu = wu; a.w2 = w2; a.res = residual; a.bg = bg; a.bu = bu;
+  a.ldx = T > 1 ? ldx : d_model; a.ldr = T > 1 ? ldr : d_model;
+  a.T = T; a.d = d_model; a.f = d_ff;
+  a.bf16 = dtype == TWELL_BF16; a.y_bf16 = y_dtype == TWELL_BF16; a.act = act;
+  a.y = y; a.g = g; a.u = u; a.ws = workspace;
+  TW_TRY(launch_gated_fwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+size_t ffn_gated_dense_bwd_workspace_bytes(int32_t T, int32_t d_model, int32_t d_ff, int32_t dtype, int32_t want_bias) {
+  if (T <= 0 || !dtype_ok(dtype) || dense_shape(T, d_model, d_ff) != TWELL_OK) return 0;
+  return gated_bwd_workspace(T, d_model, d_ff, dtype == TWELL_BF16, want_bias != 0);
+}
+
+int ffn_gated_dense_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *wg, const void *wu,
+                        const void *w2, const void *g, const void *u, int32_t dtype, int32_t T, int32_t d_model,
+                        int32_t d_ff, int32_t act, void *dx, void *dwg, void *dwu, void *dw2, float *dbg, float *dbu,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+  if (!wg || !wu || !w2 || !dwg || !dwu || !dw2 || (T > 0 && (!dy || !x || !g || !u || !dx))) return TWELL_ERR_ARG;
+  if (!dtype_ok(dtype) || !act_ok(act)) return TWELL_ERR_ARG;
+  int st = dense_shape(T, d_model, d_ff);
+  if (st || (st = dense_ld(dy, lddy, T, d_model)) || (st = dense_ld(x, ldx, T, d_model))) return st;
+  if (!al16(dy) || !al16(x) || !al16(wg) || !al16(wu) || !al16(w2) || !al16(g) || !al16(u) || !al16(dx) || !al16(dwg) ||
+      !al16(dwu) || !al16(dw2) || !al16(dbg) || !al16(dbu))
+    return TWELL_ERR_ALIGN;
+  if (T > 0) {
+    st = dense_ws(workspace, workspace_bytes, ffn_gated_dense_bwd_workspace_bytes(T, d_model, d_ff, dtype, dbg || dbu));
+    if (st) return st;
+  }
+  GatedBackArgs a = {};
+  a.dy = dy; a.x = x; a.wg = wg; a.wu = wu; a.w2 = w2; a.g = g; a.u = u;
+  a.lddy = T > 1 ? lddy : d_model; a.ldx = T > 1 ? ldx : d_model;
+  a.T = T; a.d = d_model; a.f = d_ff; a.bf16 = dtype == TWELL_BF16; a.act = act;
+  a.dx = dx; a.dwg = dwg; a.dwu = dwu; a.dw2 = dw2; a.dbg = dbg; a.dbu = dbu; a.ws = workspace;
+  TW_TRY(launch_gated_bwd(a, S(stream)));
+  return TWELL_OK;
+}
+
+// ------------------------------------------------------------------------------------- AdamW
+
+namespace {
+struct Span {
+  uintptr_t at, end;
+};
+// Host memory for up to 256 spans without the heap, which a step of 40 tensors stays below.
+struct Spans {
+  Span few[256], *p = few;
+  int n = 0;
+  explicit Spans(size_t most) {
+    if (most > 256) p = new (std::nothrow) Span[most];
+  }
+  ~Spans() {
+    if (p != few) delete[] p;
+  }
+  void add(const void *q, int64_t bytes) {
+    if (q && bytes > 0) p[n++] = {(uintptr_t)q, (uintptr_t)q + (uintptr_t)bytes};
+  }
+  void sort() {
+    std::sort(p, p + n, [](const Span &a, const Span &b) { return a.at < b.at; });
+  }
+  bool apart() const {
+    for (int k = 1; k < n; ++k)
+      if (p[k - 1].end > p[k].at) return false;
+    return true;
+  }
+  // no span reaches into [q, q + bytes) (sorted and apart)
+  bool clear_of(const void *q, int64_t bytes) const {
+    if (!q || bytes <= 0) return true;
+    const uintptr_t at = (uintptr_t)q, end = at + (uintptr_t)bytes;
+    const Span *s = std::lower_bound(p, p + n, end, [](const Span &a, uintptr_t e) { return a.at < e; });
+    return s == p || s[-1].end <= at;
+  }
+};
+}  // namespace
+
+static int64_t bytes_of(int64_t n, int32_t dtype) { return n * (dtype == TWELL_BF16 ? 2 : 4); }
+static bool aligned(const void *p, int32_t dtype) { return (uintptr_t)p % (dtype == TWELL_BF16 ? 2 : 4) == 0; }
+static int64_t adamw_blocks(int64_t n) { return (n + TWELL_ADAMW_BLOCK - 1) / TWELL_ADAMW_BLOCK; }
+static_assert(TWELL_ADAMW_BLOCK == kAdamBlock, "block");
+
+int adamw_step(void *const *params, const void *const *grads, void *const *m, void *const *v, float *const *m_scales,
+               float *const *v_scales, void *const *copies, const int64_t *sizes, const int32_t *dtypes,
+               const int32_t *grad_dtypes, const double *weight_decay, int32_t n, int32_t state_bits, double lr,
+               const float *lr_dev, double beta1, double beta2, double eps, int64_t step, const int64_t *step_dev,
+               const float *norm, float max_norm, void *stream) {
+  if (n < 0) return TWELL_ERR_SHAPE;
+  if (state_bits != 8 && state_bits != 32) return TWELL_ERR_ARG;
+  const bool eight = state_bits == 8;
+  if (n > 0 && (!params || !grads || !m || !v || !sizes || !dtypes || !grad_dtypes || !weight_decay)) return TWELL_ERR_ARG;
+  if (n > 0 && eight && (!m_scales || !v_scales)) return TWELL_ERR_ARG;
+  if (!lr_dev && !(lr >= 0.0 && lr <= 1e30)) return TWELL_ERR_ARG;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return TWELL_ERR_ARG;
+  if (!(eps >= 1.17549435e-38 && eps <= 1e30)) return TWELL_ERR_ARG;        // not zero in fp32
+  if (!step_dev && step < 1) return TWELL_ERR_ARG;
+  if (norm && !(max_norm >= 0.f)) return TWELL_ERR_ARG;
+  if (!al4(lr_dev) || !al4(norm) || ((uintptr_t)step_dev & 7u)) return TWELL_ERR_ALIGN;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] < 0) return TWELL_ERR_SHAPE;
+    if (!dtype_ok(dtypes[i]) || !dtype_ok(grad_dtypes[i])) return TWELL_ERR_ARG;
+    if (!(weight_decay[i] >= 0.0 && weight_decay[i] <= 1e30)) return TWELL_ERR_ARG;
+    if (sizes[i] == 0) continue;
+    if (!params[i] || !grads[i] || !m[i] || !v[i] || (eight && (!m_scales[i] || !v_scales[i]))) return TWELL_ERR_ARG;
+    if (copies && copies[i] && dtypes[i] != TWELL_F32) return TWELL_ERR_ARG;
+    if (!aligned(params[i], dtypes[i]) || !aligned(grads[i], grad_dtypes[i])) return TWELL_ERR_ALIGN;
+    if (copies && !aligned(copies[i], TWELL_BF16)) return TWELL_ERR_ALIGN;
+    if (eight ? !al4(m_scales[i]) || !al4(v_scales[i]) : !al4(m[i]) || !al4(v[i])) return TWELL_ERR_ALIGN;
+    // chunks of the whole set are counted in 32 bits
+    if (sizes[i] > ((int64_t)1 << 40) || (total += sizes[i]) > ((int64_t)1 << 40)) return TWELL_ERR_UNSUPPORTED;
+  }
+  // workgroups run in no order: an element that two of them write, or one writes and another reads, would
+  // come out either way
+  Spans out((size_t)n * 6);
+  if (!out.p) return TWELL_ERR_HIP;         // no host memory
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    const int64_t state = eight ? sizes[i] : sizes[i] * 4, scales = adamw_blocks(sizes[i]) * 4;
+    out.add(params[i], bytes_of(sizes[i], dtypes[i]));
+    out.add(m[i], state);
+    out.add(v[i], state);
+    if (copies) out.add(copies[i], sizes[i] * 2);
+    if (eight) {
+      out.add(m_scales[i], scales);
+      out.add(v_scales[i], scales);
+    }
+  }
+  out.sort();
+  bool ok = out.apart() && out.clear_of(norm, 4) && out.clear_of(lr_dev, 4) && out.clear_of(step_dev, 8);
+  for (int i = 0; ok && i < n; ++i) ok = out.clear_of(grads[i], bytes_of(sizes[i], grad_dtypes[i]));
+  if (!ok) return TWELL_ERR_ARG;
+  AdamArgs a = {};
+  a.p = params; a.g = grads; a.m = m; a.v = v; a.copy = copies; a.ms = m_scales; a.vs = v_scales;
+  a.len = sizes; a.p_dtype = dtypes; a.g_dtype = grad_dtypes; a.decay = weight_decay;
+  a.n = n; a.eight = eight;
+  a.lr = lr; a.beta1 = beta1; a.beta2 = beta2; a.eps = eps; a.step = step;
+  a.lr_dev = lr_dev; a.step_dev = step_dev; a.norm = norm; a.max_norm = max_norm;
+  TW_TRY(launch_adamw(a, S(stream)));
+  return TWELL_OK;
+}
+
+int adamw8_values(const void *const *codes, const float *const *scales, const int32_t *second, const int64_t *sizes,
+                  int32_t n, void *const *outs, int32_t out_dtype, void *stream) {
+  if (n < 0) return TWELL_ERR_SHAPE;
+  if (!dtype_ok(out_dtype) || (n > 0 && (!codes || !scales || !second || !sizes || !outs))) return TWELL_ERR_ARG;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] < 0) return TWELL_ERR_SHAPE;
+    if (sizes[i] == 0) continue;
+    if (!codes[i] || !scales[i] || !outs[i]) return TWELL_ERR_ARG;
+    if (!al4(scales[i]) || !aligned(outs[i], out_dtype)) return TWELL_ERR_ALIGN;
+    if (sizes[i] > ((int64_t)1 << 40) || (total += sizes[i]) > ((int64_t)1 << 40)) return TWELL_ERR_UNSUPPORTED;
+  }
+  Spans out((size_t)n);
+  if (!out.p) return TWELL_ERR_HIP;
+  for (int i = 0; i < n; ++i)
+    if (sizes[i]) out.add(outs[i], bytes_of(sizes[i], out_dtype));
+  out.sort();
+  bool ok = out.apart();
+  for (int i = 0; ok && i < n; ++i)
+    ok = sizes[i] == 0 || (out.clear_of(codes[i], sizes[i]) && out.clear_of(scales[i], adamw_blocks(sizes[i]) * 4));
+  if (!ok) return TWELL_ERR_ARG;
+  AdamValuesArgs a = {};
+  a.codes = codes; a.scales = scales; a.second = second; a.len = sizes; a.n = n;
+  a.out = outs; a.out_bf16 = out_dtype == TWELL_BF16;
+  TW_TRY(launch_adamw8_values(a, S(stream)));
+  return TWELL_OK;
+}
+
 int twell_sync_status(const twell_matrix_t *h, void *stream) {
   if (!h || !h->ovf_n) return TWELL_ERR_ARG;
   if (hipStreamSynchronize(S(stream)) != hipSuccess) return TWELL_ERR_HIP;

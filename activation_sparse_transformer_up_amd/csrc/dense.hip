@@ -1,0 +1,743 @@
+// The dense layers on gfx950 matrix cores: a linear layer with bias, activation and residual in its
+// epilogue, the gated feed-forward block, and the backward passes of both.
+//
+//   linear   z = x w^T + b (or x w + b);  y = act(z) + residual
+//            dz = dy act'(z);  dx = dz w;  dw = dz^T x;  db = sum_t dz
+//   gated    g = x Wg^T + bg;  u = x Wu^T + bu;  h = act(g) u;  y = h W2 + residual
+//            dh = dy W2^T;  dg = dh u act'(g);  du = dh act(g)
+//            dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dW2 = h^T dy
+//
+// Every product is out[n][m] = sum_k A(m, k) B(n, k) with m along the output's rows, on the loops of
+// mm.h; three kinds occur: both operands along k (forward, dh), A across k (dx, products with a [k][m]
+// weight) and both across k (the weights' gradients). No transposed copy is made. A lane of the result
+// holds 4 neighbouring columns of a row, which the epilogue turns into outputs where they are:
+//   - the gated forward stages 16 rows of Wg and 16 of Wu in turn, so that a wave holds g and u of the
+//     same columns and h leaves the kernel instead of them (they are written too where a backward follows);
+//   - dh is never written: the epilogue reads g and u and leaves dg, du and h, the next products' operands;
+//   - column sums (db) are taken from the fp32 values, per wave and then over the waves in a fixed order.
+// h, dg, du (and dz where there is an activation) are rounded to the operands' type once, as operands of
+// the next product; sums, biases, activations and residuals are fp32.
+//
+// Products with fewer tiles than the CUs can hold split k; the fp32 partial sums are added in a fixed
+// order by k_dense_rows, which runs the same epilogue.
+#include "act.h"
+#include "launch.h"
+#include "mm.h"
+#include "row8.h"
+
+namespace tw {
+namespace {
+
+typedef uint16_t bf16_t;
+
+TW_DEV f32x4_t load4(const float *p) { return *(const f32x4_t *)p; }
+TW_DEV f32x4_t load4(const bf16_t *p) {
+  const uint2 u = *(const uint2 *)p;
+  return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xFFFF0000u)};
+}
+TW_DEV void store4(float *p, f32x4_t v) { *(f32x4_t *)p = v; }
+TW_DEV void store4(bf16_t *p, f32x4_t v) { *(uint2 *)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])); }
+
+// --------------------------------------------------------------------------------- epilogues
+// Of 4 columns c .. c + 3 of row r: col(c) is loaded once per column, row(r, c) ahead of put(), which
+// writes the outputs and adds to the NSUM column sums that the backward needs. ACTS: by activation.
+
+// y = act(v + bias) + residual; pre = v + bias. b: the batch's output.
+template <typename T, bool ACTS_> struct EpiLinear {
+  static constexpr bool DUAL = false, ACTS = ACTS_;
+  static constexpr int NSUM = 0;
+  const float *bias;
+  const void *res;
+  int64_t ldr, ldy;
+  void *y, *y1, *y2;                        // y1, y2: of the second and third batch
+  T *pre;
+  int act, y_bf16;
+  float *sums;
+  struct Col { f32x4_t bias; };
+  struct Row { f32x4_t res; };
+  TW_DEV Col col(int c) const { return {bias ? load4(bias + c) : f32x4_t{}}; }
+  TW_DEV Row row(int r, int c) const {
+    if (!res) return {f32x4_t{}};
+    return {y_bf16 ? load4((const bf16_t *)res + r * ldr + c) : load4((const float *)res + r * ldr + c)};
+  }
+  template <int ACT> TW_DEV void put(int b, int r, int c, const Col &k, const Row &q, f32x4_t v, f32x4_t, f32x4_t *) const {
+    const int64_t at = r * ldy + c;
+    if constexpr (ACTS) {
+      v += k.bias;
+      if (pre) store4(pre + at, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]);
+      v += q.res;
+    }
+    void *o = ACTS || b == 0 ? y : b == 1 ? y1 : y2;
+    if (y_bf16) store4((bf16_t *)o + at, v);
+    else store4((float *)o + at, v);
+  }
+};
+
+// h = act(v + bg) (w + bu), and both factors where a backward follows.
+template <typename T> struct EpiGlu {
+  static constexpr bool DUAL = true, ACTS = true;
+  static constexpr int NSUM = 0;
+  const float *bg, *bu;
+  T *h, *g, *u;
+  int64_t ldy;
+  int act;
+  float *sums;
+  struct Col { f32x4_t bg, bu; };
+  struct Row {};
+  TW_DEV Col col(int c) const { return {bg ? load4(bg + c) : f32x4_t{}, bu ? load4(bu + c) : f32x4_t{}}; }
+  TW_DEV Row row(int, int) const { return {}; }
+  template <int ACT> TW_DEV void put(int, int r, int c, const Col &k, const Row &, f32x4_t v, f32x4_t w, f32x4_t *) const {
+    const int64_t at = r * ldy + c;
+    v += k.bg;
+    w += k.bu;
+    if (g) {
+      store4(g + at, v);
+      store4(u + at, w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]) * w[i];
+    store4(h + at, v);
+  }
+};
+
+// dg = v u act'(g), du = v act(g), h = act(g) u for v = dh.
+template <typename T> struct EpiGluBack {
+  static constexpr bool DUAL = false, ACTS = true;
+  static constexpr int NSUM = 2;
+  const T *g, *u;
+  T *dg, *du, *h;
+  int64_t ldy;
+  int act;
+  float *sums;
+  struct Col {};
+  struct Row { f32x4_t g, u; };
+  TW_DEV Col col(int) const { return {}; }
+  TW_DEV Row row(int r, int c) const { return {load4(g + r * ldy + c), load4(u + r * ldy + c)}; }
+  template <int ACT> TW_DEV void put(int, int r, int c, const Col &, const Row &q, f32x4_t v, f32x4_t, f32x4_t *sum) const {
+    const int64_t at = r * ldy + c;
+    f32x4_t a, b, hv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float d;
+      const float y = act_grad<ACT, std::is_same<T, bf16_t>::value>(q.g[i], d);
+      a[i] = v[i] * q.u[i] * d;
+      b[i] = v[i] * y;
+      hv[i] = y * q.u[i];
+    }
+    sum[0] += a;
+    sum[1] += b;
+    store4(dg + at, a);
+    store4(du + at, b);
+    store4(h + at, hv);
+  }
+};
+
+// dz = v act'(pre) for v = dy (dz == NULL: the column sums only).
+template <typename T> struct EpiDz {
+  static constexpr bool DUAL = false, ACTS = true;
+  static constexpr int NSUM = 1;
+  const T *pre;
+  T *dz;
+  int64_t ldy;
+  int act;
+  float *sums;
+  struct Col {};
+  struct Row { f32x4_t z; };
+  TW_DEV Col col(int) const { return {}; }
+  TW_DEV Row row(int r, int c) const { return {pre ? load4(pre + r * ldy + c) : f32x4_t{}}; }
+  template <int ACT> TW_DEV void put(int, int r, int c, const Col &, const Row &q, f32x4_t v, f32x4_t, f32x4_t *sum) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float d;
+      act_grad<ACT, std::is_same<T, bf16_t>::value>(q.z[i], d);
+      v[i] *= d;
+    }
+    sum[0] += v;
+    if (dz) store4(dz + r * ldy + c, v);
+  }
+};
+
+template <class E, typename F> TW_DEV void epi_act(const E &e, F &&f) {
+  if constexpr (E::ACTS) with_act(e.act, f);
+  else f(std::integral_constant<int, kActNone>());
+}
+
+// ---------------------------------------------------------------------------------- products
+
+// `batch` products of one shape, each summed over `segs` pairs of operands (A[b], B[b] for batches, A[s],
+// B[s] for segments; one of batch and segs is 1), k split S times in ranges of ks of the segs * K.
+struct Prod {
+  const void *A[3], *B[3], *A2;             // A2: the second matrix of a dual A
+  int64_t lda[3], ldb;
+  int M, N, K, batch, segs, S, ks;
+  float *part;                              // [S][batch][N][M], dual [..][2 M] (S > 1)
+};
+
+// Entry b of three (a register array indexed by b would lie in scratch).
+template <typename P> TW_DEV P pick(const P (&p)[3], int b) { return b == 0 ? p[0] : b == 1 ? p[1] : p[2]; }
+
+template <class G, class OP, typename T>
+TW_DEV void operands(const Prod &a, int b, int m0, int n0, int k0, OP &A, OP &B) {
+  constexpr bool along = !G::ATR;
+  const int dual = G::DUAL ? 2 : 1;
+  A = {};
+  B = {};
+  const int64_t lda = pick(a.lda, b), ao = along ? m0 * lda + k0 : k0 * lda + m0;
+  const int64_t bo = !G::BTR ? (int64_t)n0 * a.ldb + k0 : (int64_t)k0 * a.ldb + n0;
+  A.p = (const T *)pick(a.A, b) + ao;
+  A.ld = lda;
+  A.n = min(a.M - m0, G::BM / dual);
+  if (G::DUAL) A.p2 = (const T *)a.A2 + ao;
+  B.p = (const T *)pick(a.B, b) + bo;
+  B.ld = a.ldb;
+  B.n = min(a.N - n0, G::BN);
+}
+
+// What mm.h's three tile types have in common, by loop.
+template <class G> struct AsMM : G {
+  static constexpr bool DUAL = false;
+  template <typename ACC> static TW_DEV void mul(const Prod &a, int b, int m0, int n0, int k0, int K, ACC &acc, char *smem) {
+    MmOperand A, B;
+    operands<AsMM, MmOperand, bf16_t>(a, b, m0, n0, k0, A, B);
+    mm_loop<G, 1>(A, B, K, acc, smem);
+  }
+};
+template <class G> struct AsMM64 : G {
+  static constexpr bool ATR = false, BTR = false;
+  template <typename ACC> static TW_DEV void mul(const Prod &a, int b, int m0, int n0, int k0, int K, ACC &acc, char *smem) {
+    MmOperand A, B;
+    operands<AsMM64, MmOperand, bf16_t>(a, b, m0, n0, k0, A, B);
+    mm_loop64<G, 1>(A, B, K, acc, smem);
+  }
+};
+template <class G> struct AsMMF : G {
+  template <typename ACC> static TW_DEV void mul(const Prod &a, int b, int m0, int n0, int k0, int K, ACC &acc, char *smem) {
+    MmfOperand A, B;
+    operands<AsMMF, MmfOperand, float>(a, b, m0, n0, k0, A, B);
+    mmf_loop<G>(A, B, K, acc, smem);
+  }
+};
+
+// A wave's sums over its rows go to sums[block][NSUM][M], block = its 16-lane group's rows.
+template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_dense(Prod a, E e) {
+  __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
+  constexpr int DU = E::DUAL ? 2 : 1, BU = G::BM / DU;    // columns of a tile
+  const int mt = (a.M + BU - 1) / BU, nt = (a.N + G::BN - 1) / G::BN;
+  const int t = mm_xcd_tile(blockIdx.x, mt * nt * a.S * a.batch);
+  if (t < 0) return;
+  int m, n;
+  const int sp = t / (mt * nt), b = sp / a.S, s = sp % a.S;
+  mm_tile_mn<GM>(t % (mt * nt), mt, nt, m, n);
+  const int m0 = m * BU, n0 = n * G::BN;
+  f32x4_t acc[G::FM][G::FN];
+#pragma unroll
+  for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4_t{};
+  const int k0 = s * a.ks, k1 = min(a.segs * a.K, k0 + a.ks);
+  bool again = false;
+  for (int g = 0; g < a.segs; ++g) {
+    const int from = max(k0 - g * a.K, 0), to = min(k1 - g * a.K, a.K);
+    if (from >= to) continue;
+    if (again) __syncthreads();
+    again = true;
+    G::mul(a, b + g, m0, n0, from, to - from, acc, smem);
+  }
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
+  const int wm = wave / G::NWN, wn = wave % G::NWN;
+  const int c0 = m0 + wm * (G::WM / DU) + grp * 4, r0 = n0 + wn * G::WN + (lane & 15);
+  if (a.S > 1) {
+    float *p = a.part + ((int64_t)s * a.batch + b) * a.N * a.M * DU;
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) {
+      const int c = c0 + fm / DU * 16;
+      if (c >= a.M) continue;                             // M is a multiple of 8
+#pragma unroll
+      for (int fn = 0; fn < G::FN; ++fn) {
+        const int r = r0 + fn * 16;
+        if (r < a.N) store4(p + (int64_t)r * a.M * DU + fm % DU * a.M + c, acc[fm][fn]);
+      }
+    }
+    return;
+  }
+  epi_act(e, [&](auto ACT) __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < G::FM; fm += DU) {
+      const int c = c0 + fm / DU * 16;
+      const bool ok = c < a.M;
+      typename E::Col k = {};
+      if (ok) k = e.col(c);
+      typename E::Row q[G::FN] = {};
+#pragma unroll
+      for (int fn = 0; fn < G::FN; ++fn)
+        if (ok && r0 + fn * 16 < a.N) q[fn] = e.row(r0 + fn * 16, c);
+      f32x4_t sum[2] = {};
+#pragma unroll
+      for (int fn = 0; fn < G::FN; ++fn)
+        if (ok && r0 + fn * 16 < a.N)
+          e.template put<decltype(ACT)::value>(b, r0 + fn * 16, c, k, q[fn], acc[fm][fn], acc[fm + DU - 1][fn], sum);
+      if constexpr (E::NSUM > 0) {
+        if (e.sums) {
+#pragma unroll
+          for (int j = 0; j < E::NSUM; ++j) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[j][i] += __shfl_xor(sum[j][i], o, 64);
+            if (ok && (lane & 15) == 0) store4(e.sums + ((int64_t)(n * G::NWN + wn) * E::NSUM + j) * a.M + c, sum[j]);
+          }
+        }
+      }
+    }
+  });
+}
+
+// The epilogue over rows of partial sums, or of a matrix v (EpiDz): a workgroup takes 256 columns of a
+// strip of `strip` rows, thread t the 4 columns 4 (t % 64) of every fourth row. Its sums go to
+// sums[4 strip's number + t / 64].
+template <typename T, class E>
+__global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ part, int S, int batch, const T *__restrict__ v,
+                                                    int64_t ldv, int N, int M, int strip, E e) {
+  constexpr int DU = E::DUAL ? 2 : 1;
+  const int c = (blockIdx.x * 64 + (threadIdx.x & 63)) * 4, b = blockIdx.z, lane4 = threadIdx.x >> 6;
+  if (c >= M) return;
+  const int end = min(N, ((int)blockIdx.y + 1) * strip);
+  const int64_t plane = (int64_t)batch * N * M * DU;
+  epi_act(e, [&](auto ACT) __attribute__((always_inline)) {
+    const typename E::Col k = e.col(c);
+    f32x4_t sum[2] = {};
+    for (int r = blockIdx.y * strip + lane4; r < end; r += 4) {
+      const typename E::Row q = e.row(r, c);
+      f32x4_t a = {}, a2 = {};
+      if (part) {
+        const float *p = part + ((int64_t)b * N + r) * M * DU + c;
+#pragma unroll 8
+        for (int s = 0; s < S; ++s) {
+          a += load4(p + s * plane);
+          if constexpr (DU == 2) a2 += load4(p + s * plane + M);
+        }
+      } else {
+        a = load4(v + r * ldv + c);
+      }
+      e.template put<decltype(ACT)::value>(b, r, c, k, q, a, a2, sum);
+    }
+    if constexpr (E::NSUM > 0) {
+      if (e.sums)
+#pragma unroll
+        for (int j = 0; j < E::NSUM; ++j)
+          store4(e.sums + ((int64_t)(blockIdx.y * 4 + lane4) * E::NSUM + j) * M + c, sum[j]);
+    }
+  });
+}
+
+// out_j[c] = sum over blocks of sums[block][j][c]: a workgroup takes 64 columns, each wave every fourth
+// block.
+__global__ __launch_bounds__(256) void k_dense_sums(const float *__restrict__ sums, int blocks, int M, int nsum,
+                                                    float *__restrict__ out0, float *__restrict__ out1) {
+  __shared__ float red[4][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6, j = blockIdx.y;
+  float v = 0.f;
+  if (c < M)
+#pragma unroll 4
+    for (int i = w; i < blocks; i += 4) v += sums[((int64_t)i * nsum + j) * M + c];
+  red[w][threadIdx.x & 63] = v;
+  __syncthreads();
+  float *out = j ? out1 : out0;
+  if (w == 0 && c < M && out) {
+    const int l = threadIdx.x;
+    out[c] = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
+  }
+}
+
+__global__ __launch_bounds__(256) void k_dense_zero(uint4 *__restrict__ p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// -------------------------------------------------------------------------------------- plan
+
+// Kinds of products, and the tiles of each.
+enum { kAlong, kAcross, kBoth };            // both operands along k; A across; both across
+enum { kSmall, kMid, kLarge, kStream };
+template <int KIND, int C, bool DUAL> struct Shape;
+template <bool D> struct Shape<kAlong, kSmall, D> { typedef AsMM64<MM64<64, 64, 32, 32, 4, 4, D>> G; };
+template <bool D> struct Shape<kAlong, kMid, D> { typedef AsMM64<MM64<128, 128, 64, 64, 3, 2, D>> G; };
+template <bool D> struct Shape<kAlong, kLarge, D> { typedef AsMM64<MM64<256, 256, 128, 64, 3, 2, D>> G; };
+template <bool D> struct Shape<kAlong, kStream, D> { typedef AsMM64<MM64<128, 32, 32, 32, 4, 4, D>> G; };
+template <> struct Shape<kAcross, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, false>> G; };
+template <> struct Shape<kAcross, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, false>> G; };
+template <> struct Shape<kBoth, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, true>> G; };
+template <> struct Shape<kBoth, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, true>> G; };
+template <int KIND, bool DUAL> struct ShapeF {            // fp32 as it is
+  typedef AsMMF<MMF<64, 64, KIND != kAlong, KIND == kBoth, DUAL>> G;
+};
+template <bool DUAL> struct ShapeFew { typedef AsMMF<MMF<128, 32, false, false, DUAL>> G; };
+
+constexpr int kCUs = 256;
+constexpr int64_t kPartBytes = (int64_t)256 << 20;        // partial sums of one product
+struct Tile { int m, n, wn; };              // columns, rows, rows of a wave
+Tile tile_of(bool bf16, int kind, int c) {
+  if (!bf16) return c == kStream ? Tile{128, 32, 32} : Tile{64, 64, 32};
+  if (kind == kAlong)
+    return c == kSmall ? Tile{64, 64, 32} : c == kMid ? Tile{128, 128, 64} : c == kLarge ? Tile{256, 256, 64} : Tile{128, 32, 32};
+  return c == kSmall ? Tile{256, 64, 64} : Tile{256, 256, 128};
+}
+
+// Nanoseconds of `tiles` tiles over `stages` stages: rounds of resident workgroups, each with its stages (all
+// workgroups of a CU together) and its start and epilogue.
+struct Cost {
+  int per_cu, stage, alone, start;          // alone: a stage where no CU has two workgroups
+};
+constexpr Cost kCostAlong[4] = {{2, 450, 450, 2500}, {2, 1000, 750, 4000}, {1, 1450, 1450, 9000}, {2, 450, 450, 2500}};
+constexpr Cost kCostAcross[3] = {{2, 750, 700, 4500}, {}, {1, 850, 850, 10000}};
+constexpr Cost kCostF = {2, 1050, 550, 3000};
+constexpr int kJoin = 3000;                 // the launch that adds partial sums
+int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
+  if (tiles <= kCUs) return stages * c.alone + c.start;
+  const int64_t slots = kCUs * c.per_cu;
+  return (tiles + slots - 1) / slots * (stages * c.stage + c.start);
+}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Split {
+  int cls, S, ks;
+  size_t part;                              // bytes of the partial sums
+};
+// The tile and the split of k (1, 2, 4 .. 64 times) of a product with the least cost. M columns (of each
+// matrix of a dual A), K over all segments.
+Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batch) {
+  const int du = dual ? 2 : 1, ks = kind == kAlong && bf16 ? 64 : 32;
+  Split best = {};
+  int64_t least = 0;
+  auto consider = [&](int c, const Cost &cost) {
+    const Tile t = tile_of(bf16, kind, c);
+    const int64_t tiles = ceil_div((int64_t)M * du, t.m) * ceil_div(N, t.n) * batch;
+    for (int S0 = 1; S0 <= 64; S0 *= 2) {
+      const int64_t size = ceil_div(ceil_div(K, S0), 64) * 64, S = ceil_div(K, size);
+      const int64_t part = S > 1 ? S * batch * N * M * du * 4 : 0;
+      if (S0 > 1 && (tiles * S > kCUs * cost.per_cu || part > kPartBytes || S < S0)) break;
+      const int64_t n = cost_of(cost, tiles * S, ceil_div(size, ks)) + (S > 1 ? kJoin + part * 2 / 5000 : 0);
+      if (least && n * 20 >= least * 19) continue;        // near ties go to the larger tile and fewer splits
+      least = n;
+      best = {c, (int)S, (int)size, align256((size_t)part)};
+    }
+  };
+  if (!bf16) {
+    consider(kSmall, kCostF);
+    if (kind == kAlong && N <= 32) consider(kStream, kCostF);
+  } else if (kind == kAlong) {
+    consider(kLarge, kCostAlong[kLarge]);
+    consider(kMid, kCostAlong[kMid]);
+    consider(kSmall, kCostAlong[kSmall]);
+    if (N <= 32 && ceil_div((int64_t)M * du, 128) > kCUs) consider(kStream, kCostAlong[kStream]);
+  } else {
+    consider(kLarge, kCostAcross[kLarge]);
+    consider(kSmall, kCostAcross[kSmall]);
+  }
+  return best;
+}
+
+int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
+
+// Rows of a strip of k_dense_rows: for column sums few strips, whose sums are added afterwards.
+int strip_of(int N, bool sums) {
+  const int64_t r = ceil_div(N, sums ? 64 : 1024);
+  return (int)(ceil_div(r, 4) * 4);
+}
+int row_strips(int N, bool sums) { return (int)ceil_div(N, strip_of(N, sums)); }
+
+// Blocks of column sums that a product's epilogue leaves.
+int sum_blocks(bool bf16, int kind, const Split &p, int N) {
+  if (p.S > 1) return 4 * row_strips(N, true);
+  const Tile t = tile_of(bf16, kind, p.cls);
+  return (int)(ceil_div(N, t.n) * (t.n / t.wn));
+}
+
+template <typename T, class E>
+hipError_t launch_rows(const Prod &a, const T *v, int64_t ldv, const E &e, hipStream_t s) {
+  const bool sums = E::NSUM > 0 && e.sums;
+  const dim3 grid((unsigned)ceil_div(a.M, 256), row_strips(a.N, sums), a.batch);
+  k_dense_rows<T, E><<<grid, 256, 0, s>>>(v ? nullptr : a.part, a.S, a.batch, v, ldv, a.N, a.M, strip_of(a.N, sums), e);
+  return hipGetLastError();
+}
+
+// One product (a's shape and operands set) by plan p; ws: room for p.part bytes.
+template <typename T, int KIND, class E>
+hipError_t product(Prod a, const Split &p, void *ws, const E &e, hipStream_t s) {
+  a.S = p.S;
+  a.ks = p.ks;
+  a.part = (float *)ws;
+  auto go = [&](auto X) {
+    typedef typename decltype(X)::G G;
+    constexpr int BU = G::BM / (E::DUAL ? 2 : 1);
+    const int64_t tiles = ceil_div(a.M, BU) * ceil_div(a.N, G::BN) * a.S * a.batch;
+    k_dense<G, E, KIND == kAlong ? 4 : 8><<<grid8(tiles), G::NT, 0, s>>>(a, e);
+    return hipGetLastError();
+  };
+  constexpr bool D = E::DUAL;
+  if constexpr (std::is_same<T, float>::value) {
+    if constexpr (KIND == kAlong) {
+      if (p.cls == kStream) TW_TRY_HIP(go(ShapeFew<D>()));
+      else TW_TRY_HIP(go(ShapeF<KIND, D>()));
+    } else {
+      TW_TRY_HIP(go(ShapeF<KIND, D>()));
+    }
+  } else if constexpr (KIND == kAlong) {
+    switch (p.cls) {
+      case kSmall: TW_TRY_HIP(go(Shape<KIND, kSmall, D>())); break;
+      case kMid: TW_TRY_HIP(go(Shape<KIND, kMid, D>())); break;
+      case kLarge: TW_TRY_HIP(go(Shape<KIND, kLarge, D>())); break;
+      default: TW_TRY_HIP(go(Shape<KIND, kStream, D>())); break;
+    }
+  } else {
+    if (p.cls == kSmall) TW_TRY_HIP(go(Shape<KIND, kSmall, D>()));
+    else TW_TRY_HIP(go(Shape<KIND, kLarge, D>()));
+  }
+  return p.S > 1 ? launch_rows<T, E>(a, nullptr, 0, e, s) : hipSuccess;
+}
+
+Prod prod_of(int M, int N, int K) {
+  Prod a = {};
+  a.M = M; a.N = N; a.K = K;
+  a.batch = a.segs = 1;
+  return a;
+}
+
+hipError_t zero(void *p, size_t bytes, hipStream_t s) {
+  const size_t n = bytes / 16, wg = (n + 255) / 256;
+  if (n) k_dense_zero<<<(unsigned)(wg < 4096 ? wg : 4096), 256, 0, s>>>((uint4 *)p, n);
+  return hipGetLastError();
+}
+
+hipError_t add_sums(const float *sums, int blocks, int M, int nsum, float *o0, float *o1, hipStream_t s) {
+  k_dense_sums<<<dim3((unsigned)ceil_div(M, 64), nsum), 256, 0, s>>>(sums, blocks, M, nsum, o0, o1);
+  return hipGetLastError();
+}
+
+template <typename T> EpiLinear<T, false> store_epi(void *y, int64_t ldy) {
+  EpiLinear<T, false> e = {};
+  e.y = y;
+  e.ldy = ldy;
+  e.y_bf16 = !std::is_same<T, float>::value;
+  return e;
+}
+
+// Offsets of a workspace, in order.
+struct Take {
+  size_t at = 0;
+  size_t operator()(size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  }
+};
+
+// ------------------------------------------------------------------------------------ linear
+
+struct LinearBackPlan {
+  Split dx, dw;
+  size_t dz, sums, part, bytes;
+};
+LinearBackPlan linear_back_plan(int T, int K, int N, bool bf16, bool kn, int act, bool want_dx, bool want_dw, bool want_db) {
+  LinearBackPlan p = {};
+  Take take;
+  if (act != kActNone && (want_dx || want_dw)) p.dz = take((size_t)T * N * (bf16 ? 2 : 4));
+  if (want_db) p.sums = take((size_t)4 * row_strips(T, true) * N * 4);
+  size_t part = 0;
+  if (want_dx) {
+    p.dx = split_of(bf16, kn ? kAlong : kAcross, false, K, T, N, 1);
+    part = p.dx.part;
+  }
+  if (want_dw) {
+    p.dw = kn ? split_of(bf16, kBoth, false, N, K, T, 1) : split_of(bf16, kBoth, false, K, N, T, 1);
+    part = p.dw.part > part ? p.dw.part : part;
+  }
+  p.part = take(part);
+  p.bytes = take.at;
+  return p;
+}
+
+template <typename T> hipError_t linear_fwd_run(const LinearArgs &a, hipStream_t s) {
+  const Split p = split_of(!std::is_same<T, float>::value, a.kn ? kAcross : kAlong, false, a.N, a.T, a.K, 1);
+  EpiLinear<T, true> e = {};
+  e.bias = a.bias; e.res = a.res; e.ldr = a.ldr;
+  e.y = a.y; e.ldy = a.N; e.y_bf16 = a.y_bf16;
+  e.pre = (T *)a.pre; e.act = a.act;
+  Prod q = prod_of(a.N, a.T, a.K);
+  q.A[0] = a.w; q.lda[0] = a.kn ? a.N : a.K;
+  q.B[0] = a.x; q.ldb = a.ldx;
+  return a.kn ? product<T, kAcross>(q, p, a.ws, e, s) : product<T, kAlong>(q, p, a.ws, e, s);
+}
+
+template <typename T> hipError_t linear_bwd_run(const LinearBackArgs &a, hipStream_t s) {
+  const LinearBackPlan p = linear_back_plan(a.T, a.K, a.N, !std::is_same<T, float>::value, a.kn, a.act, a.dx != nullptr,
+                                            a.dw != nullptr, a.db != nullptr);
+  char *ws = (char *)a.ws;
+  const T *dz = (const T *)a.dy;
+  int64_t lddz = a.lddy;
+  if (a.act != kActNone || a.db) {
+    EpiDz<T> e = {};
+    e.act = a.act;
+    e.ldy = a.N;
+    if (a.act != kActNone) e.pre = (const T *)a.pre;
+    if (a.act != kActNone && (a.dx || a.dw)) {
+      e.dz = (T *)(ws + p.dz);
+      dz = e.dz;
+      lddz = a.N;
+    }
+    if (a.db) e.sums = (float *)(ws + p.sums);
+    TW_TRY_HIP(launch_rows(prod_of(a.N, a.T, 0), (const T *)a.dy, a.lddy, e, s));
+    if (a.db) TW_TRY_HIP(add_sums(e.sums, 4 * row_strips(a.T, true), a.N, 1, a.db, nullptr, s));
+  }
+  if (a.dx) {
+    Prod q = prod_of(a.K, a.T, a.N);
+    q.A[0] = a.w; q.lda[0] = a.kn ? a.N : a.K;
+    q.B[0] = dz; q.ldb = lddz;
+    const auto e = store_epi<T>(a.dx, a.K);
+    if (a.kn) TW_TRY_HIP((product<T, kAlong>(q, p.dx, ws + p.part, e, s)));
+    else TW_TRY_HIP((product<T, kAcross>(q, p.dx, ws + p.part, e, s)));
+  }
+  if (a.dw) {
+    Prod q = a.kn ? prod_of(a.N, a.K, a.T) : prod_of(a.K, a.N, a.T);
+    const void *x = a.x;
+    q.A[0] = a.kn ? dz : x; q.lda[0] = a.kn ? lddz : a.ldx;
+    q.B[0] = a.kn ? x : dz; q.ldb = a.kn ? a.ldx : lddz;
+    TW_TRY_HIP((product<T, kBoth>(q, p.dw, ws + p.part, store_epi<T>(a.dw, q.M), s)));
+  }
+  return hipSuccess;
+}
+
+// ------------------------------------------------------------------------------------- gated
+
+struct GatedPlan {
+  Split up, down;
+  size_t h, part, bytes;
+};
+GatedPlan gated_plan(int T, int d, int f, bool bf16) {
+  GatedPlan p = {};
+  Take take;
+  p.h = take((size_t)T * f * (bf16 ? 2 : 4));
+  p.up = split_of(bf16, kAlong, true, f, T, d, 1);
+  p.down = split_of(bf16, kAcross, false, d, T, f, 1);
+  p.part = take(p.up.part > p.down.part ? p.up.part : p.down.part);
+  p.bytes = take.at;
+  return p;
+}
+
+struct GatedBackPlan {
+  Split dh, dx, dw;
+  size_t dg, du, h, sums, part, bytes;
+};
+GatedBackPlan gated_back_plan(int T, int d, int f, bool bf16, bool bias) {
+  GatedBackPlan p = {};
+  Take take;
+  const size_t n = (size_t)T * f * (bf16 ? 2 : 4);
+  p.dg = take(n);
+  p.du = take(n);
+  p.h = take(n);
+  p.dh = split_of(bf16, kAlong, false, f, T, d, 1);
+  p.dx = split_of(bf16, kAcross, false, d, T, 2 * (int64_t)f, 1);
+  p.dw = split_of(bf16, kBoth, false, d, f, T, 3);
+  if (bias) p.sums = take((size_t)sum_blocks(bf16, kAlong, p.dh, T) * 2 * f * 4);
+  size_t part = p.dh.part;
+  if (p.dx.part > part) part = p.dx.part;
+  if (p.dw.part > part) part = p.dw.part;
+  p.part = take(part);
+  p.bytes = take.at;
+  return p;
+}
+
+template <typename T> hipError_t gated_fwd_run(const GatedArgs &a, hipStream_t s) {
+  const GatedPlan p = gated_plan(a.T, a.d, a.f, !std::is_same<T, float>::value);
+  char *ws = (char *)a.ws;
+  EpiGlu<T> eu = {};
+  eu.bg = a.bg; eu.bu = a.bu;
+  eu.h = (T *)(ws + p.h); eu.g = (T *)a.g; eu.u = (T *)a.u;
+  eu.ldy = a.f; eu.act = a.act;
+  Prod q = prod_of(a.f, a.T, a.d);
+  q.A[0] = a.wg; q.A2 = a.wu; q.lda[0] = a.d;
+  q.B[0] = a.x; q.ldb = a.ldx;
+  TW_TRY_HIP((product<T, kAlong>(q, p.up, ws + p.part, eu, s)));
+  EpiLinear<T, true> ed = {};
+  ed.res = a.res; ed.ldr = a.ldr;
+  ed.y = a.y; ed.ldy = a.d; ed.y_bf16 = a.y_bf16;
+  q = prod_of(a.d, a.T, a.f);
+  q.A[0] = a.w2; q.lda[0] = a.d;
+  q.B[0] = eu.h; q.ldb = a.f;
+  return product<T, kAcross>(q, p.down, ws + p.part, ed, s);
+}
+
+template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream_t s) {
+  constexpr bool bf16 = !std::is_same<T, float>::value;
+  const bool bias = a.dbg || a.dbu;
+  const GatedBackPlan p = gated_back_plan(a.T, a.d, a.f, bf16, bias);
+  char *ws = (char *)a.ws;
+  EpiGluBack<T> e = {};
+  e.g = (const T *)a.g; e.u = (const T *)a.u;
+  e.dg = (T *)(ws + p.dg); e.du = (T *)(ws + p.du); e.h = (T *)(ws + p.h);
+  e.ldy = a.f; e.act = a.act;
+  if (bias) e.sums = (float *)(ws + p.sums);
+  Prod q = prod_of(a.f, a.T, a.d);
+  q.A[0] = a.w2; q.lda[0] = a.d;
+  q.B[0] = a.dy; q.ldb = a.lddy;
+  TW_TRY_HIP((product<T, kAlong>(q, p.dh, ws + p.part, e, s)));
+  if (bias) TW_TRY_HIP(add_sums(e.sums, sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
+  q = prod_of(a.d, a.T, a.f);
+  q.segs = 2;
+  q.A[0] = a.wg; q.A[1] = a.wu; q.lda[0] = q.lda[1] = a.d;
+  q.B[0] = e.dg; q.B[1] = e.du; q.ldb = a.f;
+  TW_TRY_HIP((product<T, kAcross>(q, p.dx, ws + p.part, store_epi<T>(a.dx, a.d), s)));
+  q = prod_of(a.d, a.f, a.T);
+  q.batch = 3;
+  q.A[0] = q.A[1] = a.x; q.A[2] = a.dy;
+  q.lda[0] = q.lda[1] = a.ldx; q.lda[2] = a.lddy;
+  q.B[0] = e.dg; q.B[1] = e.du; q.B[2] = e.h; q.ldb = a.f;
+  auto ew = store_epi<T>(a.dwg, a.d);
+  ew.y1 = a.dwu;
+  ew.y2 = a.dw2;
+  return product<T, kBoth>(q, p.dw, ws + p.part, ew, s);
+}
+
+}  // namespace
+
+size_t linear_fwd_workspace(int T, int K, int N, int bf16, bool kn) {
+  return split_of(bf16, kn ? kAcross : kAlong, false, N, T, K, 1).part;
+}
+size_t linear_bwd_workspace(int T, int K, int N, int bf16, bool kn, int act, bool dx, bool dw, bool db) {
+  return linear_back_plan(T, K, N, bf16, kn, act, dx, dw, db).bytes;
+}
+size_t gated_fwd_workspace(int T, int d, int f, int bf16) { return gated_plan(T, d, f, bf16).bytes; }
+size_t gated_bwd_workspace(int T, int d, int f, int bf16, bool bias) { return gated_back_plan(T, d, f, bf16, bias).bytes; }
+
+hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s) {
+  return a.bf16 ? linear_fwd_run<bf16_t>(a, s) : linear_fwd_run<float>(a, s);
+}
+hipError_t launch_linear_bwd(const LinearBackArgs &a, hipStream_t s) {
+  const size_t e = a.bf16 ? 2 : 4;
+  if (a.T == 0) {                           // no rows: the sums over them are zero
+    if (a.dw) TW_TRY_HIP(zero(a.dw, (size_t)a.K * a.N * e, s));
+    if (a.db) TW_TRY_HIP(zero(a.db, (size_t)a.N * 4, s));
+    return hipSuccess;
+  }
+  return a.bf16 ? linear_bwd_run<bf16_t>(a, s) : linear_bwd_run<float>(a, s);
+}
+hipError_t launch_gated_fwd(const GatedArgs &a, hipStream_t s) {
+  return a.bf16 ? gated_fwd_run<bf16_t>(a, s) : gated_fwd_run<float>(a, s);
+}
+hipError_t launch_gated_bwd(const GatedBackArgs &a, hipStream_t s) {
+  const size_t n = (size_t)a.d * a.f * (a.bf16 ? 2 : 4);
+  if (a.T == 0) {
+    TW_TRY_HIP(zero(a.dwg, n, s));
+    TW_TRY_HIP(zero(a.dwu, n, s));
+    TW_TRY_HIP(zero(a.dw2, n, s));
+    if (a.dbg) TW_TRY_HIP(zero(a.dbg, (size_t)a.f * 4, s));
+    if (a.dbu) TW_TRY_HIP(zero(a.dbu, (size_t)a.f * 4, s));
+    return hipSuccess;
+  }
+  return a.bf16 ? gated_bwd_run<bf16_t>(a, s) : gated_bwd_run<float>(a, s);
+}
+
+}  // namespace tw

@@ -204,4 +204,75 @@ struct XentArgs {
 size_t xent_workspace_bytes(int T, int d, int V, int bf16, bool grad);
 hipError_t launch_xent(const XentArgs &a, hipStream_t s);
 
+// dense.hip: linear layer (w [N][K], or [K][N] where kn) and gated block, operands and gradients in one
+// type. act: twell_act_t.
+struct LinearArgs {
+  const void *x, *w, *res;
+  int64_t ldx, ldr;
+  const float *bias;
+  int T, K, N, bf16, y_bf16, kn, act;
+  void *y, *pre, *ws;
+};
+struct LinearBackArgs {
+  const void *dy, *x, *w, *pre;
+  int64_t lddy, ldx;
+  int T, K, N, bf16, kn, act;
+  void *dx, *dw;
+  float *db;
+  void *ws;
+};
+struct GatedArgs {
+  const void *x, *wg, *wu, *w2, *res;
+  int64_t ldx, ldr;
+  const float *bg, *bu;
+  int T, d, f, bf16, y_bf16, act;
+  void *y, *g, *u, *ws;
+};
+struct GatedBackArgs {
+  const void *dy, *x, *wg, *wu, *w2, *g, *u;
+  int64_t lddy, ldx;
+  int T, d, f, bf16, act;
+  void *dx, *dwg, *dwu, *dw2;
+  float *dbg, *dbu;
+  void *ws;
+};
+size_t linear_fwd_workspace(int T, int K, int N, int bf16, bool kn);
+size_t linear_bwd_workspace(int T, int K, int N, int bf16, bool kn, int act, bool dx, bool dw, bool db);
+size_t gated_fwd_workspace(int T, int d, int f, int bf16);
+size_t gated_bwd_workspace(int T, int d, int f, int bf16, bool bias);
+hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_bwd(const LinearBackArgs &a, hipStream_t s);
+hipError_t launch_gated_fwd(const GatedArgs &a, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedBackArgs &a, hipStream_t s);
+
+// adamw.hip: the host arrays are read during the call only; a launch takes kAdamTab tensors in its
+// arguments. States: m, v fp32, or codes with their scales (ms, vs) where eight.
+constexpr int kAdamTab = 40, kAdamBlock = 256;
+struct AdamArgs {
+  void *const *p, *const *m, *const *v, *const *copy;
+  const void *const *g;
+  float *const *ms, *const *vs;
+  const int64_t *len;
+  const int32_t *p_dtype, *g_dtype;
+  const double *decay;
+  int n;
+  bool eight;
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float *lr_dev;
+  const int64_t *step_dev;
+  const float *norm;
+  float max_norm;
+};
+hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
+struct AdamValuesArgs {
+  const void *const *codes;
+  const float *const *scales;
+  const int64_t *len;
+  const int32_t *second;                    // codes of v
+  int n, out_bf16;
+  void *const *out;
+};
+hipError_t launch_adamw8_values(const AdamValuesArgs &a, hipStream_t s);
+
 }  // namespace tw

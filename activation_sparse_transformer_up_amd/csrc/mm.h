@@ -60,13 +60,19 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> str
 // tile) for one across k; ld: elements between rows; n: rows (columns) of the tile that exist (a
 // multiple of 8 across k); plane: elements between the bf16 planes of an fp32 operand; rows (B of
 // mm_loop64 only): where the tile's rows are not consecutive, their numbers (n of them, in LDS, may
-// lie in smem).
+// lie in smem); p2 (A of a DUAL tile only): the second matrix.
 struct MmOperand {
   const uint16_t *p;
   int64_t ld, plane;
   int n;
   const int *rows = nullptr;
+  const uint16_t *p2 = nullptr;
 };
+
+// Row r of a DUAL tile of A is row mm_dual_row(r) of the first matrix where r / 16 is even, of the
+// second where it is odd: a wave then holds both products of the same columns in neighbouring
+// fragments.
+TW_DEV int mm_dual_row(int r) { return (r >> 5) * 16 + (r & 15); }
 
 // The six products of planes, smallest first: (lo, hi) (hi, lo) (mid, mid) (mid, hi) (hi, mid)
 // (hi, hi), as planes 0 = hi, 1 = mid, 2 = lo.
@@ -254,13 +260,15 @@ TW_DEV void mm_loop(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&acc
 //   products of (kt, second half), between them the reads of (kt + 1, first half) and the loads of
 //   stages kt + NSB of B and kt + NSA of A into the places of stage kt
 // The order of the loads (B's before A's in every step) makes the wait a fixed count.
-template <int BM_, int BN_, int WM_, int WN_, int NSA_, int NSB_> struct MM64 {
+template <int BM_, int BN_, int WM_, int WN_, int NSA_, int NSB_, bool DUAL_ = false> struct MM64 {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NSA = NSA_, NSB = NSB_;
+  static constexpr bool DUAL = DUAL_;                     // A of two matrices: n counts the rows of each
   static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, NT = NW * 64;
   static constexpr int FM = WM / 16, FN = WN / 16;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;            // 1 KB wave-loads per wave and stage
   static constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, SMEM = NSA * A_STAGE + NSB * B_STAGE;
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NSB >= 2 && (NSA == NSB || NSA == NSB + 1), "tile");
+  static_assert(!DUAL || WM % 32 == 0, "pairs of fragments");
 };
 
 template <class G, int NP>
@@ -283,7 +291,8 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
     const int blk = wave + G::NW * (i < G::LB ? i : i - G::LB), r = blk * 8 + (lane >> 3);
     const int c = (lane & 7) ^ ((r >> 1) & 7);
     kof[i] = c * 8;
-    voff[i] = r < o.n ? (uint32_t)((o.rows ? o.rows[r] : r) * o.ld + c * 8) * 2 : OOB;
+    if (G::DUAL && i >= G::LB) voff[i] = mm_dual_row(r) < o.n ? (uint32_t)(mm_dual_row(r) * o.ld + c * 8) * 2 : OOB;
+    else voff[i] = r < o.n ? (uint32_t)((o.rows ? o.rows[r] : r) * o.ld + c * 8) * 2 : OOB;
   }
   const int nk = (K + 63) / 64 * NP;
   if (nk == 0) return;
@@ -298,7 +307,7 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
     char *at = smem + (isB ? G::NSA * G::A_STAGE + lp[0] * G::B_STAGE : lp[1] * G::A_STAGE) + blk * 1024;
     const uint32_t vo = lk[o] + kof[i] < K && (NP == 1 || lt[o] < NP) ? voff[i] : OOB;
     const int64_t pb = NP > 1 ? mm_plane_b(lt[0]) * B.plane : 0, pa = NP > 1 ? mm_plane_a(lt[1]) * A.plane : 0;
-    const uint16_t *base = isB ? B.p + pb : A.p + pa;
+    const uint16_t *base = isB ? B.p + pb : (G::DUAL && (blk >> 1 & 1) ? A.p2 : A.p) + pa;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base + lk[o]), (lds_void_t *)at, 16, vo, 0, 0, 0);
     if (i != G::LB - 1 && i != NL - 1) return;            // the operand's last load of the stage
     lk[o] += 64;
@@ -395,18 +404,20 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
 // four j in one load. In LDS, without bank conflicts:
 //   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
 //   across k:  k row j at 256 j, its 64-byte chunk c at c ^ ((j >> 2) & 3)
-template <int BM_, int BN_, bool ATR_, bool BTR_> struct MMF {
+template <int BM_, int BN_, bool ATR_, bool BTR_, bool DUAL_ = false> struct MMF {
   static constexpr int BM = BM_, BN = BN_, WM = 32, WN = 32, NS = 4;
-  static constexpr bool ATR = ATR_, BTR = BTR_;
+  static constexpr bool ATR = ATR_, BTR = BTR_, DUAL = DUAL_;
   static constexpr int NWM = BM / WM, NWN = BN / WN, NW = 4, NT = 256, FM = 2, FN = 2;
   static constexpr int LA = BM / 32, LB = BN / 32, NL = LA + LB;      // 1 KB wave-loads per wave and stage
   static constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128, SMEM = NS * STAGE;
   static_assert(NWM * NWN == NW && (!ATR || BM == 64) && (!BTR || BN == 64), "tile");
+  static_assert(!DUAL || !ATR, "two matrices lie along k");
 };
 struct MmfOperand {                                       // as MmOperand; n a multiple of 4 across k
   const float *p;
   int64_t ld;
   int n;
+  const float *p2 = nullptr;
 };
 
 // Fragment at row r0 of a staged operand, half h: element j of lane l is row r0 + l % 16, k = 16 h + 4 (l
@@ -442,8 +453,9 @@ template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B
       voff[i] = col < o.n ? (uint32_t)(kof[i] * o.ld + col) * 4 : OOB;
     } else {                                              // 8 rows
       const int r = blk * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const int q = G::DUAL && i < G::LA ? mm_dual_row(r) : r;
       kof[i] = c * 4;
-      voff[i] = r < o.n ? (uint32_t)(r * o.ld + c * 4) * 4 : OOB;
+      voff[i] = q < o.n ? (uint32_t)(q * o.ld + c * 4) * 4 : OOB;
     }
   }
   const int nk = (K + 31) / 32;
@@ -454,7 +466,8 @@ template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B
     for (int i = 0; i < G::NL; ++i) {
       const bool isA = i < G::LA;
       char *at = smem + kt % G::NS * G::STAGE + (isA ? 0 : G::A_BYTES) + (wave + 4 * (isA ? i : i - G::LA)) * 1024;
-      const float *base = isA ? A.p + (G::ATR ? lk * A.ld : lk) : B.p + (G::BTR ? lk * B.ld : lk);
+      const float *pa = G::DUAL && ((wave + 4 * i) >> 1 & 1) ? A.p2 : A.p;
+      const float *base = isA ? pa + (G::ATR ? lk * A.ld : lk) : B.p + (G::BTR ? lk * B.ld : lk);
       const uint32_t vo = lk + kof[i] < K ? voff[i] : OOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(base), (lds_void_t *)at, 16, vo, 0, 0, 0);
     }

@@ -542,6 +542,116 @@ int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
               float *norm, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Dense layers: a linear layer with its epilogue, and the gated feed-forward block, each with its
+ * backward. They are the dense counterparts of the sparse layer's products (weights in the same
+ * layouts), for models whose activations are not sparse or not yet.
+ *
+ * act (twell_act_t): none; relu; silu z / (1 + exp(-z)); gelu z (1 + erf(z / sqrt 2)) / 2; gelu_tanh
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. relu'(0) = 0.
+ *
+ * linear_fwd —
+ *   z = x w^T + bias   w [d_out][d_in], w_layout TWELL_W_NK (nn.Linear's; w1t above)
+ *   z = x w + bias     w [d_in][d_out], w_layout TWELL_W_KN (w2 above)
+ *   y = act(z) + residual                                              [T][d_out] y_dtype
+ *   pre = z in dtype (may be NULL; the backward of an activation needs it)
+ * x [T][d_in] and w in dtype, bias [d_out] fp32 or NULL, residual [T][d_out] in y_dtype or NULL. x,
+ * residual, dy: rows ldx, ldr, lddy elements apart (as for layer_norm_fwd).
+ *
+ * linear_bwd — dz = dy act'(pre); dx = dz w [T][d_in], dw = dz^T x (in w's layout), db = sum_t dz [d_out] fp32.
+ * dy, x, w, pre [T][d_out], dx and dw in dtype. pre is not looked at for TWELL_ACT_NONE. dx, dw, db may
+ * each be NULL (w is not looked at without dx, x without dw).
+ *
+ * ffn_gated_dense_fwd — the block whose sparse form is twell_gated_ffn_fwd, any act:
+ *   g = x wg^T + bg;  u = x wu^T + bu;  h = act(g) u;  y = h w2 + residual       [T][d] y_dtype
+ * wg, wu, w2 [f][d] in dtype; bg, bu [f] fp32 or NULL; g, u [T][f] in dtype, both or neither (the backward
+ * needs them; in inference NULL). Both up products, the activation and their product are one kernel.
+ *
+ * ffn_gated_dense_bwd — dh = dy w2^T, dg = dh u act'(g), du = dh act(g):
+ *   dx = dg wg + du wu [T][d];  dwg = dg^T x, dwu = du^T x, dw2 = (act(g) u)^T dy [f][d]    in dtype
+ *   dbg = sum_t dg, dbu = sum_t du [f] fp32 (may be NULL)
+ *
+ * Products are summed in fp32. bf16: h, dg, du and dz are rounded to bf16 once, as operands of the next
+ * product; biases' gradients are sums of unrounded fp32 values. The same bits on every call. A NaN or
+ * infinity in a row of x, dy, g, u or residual stays in that row of y and dx. The
+ * workspaces (..._workspace_bytes; may be 0, then NULL is allowed) need not be initialised; they hold h,
+ * or dg, du and h, or dz, in dtype, and up to 256 MB of partial sums. T == 0: the forwards do nothing, the
+ * backwards write zeros to the weights' and biases' gradients.
+ * Errors: TWELL_ERR_ARG (null, dtype, act, w_layout, one of g and u), TWELL_ERR_SHAPE (T < 0, a size <= 0,
+ * ld below the row), TWELL_ERR_ALIGN (d_in, d_out, d, f, ld % 8, pointers), TWELL_ERR_WORKSPACE,
+ * TWELL_ERR_UNSUPPORTED (T > 2^24; d_in, d_out, d or f > 2^20; ld > 2^21).
+ */
+typedef enum {
+  TWELL_ACT_NONE = 0,
+  TWELL_ACT_RELU = 1,
+  TWELL_ACT_SILU = 2,
+  TWELL_ACT_GELU = 3,
+  TWELL_ACT_GELU_TANH = 4
+} twell_act_t;
+typedef enum { TWELL_W_NK = 0, TWELL_W_KN = 1 } twell_w_layout_t;
+
+size_t linear_fwd_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype, int32_t w_layout);
+int linear_fwd(const void *x, int64_t ldx, const void *w, int32_t w_layout, const float *bias,
+               const void *residual, int64_t ldr, int32_t dtype, int32_t T, int32_t d_in, int32_t d_out,
+               int32_t act, void *y, int32_t y_dtype, void *pre, void *workspace,
+               size_t workspace_bytes, void *stream);
+/* want_*: whether dx, dw, db are given. */
+size_t linear_bwd_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype, int32_t w_layout,
+                                  int32_t act, int32_t want_dx, int32_t want_dw, int32_t want_db);
+int linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w, int32_t w_layout,
+               const void *pre, int32_t dtype, int32_t T, int32_t d_in, int32_t d_out, int32_t act,
+               void *dx, void *dw, float *db, void *workspace, size_t workspace_bytes, void *stream);
+size_t ffn_gated_dense_fwd_workspace_bytes(int32_t T, int32_t d_model, int32_t d_ff, int32_t dtype);
+int ffn_gated_dense_fwd(const void *x, int64_t ldx, const void *wg, const void *wu, const void *w2,
+                        const float *bg, const float *bu, const void *residual, int64_t ldr,
+                        int32_t dtype, int32_t T, int32_t d_model, int32_t d_ff, int32_t act, void *y,
+                        int32_t y_dtype, void *g, void *u, void *workspace, size_t workspace_bytes,
+                        void *stream);
+size_t ffn_gated_dense_bwd_workspace_bytes(int32_t T, int32_t d_model, int32_t d_ff, int32_t dtype,
+                                           int32_t want_bias);
+int ffn_gated_dense_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *wg,
+                        const void *wu, const void *w2, const void *g, const void *u, int32_t dtype,
+                        int32_t T, int32_t d_model, int32_t d_ff, int32_t act, void *dx, void *dwg,
+                        void *dwu, void *dw2, float *dbg, float *dbu, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * adamw_step — one AdamW step over n tensors, in place:
+ *   g' = c g, c = min(1, max_norm / (*norm + 1e-6)) where norm is given (grad_norm's result), else g
+ *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay_i) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * The arrays are HOST arrays of length n, read during the call only, of device tensors of sizes[i]
+ * elements (contiguous, aligned to their element; 16-byte aligned ones take wider accesses): params in
+ * dtypes[i], grads in grad_dtypes[i], copies (NULL, or NULL entries, for none) the new params in bf16, for
+ * fp32 params. A size of 0 (pointers ignored) and n = 0 are allowed.
+ * state_bits 32: m, v fp32 (m_scales, v_scales ignored). state_bits 8: m, v one byte per element, with a
+ * fp32 scale per block of TWELL_ADAMW_BLOCK consecutive elements (ceil(size / block) each):
+ *   m = q |q| m_scale (q signed);  v = q^4 v_scale (q unsigned)
+ * requantised every step to the nearest code, scale = block's largest / 127^2 (255^4), at least 2^-126; a v
+ * above zero keeps a code above zero. All zeros is the initial state. The step itself uses the unrounded
+ * m and v.
+ * lr and step are host values, or, where lr_dev or step_dev is given, device scalars read by the
+ * kernel (a captured step replays with the values that they then hold). step >= 1 counts this step.
+ * A norm that is NaN or infinite skips the step: nothing is written. Without a norm, a NaN or infinite
+ * gradient reaches its own element, with 8-bit states its block's states too.
+ * Errors: TWELL_ERR_ARG (null, dtypes, state_bits, a copy of a bf16 param; lr, weight decay, max_norm
+ * negative or NaN, betas outside [0, 1), eps <= 0, step < 1; an output that overlaps another, a gradient
+ * or the scalars: a tensor stands in the list once), TWELL_ERR_SHAPE (negative n or size), TWELL_ERR_ALIGN,
+ * TWELL_ERR_UNSUPPORTED (more than 2^40 elements in all).
+ *
+ * adamw8_values — the values of n tensors of 8-bit states, in out_dtype: codes[i] of m, or of v where
+ * second[i] is not 0. Outputs must not overlap each other or the codes. Errors as above.
+ */
+#define TWELL_ADAMW_BLOCK 256
+int adamw_step(void *const *params, const void *const *grads, void *const *m, void *const *v,
+               float *const *m_scales, float *const *v_scales, void *const *copies,
+               const int64_t *sizes, const int32_t *dtypes, const int32_t *grad_dtypes,
+               const double *weight_decay, int32_t n, int32_t state_bits, double lr, const float *lr_dev,
+               double beta1, double beta2, double eps, int64_t step, const int64_t *step_dev,
+               const float *norm, float max_norm, void *stream);
+int adamw8_values(const void *const *codes, const float *const *scales, const int32_t *second,
+                  const int64_t *sizes, int32_t n, void *const *outs, int32_t out_dtype, void *stream);
+
+/*
  * twell_sync_status — waits for `stream`, then reads *ovf_n: TWELL_ERR_OVF_CAPACITY if it
  * exceeds ovf_cap, TWELL_OK otherwise (TWELL_ERR_HIP if the wait or copy fails).
  */
