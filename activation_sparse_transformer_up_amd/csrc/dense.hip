@@ -30,49 +30,76 @@ namespace {
 
 typedef uint16_t bf16_t;
 
-TW_DEV f32x4_t load4(const float *p) { return *(const f32x4_t *)p; }
-TW_DEV f32x4_t load4(const bf16_t *p) {
-  const uint2 u = *(const uint2 *)p;
-  return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                 __uint_as_float(u.y & 0xFFFF0000u)};
-}
 TW_DEV void store4(float *p, f32x4_t v) { *(f32x4_t *)p = v; }
-TW_DEV void store4(bf16_t *p, f32x4_t v) { *(uint2 *)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])); }
+
+// 8 neighbouring elements; plain stores, for what the next product reads.
+TW_DEV void keep8(float *p, const float (&v)[8]) {
+  *(f32x4_t *)p = f32x4_t{v[0], v[1], v[2], v[3]};
+  *(f32x4_t *)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
+TW_DEV void keep8(bf16_t *p, const float (&v)[8]) {
+  *(uint4 *)p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+TW_DEV void opt8(const float *p, int c, float (&o)[8]) {
+  if (p) {
+    load8(p + c, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  }
+}
 
 // --------------------------------------------------------------------------------- epilogues
-// Of 4 columns c .. c + 3 of row r: col(c) is loaded once per column, row(r, c) ahead of put(), which
-// writes the outputs and adds to the NSUM column sums that the backward needs. ACTS: by activation.
+// shift(r, c) moves the pointers to a tile's first row and column, from which offsets fit 32 bits. Of 8
+// columns c .. c + 7 of row r: col(c) is loaded once per column, Row::load(e, r, c) ahead of put(), which
+// writes the outputs and adds to the NSUM column sums that the backward needs. v: the product (the first
+// of a dual one), w: the second. ACTS: by activation.
 
-// y = act(v + bias) + residual; pre = v + bias. b: the batch's output.
-template <typename T, bool ACTS_> struct EpiLinear {
+// y = act(v + bias) + residual; pre = v + bias. RES: with a residual, of y's type YT.
+template <typename T, typename YT, bool ACTS_, bool RES> struct EpiLinear {
   static constexpr bool DUAL = false, ACTS = ACTS_;
   static constexpr int NSUM = 0;
   const float *bias;
-  const void *res;
+  const YT *res;
   int64_t ldr, ldy;
-  void *y, *y1, *y2;                        // y1, y2: of the second and third batch
+  YT *y, *y1, *y2;                          // y1, y2: of the second and third batch
   T *pre;
-  int act, y_bf16;
+  int act;
   float *sums;
-  struct Col { f32x4_t bias; };
-  struct Row { f32x4_t res; };
-  TW_DEV Col col(int c) const { return {bias ? load4(bias + c) : f32x4_t{}}; }
-  TW_DEV Row row(int r, int c) const {
-    if (!res) return {f32x4_t{}};
-    return {y_bf16 ? load4((const bf16_t *)res + r * ldr + c) : load4((const float *)res + r * ldr + c)};
-  }
-  template <int ACT> TW_DEV void put(int b, int r, int c, const Col &k, const Row &q, f32x4_t v, f32x4_t, f32x4_t *) const {
-    const int64_t at = r * ldy + c;
-    if constexpr (ACTS) {
-      v += k.bias;
-      if (pre) store4(pre + at, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]);
-      v += q.res;
+  struct Col { float bias[8]; };
+  struct Row {
+    Raw8<YT> res;
+    TW_DEV void load(const EpiLinear &e, int r, int c) {
+      if constexpr (RES) res.load(e.res + (uint32_t)(r * (int)e.ldr + c));
     }
-    void *o = ACTS || b == 0 ? y : b == 1 ? y1 : y2;
-    if (y_bf16) store4((bf16_t *)o + at, v);
-    else store4((float *)o + at, v);
+  };
+  TW_DEV void shift(int b, int64_t r, int c) {
+    YT *const y0 = y, *const o = b == 1 ? y1 + 0 : y2 + 0;  // (values: a choice of members would lie in scratch)
+    y = (ACTS || b == 0 ? y0 : o) + r * ldy + c;
+    if (pre) pre += r * ldy + c;
+    if (bias) bias += c;
+    if constexpr (RES) res += r * ldr + c;
+  }
+  TW_DEV void col(int c, Col &k) const {
+    if constexpr (ACTS) opt8(bias, c, k.bias);
+  }
+  template <int ACT>
+  TW_DEV void put(int r, int c, const Col &k, const Row &q, float (&v)[8], float (&)[8], float (*)[8]) const {
+    const uint32_t at = r * (int)ldy + c;
+    if constexpr (ACTS) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += k.bias[i];
+      if (pre) store8(pre + at, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]);
+    }
+    if constexpr (RES) {
+      float u[8];
+      q.res.to(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += u[i];
+    }
+    store8(y + at, v);
   }
 };
 
@@ -85,53 +112,90 @@ template <typename T> struct EpiGlu {
   int64_t ldy;
   int act;
   float *sums;
-  struct Col { f32x4_t bg, bu; };
-  struct Row {};
-  TW_DEV Col col(int c) const { return {bg ? load4(bg + c) : f32x4_t{}, bu ? load4(bu + c) : f32x4_t{}}; }
-  TW_DEV Row row(int, int) const { return {}; }
-  template <int ACT> TW_DEV void put(int, int r, int c, const Col &k, const Row &, f32x4_t v, f32x4_t w, f32x4_t *) const {
-    const int64_t at = r * ldy + c;
-    v += k.bg;
-    w += k.bu;
+  struct Col { float bg[8], bu[8]; };
+  struct Row {
+    TW_DEV void load(const EpiGlu &, int, int) {}
+  };
+  TW_DEV void shift(int, int64_t r, int c) {
+    h += r * ldy + c;
     if (g) {
-      store4(g + at, v);
-      store4(u + at, w);
+      g += r * ldy + c;
+      u += r * ldy + c;
+    }
+    if (bg) bg += c;
+    if (bu) bu += c;
+  }
+  TW_DEV void col(int c, Col &k) const {
+    opt8(bg, c, k.bg);
+    opt8(bu, c, k.bu);
+  }
+  template <int ACT>
+  TW_DEV void put(int r, int c, const Col &k, const Row &, float (&v)[8], float (&w)[8], float (*)[8]) const {
+    const uint32_t at = r * (int)ldy + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] += k.bg[i];
+      w[i] += k.bu[i];
+    }
+    if (g) {
+      store8(g + at, v);
+      store8(u + at, w);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]) * w[i];
-    store4(h + at, v);
+    for (int i = 0; i < 8; ++i) v[i] = act_of<ACT, std::is_same<T, bf16_t>::value>(v[i]) * w[i];
+    keep8(h + at, v);
   }
 };
 
-// dg = v u act'(g), du = v act(g), h = act(g) u for v = dh.
-template <typename T> struct EpiGluBack {
+// dg = v u act'(g), du = v act(g), h = act(g) u for v = dh. SUMS: with the sums of dg and du.
+template <typename T, bool SUMS> struct EpiGluBack {
   static constexpr bool DUAL = false, ACTS = true;
-  static constexpr int NSUM = 2;
+  static constexpr int NSUM = SUMS ? 2 : 0;
   const T *g, *u;
   T *dg, *du, *h;
   int64_t ldy;
   int act;
   float *sums;
   struct Col {};
-  struct Row { f32x4_t g, u; };
-  TW_DEV Col col(int) const { return {}; }
-  TW_DEV Row row(int r, int c) const { return {load4(g + r * ldy + c), load4(u + r * ldy + c)}; }
-  template <int ACT> TW_DEV void put(int, int r, int c, const Col &, const Row &q, f32x4_t v, f32x4_t, f32x4_t *sum) const {
-    const int64_t at = r * ldy + c;
-    f32x4_t a, b, hv;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float d;
-      const float y = act_grad<ACT, std::is_same<T, bf16_t>::value>(q.g[i], d);
-      a[i] = v[i] * q.u[i] * d;
-      b[i] = v[i] * y;
-      hv[i] = y * q.u[i];
+  struct Row {
+    Raw8<T> g, u;
+    TW_DEV void load(const EpiGluBack &e, int r, int c) {
+      const uint32_t at = r * (int)e.ldy + c;
+      g.load(e.g + at);
+      u.load(e.u + at);
     }
-    sum[0] += a;
-    sum[1] += b;
-    store4(dg + at, a);
-    store4(du + at, b);
-    store4(h + at, hv);
+  };
+  TW_DEV void shift(int, int64_t r, int c) {
+    const int64_t at = r * ldy + c;
+    g += at;
+    u += at;
+    dg += at;
+    du += at;
+    h += at;
+  }
+  TW_DEV void col(int, Col &) const {}
+  template <int ACT>
+  TW_DEV void put(int r, int c, const Col &, const Row &q, float (&v)[8], float (&)[8], float (*sum)[8]) const {
+    const uint32_t at = r * (int)ldy + c;
+    float g[8], u[8], hv[8];
+    q.g.to(g);
+    q.u.to(u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float d;
+      const float a = act_grad<ACT, std::is_same<T, bf16_t>::value>(g[i], d);
+      hv[i] = a * u[i];
+      g[i] = v[i] * u[i] * d;
+      u[i] = v[i] * a;
+      if constexpr (SUMS) {
+        sum[0][i] += g[i];
+        sum[1][i] += u[i];
+      }
+      if (i % 2) __builtin_amdgcn_sched_barrier(0);       // the registers of two elements at a time
+    }
+    keep8(dg + at, g);
+    keep8(du + at, u);
+    keep8(h + at, hv);
   }
 };
 
@@ -145,18 +209,32 @@ template <typename T> struct EpiDz {
   int act;
   float *sums;
   struct Col {};
-  struct Row { f32x4_t z; };
-  TW_DEV Col col(int) const { return {}; }
-  TW_DEV Row row(int r, int c) const { return {pre ? load4(pre + r * ldy + c) : f32x4_t{}}; }
-  template <int ACT> TW_DEV void put(int, int r, int c, const Col &, const Row &q, f32x4_t v, f32x4_t, f32x4_t *sum) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float d;
-      act_grad<ACT, std::is_same<T, bf16_t>::value>(q.z[i], d);
-      v[i] *= d;
+  struct Row {
+    Raw8<T> z;
+    TW_DEV void load(const EpiDz &e, int r, int c) {
+      if (e.pre) z.load(e.pre + (uint32_t)(r * (int)e.ldy + c));
     }
-    sum[0] += v;
-    if (dz) store4(dz + r * ldy + c, v);
+  };
+  TW_DEV void shift(int, int64_t r, int c) {
+    if (pre) pre += r * ldy + c;
+    if (dz) dz += r * ldy + c;
+  }
+  TW_DEV void col(int, Col &) const {}
+  template <int ACT>
+  TW_DEV void put(int r, int c, const Col &, const Row &q, float (&v)[8], float (&)[8], float (*sum)[8]) const {
+    if constexpr (ACT != kActNone) {
+      float z[8];
+      q.z.to(z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float d;
+        act_grad<ACT, std::is_same<T, bf16_t>::value>(z[i], d);
+        v[i] *= d;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[0][i] += v[i];
+    if (dz) keep8(dz + (uint32_t)(r * (int)ldy + c), v);
   }
 };
 
@@ -221,10 +299,17 @@ template <class G> struct AsMMF : G {
   }
 };
 
-// A wave's sums over its rows go to sums[block][NSUM][M], block = its 16-lane group's rows.
+// The epilogue turns each wave's tile through LDS, which the loop no longer needs, 32 rows at a time: a lane of
+// the accumulators holds 4 columns of one row (32-byte pieces of 16 rows per access), turned it holds 8, and a
+// wave reads and writes whole 128-byte lines. What an epilogue reads (a residual, g and u) is loaded 32 rows ahead.
+// T = 4096, N = 8192, two rounds of tiles: K = 64 36 -> 21 us, with a residual 69 -> 27; the gated backward of
+// T = 16384, d = 4096, f = 14336 10.2 -> 9.0 ms, of which dh's epilogue moves 2.3 GB.
+// The wave's column sums go to sums[block][NSUM][M], block = the number of its rows' tile.
 template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_dense(Prod a, E e) {
+  constexpr int DU = E::DUAL ? 2 : 1, BU = G::BM / DU, WU = G::WM / DU;       // columns of a tile, of a wave
+  constexpr int LD = G::WM + 4;                           // floats from row to row in LDS
+  static_assert(G::FN % 2 == 0 && G::NW * 32 * LD * 4 <= G::SMEM, "turning");
   __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
-  constexpr int DU = E::DUAL ? 2 : 1, BU = G::BM / DU;    // columns of a tile
   const int mt = (a.M + BU - 1) / BU, nt = (a.N + G::BN - 1) / G::BN;
   const int t = mm_xcd_tile(blockIdx.x, mt * nt * a.S * a.batch);
   if (t < 0) return;
@@ -249,8 +334,8 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 4;
   const int wm = wave / G::NWN, wn = wave % G::NWN;
-  const int c0 = m0 + wm * (G::WM / DU) + grp * 4, r0 = n0 + wn * G::WN + (lane & 15);
   if (a.S > 1) {
+    const int c0 = m0 + wm * WU + grp * 4, r0 = n0 + wn * G::WN + (lane & 15);
     float *p = a.part + ((int64_t)s * a.batch + b) * a.N * a.M * DU;
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) {
@@ -264,32 +349,57 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
     }
     return;
   }
+  // rows of a pass, lanes per row, rows per access, accesses; 16 rows where the inputs of 32 would not stay in
+  // registers beside the accumulators
+  constexpr int PR = WU == 128 && sizeof(typename E::Row) > 16 ? 16 : 32, LPR = WU / 8, RPI = 64 / LPR, NI = PR / RPI;
+  static_assert(LPR * RPI == 64 && NI * RPI == PR, "turning");
+  e.shift(b, n0, m0);
+  const int c = wm * WU + lane % LPR * 8, r0 = wn * G::WN + lane / LPR, rows = a.N - n0;      // of the tile
+  float *own = (float *)smem + wave * PR * LD;            // this wave's rows
+  const bool ok = c < a.M - m0;
+  typename E::Col k;
+  typename E::Row q[NI];
+  if (ok) {
+    e.col(c, k);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (r0 + i * RPI < rows) q[i].load(e, r0 + i * RPI, c);
+  }
+  __syncthreads();                                        // the other waves have read the last stage
   epi_act(e, [&](auto ACT) __attribute__((always_inline)) {
+    float sum[2][8] = {};
 #pragma unroll
-    for (int fm = 0; fm < G::FM; fm += DU) {
-      const int c = c0 + fm / DU * 16;
-      const bool ok = c < a.M;
-      typename E::Col k = {};
-      if (ok) k = e.col(c);
-      typename E::Row q[G::FN] = {};
+    for (int h = 0; h < G::WN / PR; ++h) {
+      wave_lds_order();
 #pragma unroll
-      for (int fn = 0; fn < G::FN; ++fn)
-        if (ok && r0 + fn * 16 < a.N) q[fn] = e.row(r0 + fn * 16, c);
-      f32x4_t sum[2] = {};
+      for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
-      for (int fn = 0; fn < G::FN; ++fn)
-        if (ok && r0 + fn * 16 < a.N)
-          e.template put<decltype(ACT)::value>(b, r0 + fn * 16, c, k, q[fn], acc[fm][fn], acc[fm + DU - 1][fn], sum);
-      if constexpr (E::NSUM > 0) {
-        if (e.sums) {
+        for (int j = 0; j < PR / 16; ++j)
+          *(f32x4_t *)(own + (j * 16 + (lane & 15)) * LD + fm % DU * WU + fm / DU * 16 + grp * 4) = acc[fm][h * PR / 16 + j];
+      wave_lds_order();
 #pragma unroll
-          for (int j = 0; j < E::NSUM; ++j) {
+      for (int i = 0; i < NI; ++i) {
+        const int r = r0 + h * PR + i * RPI;
+        if (ok && r < rows) {
+          float v[8], w[8];
+          const float *at = own + (i * RPI + lane / LPR) * LD + lane % LPR * 8;
+          load8(at, v);
+          if constexpr (DU == 2) load8(at + WU, w);
+          e.template put<decltype(ACT)::value>(r, c, k, q[i], v, w, sum);
+          if (h + 1 < G::WN / PR && r + PR < rows) q[i].load(e, r + PR, c);
+        }
+        __builtin_amdgcn_sched_barrier(0);                // one access's registers at a time
+      }
+    }
+    if constexpr (E::NSUM > 0) {
+      if (e.sums) {
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1)
+        for (int j = 0; j < E::NSUM; ++j) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sum[j][i] += __shfl_xor(sum[j][i], o, 64);
-            if (ok && (lane & 15) == 0) store4(e.sums + ((int64_t)(n * G::NWN + wn) * E::NSUM + j) * a.M + c, sum[j]);
-          }
+          for (int o = LPR; o < 64; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], o, 64);
+          if (ok && lane < LPR) keep8(e.sums + ((int64_t)(n * G::NWN + wn) * E::NSUM + j) * a.M + m0 + c, sum[j]);
         }
       }
     }
@@ -297,39 +407,72 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
 }
 
 // The epilogue over rows of partial sums, or of a matrix v (EpiDz): a workgroup takes 256 columns of a
-// strip of `strip` rows, thread t the 4 columns 4 (t % 64) of every fourth row. Its sums go to
-// sums[4 strip's number + t / 64].
+// strip of `strip` rows, thread t the 8 columns 8 (t % 32) of every eighth row. Its sums go to
+// sums[4 strip's number + t / 64], the two rows of a wave added.
 template <typename T, class E>
 __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ part, int S, int batch, const T *__restrict__ v,
                                                     int64_t ldv, int N, int M, int strip, E e) {
-  constexpr int DU = E::DUAL ? 2 : 1;
-  const int c = (blockIdx.x * 64 + (threadIdx.x & 63)) * 4, b = blockIdx.z, lane4 = threadIdx.x >> 6;
-  if (c >= M) return;
-  const int end = min(N, ((int)blockIdx.y + 1) * strip);
+  constexpr int DU = E::DUAL ? 2 : 1, UR = 4;             // rows in flight
+  const int m0 = blockIdx.x * 256, n0 = blockIdx.y * strip, b = blockIdx.z, c = (threadIdx.x & 31) * 8;
+  const bool ok = c < M - m0;
+  const int end = ok ? min(N - n0, strip) : 0;
   const int64_t plane = (int64_t)batch * N * M * DU;
+  e.shift(b, n0, m0);
+  if (part) part += ((int64_t)b * N + n0) * M * DU + m0;
+  else v += n0 * ldv + m0;
   epi_act(e, [&](auto ACT) __attribute__((always_inline)) {
-    const typename E::Col k = e.col(c);
-    f32x4_t sum[2] = {};
-    for (int r = blockIdx.y * strip + lane4; r < end; r += 4) {
-      const typename E::Row q = e.row(r, c);
-      f32x4_t a = {}, a2 = {};
-      if (part) {
-        const float *p = part + ((int64_t)b * N + r) * M * DU + c;
-#pragma unroll 8
+    typename E::Col k;
+    if (ok) e.col(c, k);
+    float sum[2][8] = {};
+    int r = threadIdx.x >> 5;
+    if (part) {
+      for (; r < end; r += 8) {
+        typename E::Row q;
+        q.load(e, r, c);
+        float x[8] = {}, x2[8] = {};
+        const float *p = part + (int64_t)r * M * DU + c;
+#pragma unroll 4
         for (int s = 0; s < S; ++s) {
-          a += load4(p + s * plane);
-          if constexpr (DU == 2) a2 += load4(p + s * plane + M);
+          float u[8];
+          load8(p + s * plane, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] += u[i];
+          if constexpr (DU == 2) {
+            load8(p + s * plane + M, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x2[i] += u[i];
+          }
         }
-      } else {
-        a = load4(v + r * ldv + c);
+        e.template put<decltype(ACT)::value>(r, c, k, q, x, x2, sum);
       }
-      e.template put<decltype(ACT)::value>(b, r, c, k, q, a, a2, sum);
+    } else {
+      for (; r < end; r += 8 * UR) {
+        typename E::Row q[UR];
+        Raw8<T> raw[UR];
+#pragma unroll
+        for (int i = 0; i < UR; ++i)
+          if (r + 8 * i < end) {
+            raw[i].load(v + (r + 8 * i) * ldv + c);
+            q[i].load(e, r + 8 * i, c);
+          }
+#pragma unroll
+        for (int i = 0; i < UR; ++i)
+          if (r + 8 * i < end) {
+            float x[8];
+            raw[i].to(x);
+            e.template put<decltype(ACT)::value>(r + 8 * i, c, k, q[i], x, x, sum);
+          }
+      }
     }
     if constexpr (E::NSUM > 0) {
       if (e.sums)
 #pragma unroll
-        for (int j = 0; j < E::NSUM; ++j)
-          store4(e.sums + ((int64_t)(blockIdx.y * 4 + lane4) * E::NSUM + j) * M + c, sum[j]);
+        for (int j = 0; j < E::NSUM; ++j) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], 32, 64);
+          if (ok && (threadIdx.x & 32) == 0)
+            keep8(e.sums + ((int64_t)(blockIdx.y * 4 + (threadIdx.x >> 6)) * E::NSUM + j) * M + m0 + c, sum[j]);
+        }
     }
   });
 }
@@ -445,7 +588,7 @@ int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 // Rows of a strip of k_dense_rows: for column sums few strips, whose sums are added afterwards.
 int strip_of(int N, bool sums) {
   const int64_t r = ceil_div(N, sums ? 64 : 1024);
-  return (int)(ceil_div(r, 4) * 4);
+  return (int)(ceil_div(r, 8) * 8);
 }
 int row_strips(int N, bool sums) { return (int)ceil_div(N, strip_of(N, sums)); }
 
@@ -517,12 +660,29 @@ hipError_t add_sums(const float *sums, int blocks, int M, int nsum, float *o0, f
   return hipGetLastError();
 }
 
-template <typename T> EpiLinear<T, false> store_epi(void *y, int64_t ldy) {
-  EpiLinear<T, false> e = {};
-  e.y = y;
+template <typename T> EpiLinear<T, T, false, false> store_epi(void *y, int64_t ldy) {
+  EpiLinear<T, T, false, false> e = {};
+  e.y = (T *)y;
   e.ldy = ldy;
-  e.y_bf16 = !std::is_same<T, float>::value;
   return e;
+}
+
+// f(epilogue) for y in its type, with or without a residual
+template <typename T, typename F>
+hipError_t with_linear(const float *bias, const void *res, int64_t ldr, void *y, int64_t ldy, int y_bf16, void *pre, int act, F &&f) {
+  auto go = [&](auto yt, auto with_res) {
+    typedef decltype(yt) YT;
+    EpiLinear<T, YT, true, decltype(with_res)::value> e = {};
+    e.bias = bias;
+    e.res = (const YT *)res; e.ldr = ldr;
+    e.y = (YT *)y; e.ldy = ldy;
+    e.pre = (T *)pre; e.act = act;
+    return f(e);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if (y_bf16) return res ? go(bf16_t(), yes) : go(bf16_t(), no);
+  return res ? go(float(), yes) : go(float(), no);
 }
 
 // Offsets of a workspace, in order.
@@ -562,14 +722,12 @@ LinearBackPlan linear_back_plan(int T, int K, int N, bool bf16, bool kn, int act
 
 template <typename T> hipError_t linear_fwd_run(const LinearArgs &a, hipStream_t s) {
   const Split p = split_of(!std::is_same<T, float>::value, a.kn ? kAcross : kAlong, false, a.N, a.T, a.K, 1);
-  EpiLinear<T, true> e = {};
-  e.bias = a.bias; e.res = a.res; e.ldr = a.ldr;
-  e.y = a.y; e.ldy = a.N; e.y_bf16 = a.y_bf16;
-  e.pre = (T *)a.pre; e.act = a.act;
   Prod q = prod_of(a.N, a.T, a.K);
   q.A[0] = a.w; q.lda[0] = a.kn ? a.N : a.K;
   q.B[0] = a.x; q.ldb = a.ldx;
-  return a.kn ? product<T, kAcross>(q, p, a.ws, e, s) : product<T, kAlong>(q, p, a.ws, e, s);
+  return with_linear<T>(a.bias, a.res, a.ldr, a.y, a.N, a.y_bf16, a.pre, a.act, [&](const auto &e) {
+    return a.kn ? product<T, kAcross>(q, p, a.ws, e, s) : product<T, kAlong>(q, p, a.ws, e, s);
+  });
 }
 
 template <typename T> hipError_t linear_bwd_run(const LinearBackArgs &a, hipStream_t s) {
@@ -661,13 +819,11 @@ template <typename T> hipError_t gated_fwd_run(const GatedArgs &a, hipStream_t s
   q.A[0] = a.wg; q.A2 = a.wu; q.lda[0] = a.d;
   q.B[0] = a.x; q.ldb = a.ldx;
   TW_TRY_HIP((product<T, kAlong>(q, p.up, ws + p.part, eu, s)));
-  EpiLinear<T, true> ed = {};
-  ed.res = a.res; ed.ldr = a.ldr;
-  ed.y = a.y; ed.ldy = a.d; ed.y_bf16 = a.y_bf16;
   q = prod_of(a.d, a.T, a.f);
   q.A[0] = a.w2; q.lda[0] = a.d;
   q.B[0] = eu.h; q.ldb = a.f;
-  return product<T, kAcross>(q, p.down, ws + p.part, ed, s);
+  return with_linear<T>(nullptr, a.res, a.ldr, a.y, a.d, a.y_bf16, nullptr, kActNone,
+                        [&](const auto &e) { return product<T, kAcross>(q, p.down, ws + p.part, e, s); });
 }
 
 template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream_t s) {
@@ -675,29 +831,37 @@ template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream
   const bool bias = a.dbg || a.dbu;
   const GatedBackPlan p = gated_back_plan(a.T, a.d, a.f, bf16, bias);
   char *ws = (char *)a.ws;
-  EpiGluBack<T> e = {};
-  e.g = (const T *)a.g; e.u = (const T *)a.u;
-  e.dg = (T *)(ws + p.dg); e.du = (T *)(ws + p.du); e.h = (T *)(ws + p.h);
-  e.ldy = a.f; e.act = a.act;
-  if (bias) e.sums = (float *)(ws + p.sums);
+  T *dg = (T *)(ws + p.dg), *du = (T *)(ws + p.du), *h = (T *)(ws + p.h);
   Prod q = prod_of(a.f, a.T, a.d);
   q.A[0] = a.w2; q.lda[0] = a.d;
   q.B[0] = a.dy; q.ldb = a.lddy;
-  TW_TRY_HIP((product<T, kAlong>(q, p.dh, ws + p.part, e, s)));
-  if (bias) TW_TRY_HIP(add_sums(e.sums, sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
+  auto back = [&](auto sums) {
+    EpiGluBack<T, decltype(sums)::value> e = {};
+    e.g = (const T *)a.g; e.u = (const T *)a.u;
+    e.dg = dg; e.du = du; e.h = h;
+    e.ldy = a.f; e.act = a.act;
+    if (bias) e.sums = (float *)(ws + p.sums);
+    return product<T, kAlong>(q, p.dh, ws + p.part, e, s);
+  };
+  if (bias) {
+    TW_TRY_HIP(back(std::true_type()));
+    TW_TRY_HIP(add_sums((const float *)(ws + p.sums), sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
+  } else {
+    TW_TRY_HIP(back(std::false_type()));
+  }
   q = prod_of(a.d, a.T, a.f);
   q.segs = 2;
   q.A[0] = a.wg; q.A[1] = a.wu; q.lda[0] = q.lda[1] = a.d;
-  q.B[0] = e.dg; q.B[1] = e.du; q.ldb = a.f;
+  q.B[0] = dg; q.B[1] = du; q.ldb = a.f;
   TW_TRY_HIP((product<T, kAcross>(q, p.dx, ws + p.part, store_epi<T>(a.dx, a.d), s)));
   q = prod_of(a.d, a.f, a.T);
   q.batch = 3;
   q.A[0] = q.A[1] = a.x; q.A[2] = a.dy;
   q.lda[0] = q.lda[1] = a.ldx; q.lda[2] = a.lddy;
-  q.B[0] = e.dg; q.B[1] = e.du; q.B[2] = e.h; q.ldb = a.f;
+  q.B[0] = dg; q.B[1] = du; q.B[2] = h; q.ldb = a.f;
   auto ew = store_epi<T>(a.dwg, a.d);
-  ew.y1 = a.dwu;
-  ew.y2 = a.dw2;
+  ew.y1 = (T *)a.dwu;
+  ew.y2 = (T *)a.dw2;
   return product<T, kBoth>(q, p.dw, ws + p.part, ew, s);
 }
 
