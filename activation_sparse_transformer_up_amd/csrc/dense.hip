@@ -308,7 +308,6 @@ template <class G> struct AsMMF : G {
 template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_dense(Prod a, E e) {
   constexpr int DU = E::DUAL ? 2 : 1, BU = G::BM / DU, WU = G::WM / DU;       // columns of a tile, of a wave
   constexpr int LD = G::WM + 4;                           // floats from row to row in LDS
-  static_assert(G::FN % 2 == 0 && G::NW * 32 * LD * 4 <= G::SMEM, "turning");
   __shared__ __attribute__((aligned(16))) char smem[G::SMEM];
   const int mt = (a.M + BU - 1) / BU, nt = (a.N + G::BN - 1) / G::BN;
   const int t = mm_xcd_tile(blockIdx.x, mt * nt * a.S * a.batch);
@@ -351,12 +350,13 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
   }
   // rows of a pass, lanes per row, rows per access, accesses; 16 rows where the inputs of 32 would not stay in
   // registers beside the accumulators
-  constexpr int PR = WU == 128 && sizeof(typename E::Row) > 16 ? 16 : 32, LPR = WU / 8, RPI = 64 / LPR, NI = PR / RPI;
-  static_assert(LPR * RPI == 64 && NI * RPI == PR, "turning");
+  constexpr int PR = G::WN == 16 || (WU == 128 && sizeof(typename E::Row) > 16) ? 16 : 32;
+  constexpr int LPR = WU / 8, RPI = 64 / LPR < PR ? 64 / LPR : PR, NI = PR / RPI;
+  static_assert(LPR <= 64 && NI * RPI == PR && G::WN % PR == 0 && G::NW * PR * LD * 4 <= G::SMEM, "turning");
   e.shift(b, n0, m0);
   const int c = wm * WU + lane % LPR * 8, r0 = wn * G::WN + lane / LPR, rows = a.N - n0;      // of the tile
   float *own = (float *)smem + wave * PR * LD;            // this wave's rows
-  const bool ok = c < a.M - m0;
+  const bool ok = c < a.M - m0 && lane < LPR * RPI;
   typename E::Col k;
   typename E::Row q[NI];
   if (ok) {
@@ -396,7 +396,7 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
 #pragma unroll
         for (int j = 0; j < E::NSUM; ++j) {
 #pragma unroll
-          for (int o = LPR; o < 64; o <<= 1)
+          for (int o = LPR; o < LPR * RPI; o <<= 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], o, 64);
           if (ok && lane < LPR) keep8(e.sums + ((int64_t)(n * G::NWN + wn) * E::NSUM + j) * a.M + m0 + c, sum[j]);
@@ -477,22 +477,25 @@ __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ pa
   });
 }
 
-// out_j[c] = sum over blocks of sums[block][j][c]: a workgroup takes 64 columns, each wave every fourth
-// block.
+// out_j[c] = sum over blocks of sums[block][j][c]: a workgroup takes 64 columns, thread t the 4 columns 4 (t % 16)
+// of every sixteenth block.
 __global__ __launch_bounds__(256) void k_dense_sums(const float *__restrict__ sums, int blocks, int M, int nsum,
                                                     float *__restrict__ out0, float *__restrict__ out1) {
-  __shared__ float red[4][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6, j = blockIdx.y;
-  float v = 0.f;
-  if (c < M)
-#pragma unroll 4
-    for (int i = w; i < blocks; i += 4) v += sums[((int64_t)i * nsum + j) * M + c];
-  red[w][threadIdx.x & 63] = v;
+  __shared__ float red[16][64];
+  const int c = (threadIdx.x & 15) * 4, at = blockIdx.x * 64 + c, w = threadIdx.x >> 4, j = blockIdx.y;
+  f32x4_t v = {};
+  if (at < M)                                             // M is a multiple of 8
+#pragma unroll 8
+    for (int i = w; i < blocks; i += 16) v += *(const f32x4_t *)(sums + ((int64_t)i * nsum + j) * M + at);
+  *(f32x4_t *)&red[w][c] = v;
   __syncthreads();
   float *out = j ? out1 : out0;
-  if (w == 0 && c < M && out) {
-    const int l = threadIdx.x;
-    out[c] = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
+  const int t = threadIdx.x, o = blockIdx.x * 64 + t;
+  if (t < 64 && o < M && out) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[i][t];
+    out[o] = s;
   }
 }
 
@@ -502,16 +505,23 @@ __global__ __launch_bounds__(256) void k_dense_zero(uint4 *__restrict__ p, size_
 
 // -------------------------------------------------------------------------------------- plan
 
-// Kinds of products, and the tiles of each.
+// Kinds of products, and the tiles of each. Large tiles have the least traffic per operation, one workgroup
+// of 8 waves per CU; the others are for products that large tiles would leave CUs idle in. Few rows make a
+// product a stream of its weights, which needs many loads in flight per CU more than anything: the narrow
+// tiles' rings keep 28 KB of weights per workgroup in flight (two per CU along k), the deep ones' 80 KB.
 enum { kAlong, kAcross, kBoth };            // both operands along k; A across; both across
-enum { kSmall, kMid, kLarge, kStream };
+enum { kSmall, kMid, kLarge, kNarrow, kDeep };
 template <int KIND, int C, bool DUAL> struct Shape;
 template <bool D> struct Shape<kAlong, kSmall, D> { typedef AsMM64<MM64<64, 64, 32, 32, 4, 4, D>> G; };
 template <bool D> struct Shape<kAlong, kMid, D> { typedef AsMM64<MM64<128, 128, 64, 64, 3, 2, D>> G; };
 template <bool D> struct Shape<kAlong, kLarge, D> { typedef AsMM64<MM64<256, 256, 128, 64, 3, 2, D>> G; };
-template <bool D> struct Shape<kAlong, kStream, D> { typedef AsMM64<MM64<128, 32, 32, 32, 4, 4, D>> G; };
+template <> struct Shape<kAlong, kNarrow, false> { typedef AsMM64<MM64<32, 32, 16, 16, 8, 8>> G; };
+template <> struct Shape<kAlong, kNarrow, true> { typedef AsMM64<MM64<64, 32, 32, 16, 6, 6, true>> G; };
 template <> struct Shape<kAcross, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, false>> G; };
+template <> struct Shape<kAcross, kMid, false> { typedef AsMM<MM<256, 128, 64, 64, 6, true, false>> G; };
 template <> struct Shape<kAcross, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, false>> G; };
+template <> struct Shape<kAcross, kNarrow, false> { typedef AsMM<MM<64, 64, 64, 16, 8, true, false>> G; };
+template <> struct Shape<kAcross, kDeep, false> { typedef AsMM<MM<256, 64, 64, 64, 6, true, false>> G; };
 template <> struct Shape<kBoth, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, true>> G; };
 template <> struct Shape<kBoth, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, true>> G; };
 template <int KIND, bool DUAL> struct ShapeF {            // fp32 as it is
@@ -522,26 +532,34 @@ template <bool DUAL> struct ShapeFew { typedef AsMMF<MMF<128, 32, false, false, 
 constexpr int kCUs = 256;
 constexpr int64_t kPartBytes = (int64_t)256 << 20;        // partial sums of one product
 struct Tile { int m, n, wn; };              // columns, rows, rows of a wave
-Tile tile_of(bool bf16, int kind, int c) {
-  if (!bf16) return c == kStream ? Tile{128, 32, 32} : Tile{64, 64, 32};
+Tile tile_of(bool bf16, int kind, int c, bool dual) {
+  if (!bf16) return c == kNarrow ? Tile{128, 32, 32} : Tile{64, 64, 32};
   if (kind == kAlong)
-    return c == kSmall ? Tile{64, 64, 32} : c == kMid ? Tile{128, 128, 64} : c == kLarge ? Tile{256, 256, 64} : Tile{128, 32, 32};
-  return c == kSmall ? Tile{256, 64, 64} : Tile{256, 256, 128};
+    return c == kSmall ? Tile{64, 64, 32} : c == kMid ? Tile{128, 128, 64} : c == kLarge ? Tile{256, 256, 64}
+                                                                                      : Tile{dual ? 64 : 32, 32, 16};
+  return c == kLarge ? Tile{256, 256, 128} : c == kMid ? Tile{256, 128, 64} : c == kNarrow ? Tile{64, 64, 16} : Tile{256, 64, 64};
 }
 
 // Nanoseconds of `tiles` tiles over `stages` stages: rounds of resident workgroups, each with its stages (all
-// workgroups of a CU together) and its start and epilogue.
+// workgroups of a CU together; `alone` where at most half the places are taken) and its start and epilogue. Measured
+// with every tile and split forced (us, x w of T x K by N; along k small / mid / large, across it small / mid /
+// large, one split): 1000 x 2048 by 8192: 54 / 34 / 42, 45 / 36 / 44; 4096 x 2048 by 8192: 202 / 128 / 109, 171 / 141 /
+// 106; 2048 x 4096 by 4096 across: 87 / 65 / 79; 1000 x 8192 by 2048 in four splits: 60 / 43 / 55, 60 / 46 / 57. Few rows
+// (small / narrow): 1 x 4096 by 14336 along k 26.2 / 23.3, 64 rows 28.4 / 40; across it, 64 x 14336 by 4096 in 256
+// workgroups: small 38, narrow 37, deep 31; one row small 34, narrow 25, deep 26.
 struct Cost {
-  int per_cu, stage, alone, start;          // alone: a stage where no CU has two workgroups
+  int per_cu, stage, alone, start;
 };
-constexpr Cost kCostAlong[4] = {{2, 450, 450, 2500}, {2, 1000, 750, 4000}, {1, 1450, 1450, 9000}, {2, 450, 450, 2500}};
-constexpr Cost kCostAcross[3] = {{2, 750, 700, 4500}, {}, {1, 850, 850, 10000}};
+constexpr Cost kCostAlong[4] = {{2, 330, 210, 2000}, {2, 840, 460, 4000}, {1, 1400, 1080, 8000}, {2, 270, 160, 1500}};     // 64-k stages
+constexpr Cost kCostAcross[3] = {{2, 600, 590, 4500}, {1, 460, 390, 5000}, {1, 740, 530, 8000}};                        // 32-k stages
+constexpr Cost kCostBoth[3] = {{2, 680, 620, 3500}, {}, {1, 740, 540, 8000}};
 constexpr Cost kCostF = {2, 1050, 550, 3000};
-constexpr int kJoin = 3000;                 // the launch that adds partial sums
+constexpr int kJoin = 5000;                 // the launch that adds partial sums
+constexpr double kStream = 5500;            // bytes per nanosecond from HBM
 int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
-  if (tiles <= kCUs) return stages * c.alone + c.start;
-  const int64_t slots = kCUs * c.per_cu;
-  return (tiles + slots - 1) / slots * (stages * c.stage + c.start);
+  const int64_t slots = kCUs * c.per_cu, left = tiles % slots, over = left * 2 > slots ? left * 2 - slots : 0;
+  return tiles / slots * (stages * c.stage + c.start) +
+         (left ? stages * (c.alone + (c.stage - c.alone) * over / slots) + c.start : 0);
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -555,30 +573,40 @@ Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batc
   const int du = dual ? 2 : 1, ks = kind == kAlong && bf16 ? 64 : 32;
   Split best = {};
   int64_t least = 0;
+  const int64_t stream = (int64_t)((double)((int64_t)M * du + N) * (double)K * batch * (bf16 ? 2 : 4) / kStream);
   auto consider = [&](int c, const Cost &cost) {
-    const Tile t = tile_of(bf16, kind, c);
+    const Tile t = tile_of(bf16, kind, c, dual);
     const int64_t tiles = ceil_div((int64_t)M * du, t.m) * ceil_div(N, t.n) * batch;
     for (int S0 = 1; S0 <= 64; S0 *= 2) {
       const int64_t size = ceil_div(ceil_div(K, S0), 64) * 64, S = ceil_div(K, size);
       const int64_t part = S > 1 ? S * batch * N * M * du * 4 : 0;
       if (S0 > 1 && (tiles * S > kCUs * cost.per_cu || part > kPartBytes || S < S0)) break;
-      const int64_t n = cost_of(cost, tiles * S, ceil_div(size, ks)) + (S > 1 ? kJoin + part * 2 / 5000 : 0);
-      if (least && n * 20 >= least * 19) continue;        // near ties go to the larger tile and fewer splits
+      int64_t n = cost_of(cost, tiles * S, ceil_div(size, ks));
+      n = (n > stream ? n : stream) + (S > 1 ? kJoin + part / 5000 : 0);
+      if (least && n * 20 >= least * 19) continue;        // near ties go to the earlier tile and fewer splits
       least = n;
       best = {c, (int)S, (int)size, align256((size_t)part)};
     }
   };
   if (!bf16) {
     consider(kSmall, kCostF);
-    if (kind == kAlong && N <= 32) consider(kStream, kCostF);
+    if (kind == kAlong && N <= 32) consider(kNarrow, kCostF);
   } else if (kind == kAlong) {
+    if (N <= 64) consider(kNarrow, kCostAlong[kNarrow]);
     consider(kLarge, kCostAlong[kLarge]);
     consider(kMid, kCostAlong[kMid]);
     consider(kSmall, kCostAlong[kSmall]);
-    if (N <= 32 && ceil_div((int64_t)M * du, 128) > kCUs) consider(kStream, kCostAlong[kStream]);
-  } else {
+  } else if (kind == kAcross && N <= 64) {
+    const int rows = N;                     // the rows' share of a stage
+    consider(kNarrow, {1, 165 + rows * 7 / 5, 165 + rows * 7 / 5, 1500});
+    consider(kDeep, {1, 680 + rows * 9 / 4, 680 + rows * 9 / 4, 2500});
+  } else if (kind == kAcross) {
     consider(kLarge, kCostAcross[kLarge]);
+    consider(kMid, kCostAcross[kMid]);
     consider(kSmall, kCostAcross[kSmall]);
+  } else {
+    consider(kLarge, kCostBoth[kLarge]);
+    consider(kSmall, kCostBoth[kSmall]);
   }
   return best;
 }
@@ -595,7 +623,7 @@ int row_strips(int N, bool sums) { return (int)ceil_div(N, strip_of(N, sums)); }
 // Blocks of column sums that a product's epilogue leaves.
 int sum_blocks(bool bf16, int kind, const Split &p, int N) {
   if (p.S > 1) return 4 * row_strips(N, true);
-  const Tile t = tile_of(bf16, kind, p.cls);
+  const Tile t = tile_of(bf16, kind, p.cls, false);
   return (int)(ceil_div(N, t.n) * (t.n / t.wn));
 }
 
@@ -623,7 +651,7 @@ hipError_t product(Prod a, const Split &p, void *ws, const E &e, hipStream_t s) 
   constexpr bool D = E::DUAL;
   if constexpr (std::is_same<T, float>::value) {
     if constexpr (KIND == kAlong) {
-      if (p.cls == kStream) TW_TRY_HIP(go(ShapeFew<D>()));
+      if (p.cls == kNarrow) TW_TRY_HIP(go(ShapeFew<D>()));
       else TW_TRY_HIP(go(ShapeF<KIND, D>()));
     } else {
       TW_TRY_HIP(go(ShapeF<KIND, D>()));
@@ -633,11 +661,16 @@ hipError_t product(Prod a, const Split &p, void *ws, const E &e, hipStream_t s) 
       case kSmall: TW_TRY_HIP(go(Shape<KIND, kSmall, D>())); break;
       case kMid: TW_TRY_HIP(go(Shape<KIND, kMid, D>())); break;
       case kLarge: TW_TRY_HIP(go(Shape<KIND, kLarge, D>())); break;
-      default: TW_TRY_HIP(go(Shape<KIND, kStream, D>())); break;
+      default: TW_TRY_HIP(go(Shape<KIND, kNarrow, D>())); break;
     }
   } else {
     if (p.cls == kSmall) TW_TRY_HIP(go(Shape<KIND, kSmall, D>()));
-    else TW_TRY_HIP(go(Shape<KIND, kLarge, D>()));
+    else if (p.cls == kLarge) TW_TRY_HIP(go(Shape<KIND, kLarge, D>()));
+    if constexpr (KIND == kAcross) {
+      if (p.cls == kNarrow) TW_TRY_HIP(go(Shape<KIND, kNarrow, D>()));
+      else if (p.cls == kDeep) TW_TRY_HIP(go(Shape<KIND, kDeep, D>()));
+      else if (p.cls == kMid) TW_TRY_HIP(go(Shape<KIND, kMid, D>()));
+    }
   }
   return p.S > 1 ? launch_rows<T, E>(a, nullptr, 0, e, s) : hipSuccess;
 }

@@ -41,6 +41,12 @@ template <int BX> struct MmTr {
   static TW_DEV int swz(int j) { return BX == 256 ? j & 1 : (j >> 1) & 1; }
 };
 
+// Bytes from 1 KB block to 1 KB block of an operand in the stage.
+template <int BX, bool TR> constexpr int mm_step() {
+  if constexpr (TR) return MmTr<BX>::BLK;
+  else return 1024;
+}
+
 template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> struct MM {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr bool ATR = ATR_, BTR = BTR_;
@@ -49,7 +55,7 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ATR_, bool BTR_> str
   static constexpr int KS = 32;                           // k per stage
   static constexpr int A_BLK = BM * KS * 2 / 1024, B_BLK = BN * KS * 2 / 1024;      // 1 KB blocks of a stage
   static constexpr int LPW = (A_BLK + B_BLK) / NW;        // 1 KB wave-loads per wave and stage
-  static constexpr int A_STEP = ATR ? MmTr<BM>::BLK : 1024, B_STEP = BTR ? MmTr<BN>::BLK : 1024;
+  static constexpr int A_STEP = mm_step<BM, ATR>(), B_STEP = mm_step<BN, BTR>();
   static constexpr int A_BYTES = A_BLK * A_STEP;
   static constexpr int STAGE = A_BYTES + B_BLK * B_STEP, SMEM = NS * STAGE;
   static_assert((A_BLK + B_BLK) % NW == 0 && NS >= 3, "tile");
