@@ -525,7 +525,7 @@ template <> struct Shape<kAcross, kDeep, false> { typedef AsMM<MM<256, 64, 64, 6
 template <> struct Shape<kBoth, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, true>> G; };
 template <> struct Shape<kBoth, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, true>> G; };
 template <int KIND, bool DUAL> struct ShapeF {            // fp32 as it is
-  typedef AsMMF<MMF<64, 64, KIND != kAlong, KIND == kBoth, DUAL>> G;
+  typedef AsMMF<MMF<64, 64, KIND != kAlong, KIND == kBoth, DUAL, 3>> G;
 };
 template <bool DUAL> struct ShapeFew { typedef AsMMF<MMF<128, 32, false, false, DUAL>> G; };
 

@@ -410,8 +410,8 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
 // four j in one load. In LDS, without bank conflicts:
 //   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
 //   across k:  k row j at 256 j, its 64-byte chunk c at c ^ ((j >> 2) & 3)
-template <int BM_, int BN_, bool ATR_, bool BTR_, bool DUAL_ = false> struct MMF {
-  static constexpr int BM = BM_, BN = BN_, WM = 32, WN = 32, NS = 4;
+template <int BM_, int BN_, bool ATR_, bool BTR_, bool DUAL_ = false, int NS_ = 4> struct MMF {
+  static constexpr int BM = BM_, BN = BN_, WM = 32, WN = 32, NS = NS_;
   static constexpr bool ATR = ATR_, BTR = BTR_, DUAL = DUAL_;
   static constexpr int NWM = BM / WM, NWN = BN / WN, NW = 4, NT = 256, FM = 2, FN = 2;
   static constexpr int LA = BM / 32, LB = BN / 32, NL = LA + LB;      // 1 KB wave-loads per wave and stage
