@@ -249,7 +249,7 @@ template <class E, typename F> TW_DEV void epi_act(const E &e, F &&f) {
 // B[s] for segments; one of batch and segs is 1), k split S times in ranges of ks of the segs * K.
 struct Prod {
   const void *A[3], *B[3], *A2;             // A2: the second matrix of a dual A
-  int64_t lda[3], ldb;
+  int64_t lda[3], ldb, planeA, planeB;      // elements between the planes of split fp32 operands
   int M, N, K, batch, segs, S, ks;
   float *part;                              // [S][batch][N][M], dual [..][2 M] (S > 1)
 };
@@ -269,26 +269,30 @@ TW_DEV void operands(const Prod &a, int b, int m0, int n0, int k0, OP &A, OP &B)
   A.ld = lda;
   A.n = min(a.M - m0, G::BM / dual);
   if (G::DUAL) A.p2 = (const T *)a.A2 + ao;
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    A.plane = a.planeA;
+    B.plane = a.planeB;
+  }
   B.p = (const T *)pick(a.B, b) + bo;
   B.ld = a.ldb;
   B.n = min(a.N - n0, G::BN);
 }
 
-// What mm.h's three tile types have in common, by loop.
-template <class G> struct AsMM : G {
+// What mm.h's three tile types have in common, by loop; NP: products of planes.
+template <class G, int NP = 1> struct AsMM : G {
   static constexpr bool DUAL = false;
   template <typename ACC> static TW_DEV void mul(const Prod &a, int b, int m0, int n0, int k0, int K, ACC &acc, char *smem) {
     MmOperand A, B;
     operands<AsMM, MmOperand, bf16_t>(a, b, m0, n0, k0, A, B);
-    mm_loop<G, 1>(A, B, K, acc, smem);
+    mm_loop<G, NP>(A, B, K, acc, smem);
   }
 };
-template <class G> struct AsMM64 : G {
+template <class G, int NP = 1> struct AsMM64 : G {
   static constexpr bool ATR = false, BTR = false;
   template <typename ACC> static TW_DEV void mul(const Prod &a, int b, int m0, int n0, int k0, int K, ACC &acc, char *smem) {
     MmOperand A, B;
     operands<AsMM64, MmOperand, bf16_t>(a, b, m0, n0, k0, A, B);
-    mm_loop64<G, 1>(A, B, K, acc, smem);
+    mm_loop64<G, NP>(A, B, K, acc, smem);
   }
 };
 template <class G> struct AsMMF : G {
@@ -503,6 +507,18 @@ __global__ __launch_bounds__(256) void k_dense_zero(uint4 *__restrict__ p, size_
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = make_uint4(0, 0, 0, 0);
 }
 
+// The three planes of a [rows][cols] fp32 operand (cols a multiple of 8), each [rows][cols].
+__global__ __launch_bounds__(256) void k_dense_split(const float *__restrict__ x, int64_t ld, int rows, int cols,
+                                                     bf16_t *__restrict__ to, int64_t plane) {
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
+  if (c >= cols) return;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float v[8];
+    load8(x + r * ld + c, v);
+    split8(v, to + (int64_t)r * cols + c, plane);
+  }
+}
+
 // -------------------------------------------------------------------------------------- plan
 
 // Kinds of products, and the tiles of each. Large tiles have the least traffic per operation, one workgroup
@@ -511,19 +527,19 @@ __global__ __launch_bounds__(256) void k_dense_zero(uint4 *__restrict__ p, size_
 // tiles' rings keep 28 KB of weights per workgroup in flight (two per CU along k), the deep ones' 80 KB.
 enum { kAlong, kAcross, kBoth };            // both operands along k; A across; both across
 enum { kSmall, kMid, kLarge, kNarrow, kDeep };
-template <int KIND, int C, bool DUAL> struct Shape;
+template <int KIND, int C, bool DUAL, int NP = 1> struct Shape;
 template <bool D> struct Shape<kAlong, kSmall, D> { typedef AsMM64<MM64<64, 64, 32, 32, 4, 4, D>> G; };
-template <bool D> struct Shape<kAlong, kMid, D> { typedef AsMM64<MM64<128, 128, 64, 64, 3, 2, D>> G; };
-template <bool D> struct Shape<kAlong, kLarge, D> { typedef AsMM64<MM64<256, 256, 128, 64, 3, 2, D>> G; };
+template <bool D, int NP> struct Shape<kAlong, kMid, D, NP> { typedef AsMM64<MM64<128, 128, 64, 64, 3, 2, D>, NP> G; };
+template <bool D, int NP> struct Shape<kAlong, kLarge, D, NP> { typedef AsMM64<MM64<256, 256, 128, 64, 3, 2, D>, NP> G; };
 template <> struct Shape<kAlong, kNarrow, false> { typedef AsMM64<MM64<32, 32, 16, 16, 8, 8>> G; };
 template <> struct Shape<kAlong, kNarrow, true> { typedef AsMM64<MM64<64, 32, 32, 16, 6, 6, true>> G; };
 template <> struct Shape<kAcross, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, false>> G; };
-template <> struct Shape<kAcross, kMid, false> { typedef AsMM<MM<256, 128, 64, 64, 6, true, false>> G; };
-template <> struct Shape<kAcross, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, false>> G; };
+template <int NP> struct Shape<kAcross, kMid, false, NP> { typedef AsMM<MM<256, 128, 64, 64, 6, true, false>, NP> G; };
+template <int NP> struct Shape<kAcross, kLarge, false, NP> { typedef AsMM<MM<256, 256, 64, 128, 4, true, false>, NP> G; };
 template <> struct Shape<kAcross, kNarrow, false> { typedef AsMM<MM<64, 64, 64, 16, 8, true, false>> G; };
 template <> struct Shape<kAcross, kDeep, false> { typedef AsMM<MM<256, 64, 64, 64, 6, true, false>> G; };
 template <> struct Shape<kBoth, kSmall, false> { typedef AsMM<MM<256, 64, 64, 64, 3, true, true>> G; };
-template <> struct Shape<kBoth, kLarge, false> { typedef AsMM<MM<256, 256, 64, 128, 4, true, true>> G; };
+template <int NP> struct Shape<kBoth, kLarge, false, NP> { typedef AsMM<MM<256, 256, 64, 128, 4, true, true>, NP> G; };
 template <int KIND, bool DUAL> struct ShapeF {            // fp32 as it is
   typedef AsMMF<MMF<64, 64, KIND != kAlong, KIND == kBoth, DUAL, 3>> G;
 };
@@ -532,8 +548,8 @@ template <bool DUAL> struct ShapeFew { typedef AsMMF<MMF<128, 32, false, false, 
 constexpr int kCUs = 256;
 constexpr int64_t kPartBytes = (int64_t)256 << 20;        // partial sums of one product
 struct Tile { int m, n, wn; };              // columns, rows, rows of a wave
-Tile tile_of(bool bf16, int kind, int c, bool dual) {
-  if (!bf16) return c == kNarrow ? Tile{128, 32, 32} : Tile{64, 64, 32};
+Tile tile_of(bool wide, int kind, int c, bool dual) {      // wide: bf16 operands or planes
+  if (!wide) return c == kNarrow ? Tile{128, 32, 32} : Tile{64, 64, 32};
   if (kind == kAlong)
     return c == kSmall ? Tile{64, 64, 32} : c == kMid ? Tile{128, 128, 64} : c == kLarge ? Tile{256, 256, 64}
                                                                                       : Tile{dual ? 64 : 32, 32, 16};
@@ -553,44 +569,59 @@ struct Cost {
 constexpr Cost kCostAlong[4] = {{2, 330, 210, 2000}, {2, 840, 460, 4000}, {1, 1400, 1080, 8000}, {2, 270, 160, 1500}};     // 64-k stages
 constexpr Cost kCostAcross[3] = {{2, 600, 590, 4500}, {1, 460, 390, 5000}, {1, 740, 530, 8000}};                        // 32-k stages
 constexpr Cost kCostBoth[3] = {{2, 680, 620, 3500}, {}, {1, 740, 540, 8000}};
-constexpr Cost kCostF = {2, 1050, 550, 3000};
-constexpr int kJoin = 5000;                 // the launch that adds partial sums
+constexpr Cost kCostF = {1, 500, 550, 2000};                                        // fp32 as it is: 32-k stages
+constexpr int kJoin = 6000;                 // the launch that adds partial sums, the host's part among it
 constexpr double kStream = 5500;            // bytes per nanosecond from HBM
 int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
-  const int64_t slots = kCUs * c.per_cu, left = tiles % slots, over = left * 2 > slots ? left * 2 - slots : 0;
+  const int64_t slots = kCUs * c.per_cu, left = tiles % slots;
+  double more = left * 2 > slots ? (double)(left * 2 - slots) / slots : 0.0;
+  if (c.per_cu > 1 && more > 0.0) more = 0.75 + 0.25 * more;          // some CUs have two: the others wait for them
   return tiles / slots * (stages * c.stage + c.start) +
-         (left ? stages * (c.alone + (c.stage - c.alone) * over / slots) + c.start : 0);
+         (left ? (int64_t)(stages * (c.alone + (c.stage - c.alone) * more)) + c.start : 0);
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Split {
   int cls, S, ks;
-  size_t part;                              // bytes of the partial sums
+  bool planes;                              // fp32 operands split into bf16 planes
+  size_t part, ws;                          // bytes of the partial sums, and with them of the planes
 };
-// The tile and the split of k (1, 2, 4 .. 64 times) of a product with the least cost. M columns (of each
+// The tile and the split of k (1 to 64 times) of a product with the least cost. M columns (of each
 // matrix of a dual A), K over all segments.
 Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batch) {
-  const int du = dual ? 2 : 1, ks = kind == kAlong && bf16 ? 64 : 32;
+  const int du = dual ? 2 : 1;
   Split best = {};
   int64_t least = 0;
-  const int64_t stream = (int64_t)((double)((int64_t)M * du + N) * (double)K * batch * (bf16 ? 2 : 4) / kStream);
-  auto consider = [&](int c, const Cost &cost) {
-    const Tile t = tile_of(bf16, kind, c, dual);
+  const int64_t elements = ((int64_t)M * du + N) * K * batch;
+  const int64_t stream = (int64_t)((double)elements * (bf16 ? 2 : 4) / kStream);
+  // np: products of planes; more: the launches that make them
+  auto consider = [&](int c, const Cost &cost, int np = 1, int64_t more = 0) {
+    const bool wide = bf16 || np > 1;
+    const Tile t = tile_of(wide, kind, c, dual);
+    const int ks = kind == kAlong && wide ? 64 : 32;
     const int64_t tiles = ceil_div((int64_t)M * du, t.m) * ceil_div(N, t.n) * batch;
-    for (int S0 = 1; S0 <= 64; S0 *= 2) {
+    for (int S0 = 1; S0 <= 64; S0 += S0 < 8 ? 1 : S0 / 8 * 2) {
       const int64_t size = ceil_div(ceil_div(K, S0), 64) * 64, S = ceil_div(K, size);
       const int64_t part = S > 1 ? S * batch * N * M * du * 4 : 0;
-      if (S0 > 1 && (tiles * S > kCUs * cost.per_cu || part > kPartBytes || S < S0)) break;
-      int64_t n = cost_of(cost, tiles * S, ceil_div(size, ks));
-      n = (n > stream ? n : stream) + (S > 1 ? kJoin + part / 5000 : 0);
-      if (least && n * 20 >= least * 19) continue;        // near ties go to the earlier tile and fewer splits
+      if (S0 > 1 && (tiles * S > kCUs * cost.per_cu || part > kPartBytes)) break;
+      if (S < S0) continue;
+      int64_t n = cost_of(cost, tiles * S, ceil_div(size, ks) * np);
+      n = (n > stream ? n : stream) + (S > 1 ? kJoin + part / 5000 : 0) + more;
+      if (least && n * 100 >= least * 97) continue;       // near ties go to the earlier tile and fewer splits
       least = n;
-      best = {c, (int)S, (int)size, align256((size_t)part)};
+      best = {c, (int)S, (int)size, np > 1, align256((size_t)part), 0};
     }
   };
   if (!bf16) {
     consider(kSmall, kCostF);
     if (kind == kAlong && N <= 32) consider(kNarrow, kCostF);
+    // planes: six products of twice the bytes, 10 bytes moved per element before them
+    if (N > 128) {
+      const int64_t more = 16000 + elements * 10 / 5000;
+      const Cost *const cost = kind == kAlong ? kCostAlong : kind == kAcross ? kCostAcross : kCostBoth;
+      consider(kLarge, cost[kLarge], 6, more);
+      if (kind != kBoth) consider(kMid, cost[kMid], 6, more);
+    }
   } else if (kind == kAlong) {
     if (N <= 64) consider(kNarrow, kCostAlong[kNarrow]);
     consider(kLarge, kCostAlong[kLarge]);
@@ -608,6 +639,7 @@ Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batc
     consider(kLarge, kCostBoth[kLarge]);
     consider(kSmall, kCostBoth[kSmall]);
   }
+  best.ws = best.part + (best.planes ? align256((size_t)elements * 6) + 2048 : 0);
   return best;
 }
 
@@ -623,7 +655,7 @@ int row_strips(int N, bool sums) { return (int)ceil_div(N, strip_of(N, sums)); }
 // Blocks of column sums that a product's epilogue leaves.
 int sum_blocks(bool bf16, int kind, const Split &p, int N) {
   if (p.S > 1) return 4 * row_strips(N, true);
-  const Tile t = tile_of(bf16, kind, p.cls, false);
+  const Tile t = tile_of(bf16 || p.planes, kind, p.cls, false);
   return (int)(ceil_div(N, t.n) * (t.n / t.wn));
 }
 
@@ -635,7 +667,7 @@ hipError_t launch_rows(const Prod &a, const T *v, int64_t ldv, const E &e, hipSt
   return hipGetLastError();
 }
 
-// One product (a's shape and operands set) by plan p; ws: room for p.part bytes.
+// One product (a's shape and operands set) by plan p; ws: room for p.ws bytes.
 template <typename T, int KIND, class E>
 hipError_t product(Prod a, const Split &p, void *ws, const E &e, hipStream_t s) {
   a.S = p.S;
@@ -650,7 +682,38 @@ hipError_t product(Prod a, const Split &p, void *ws, const E &e, hipStream_t s) 
   };
   constexpr bool D = E::DUAL;
   if constexpr (std::is_same<T, float>::value) {
-    if constexpr (KIND == kAlong) {
+    if (p.planes) {
+      // every operand once: [3][rows][columns], 256-byte aligned
+      bf16_t *at = (bf16_t *)((char *)ws + p.part);
+      const int n = a.batch * a.segs;                     // operands on each side
+      const void *from[7];
+      int64_t stride[7];
+      bf16_t *to[7];
+      int made = 0;
+      auto planes = [&](const void *src, int rows, int cols, int64_t ld) -> const void * {
+        for (int i = 0; i < made; ++i)
+          if (from[i] == src && stride[i] == ld) return to[i];
+        from[made] = src;
+        stride[made] = ld;
+        to[made] = at;
+        k_dense_split<<<dim3((unsigned)ceil_div(cols, 2048), (unsigned)(rows < 4096 ? rows : 4096)), 256, 0, s>>>(
+            (const float *)src, ld, rows, cols, at, (int64_t)rows * cols);
+        at += align256((size_t)rows * cols * 6) / 2;
+        return to[made++];
+      };
+      constexpr bool AT = KIND != kAlong, BT = KIND == kBoth;
+      for (int i = 0; i < n; ++i) a.A[i] = planes(a.A[i], AT ? a.K : a.M, AT ? a.M : a.K, a.lda[i]);
+      if (D) a.A2 = planes(a.A2, a.M, a.K, a.lda[0]);
+      made = 0;                                           // B's may be A's, in another shape
+      for (int i = 0; i < n; ++i) a.B[i] = planes(a.B[i], BT ? a.K : a.N, BT ? a.N : a.K, a.ldb);
+      TW_TRY_HIP(hipGetLastError());
+      a.lda[0] = a.lda[1] = a.lda[2] = AT ? a.M : a.K;
+      a.ldb = BT ? a.N : a.K;
+      a.planeA = (int64_t)a.M * a.K;
+      a.planeB = (int64_t)a.N * a.K;
+      if (p.cls == kLarge) TW_TRY_HIP(go(Shape<KIND, kLarge, D, 6>()));
+      else if constexpr (KIND != kBoth) TW_TRY_HIP(go(Shape<KIND, kMid, D, 6>()));
+    } else if constexpr (KIND == kAlong) {
       if (p.cls == kNarrow) TW_TRY_HIP(go(ShapeFew<D>()));
       else TW_TRY_HIP(go(ShapeF<KIND, D>()));
     } else {
@@ -742,11 +805,11 @@ LinearBackPlan linear_back_plan(int T, int K, int N, bool bf16, bool kn, int act
   size_t part = 0;
   if (want_dx) {
     p.dx = split_of(bf16, kn ? kAlong : kAcross, false, K, T, N, 1);
-    part = p.dx.part;
+    part = p.dx.ws;
   }
   if (want_dw) {
     p.dw = kn ? split_of(bf16, kBoth, false, N, K, T, 1) : split_of(bf16, kBoth, false, K, N, T, 1);
-    part = p.dw.part > part ? p.dw.part : part;
+    part = p.dw.ws > part ? p.dw.ws : part;
   }
   p.part = take(part);
   p.bytes = take.at;
@@ -813,7 +876,7 @@ GatedPlan gated_plan(int T, int d, int f, bool bf16) {
   p.h = take((size_t)T * f * (bf16 ? 2 : 4));
   p.up = split_of(bf16, kAlong, true, f, T, d, 1);
   p.down = split_of(bf16, kAcross, false, d, T, f, 1);
-  p.part = take(p.up.part > p.down.part ? p.up.part : p.down.part);
+  p.part = take(p.up.ws > p.down.ws ? p.up.ws : p.down.ws);
   p.bytes = take.at;
   return p;
 }
@@ -833,9 +896,9 @@ GatedBackPlan gated_back_plan(int T, int d, int f, bool bf16, bool bias) {
   p.dx = split_of(bf16, kAcross, false, d, T, 2 * (int64_t)f, 1);
   p.dw = split_of(bf16, kBoth, false, d, f, T, 3);
   if (bias) p.sums = take((size_t)sum_blocks(bf16, kAlong, p.dh, T) * 2 * f * 4);
-  size_t part = p.dh.part;
-  if (p.dx.part > part) part = p.dx.part;
-  if (p.dw.part > part) part = p.dw.part;
+  size_t part = p.dh.ws;
+  if (p.dx.ws > part) part = p.dx.ws;
+  if (p.dw.ws > part) part = p.dw.ws;
   p.part = take(part);
   p.bytes = take.at;
   return p;
@@ -901,7 +964,7 @@ template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream
 }  // namespace
 
 size_t linear_fwd_workspace(int T, int K, int N, int bf16, bool kn) {
-  return split_of(bf16, kn ? kAcross : kAlong, false, N, T, K, 1).part;
+  return split_of(bf16, kn ? kAcross : kAlong, false, N, T, K, 1).ws;
 }
 size_t linear_bwd_workspace(int T, int K, int N, int bf16, bool kn, int act, bool dx, bool dw, bool db) {
   return linear_back_plan(T, K, N, bf16, kn, act, dx, dw, db).bytes;

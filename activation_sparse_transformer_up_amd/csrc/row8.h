@@ -57,4 +57,25 @@ template <typename T> TW_DEV float rounded(float v) {
   else return __uint_as_float(pack_bf16(0.f, v) & 0xFFFF0000u);
 }
 
+// Splits 8 fp32 values into three bf16 planes, hi + mid + lo = v (24 bits; rounded to nearest,
+// so mid and lo are at most 2^-8 and 2^-17 of v). The largest finite values would round to infinity
+// and leave inf - inf: their hi is cut off instead. An infinite v has NaN in mid and lo.
+TW_DEV void split8(const float (&v)[8], uint16_t *p, int64_t plane) {
+  float h[8], r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    h[k] = rounded<uint16_t>(v[k]);
+    if (__builtin_isinf(h[k])) h[k] = __uint_as_float(__float_as_uint(v[k]) & 0xFFFF0000u);
+    r[k] = v[k] - h[k];
+  }
+  store8(p, h);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    h[k] = rounded<uint16_t>(r[k]);
+    r[k] -= h[k];
+  }
+  store8(p + plane, h);
+  store8(p + 2 * plane, r);
+}
+
 }  // namespace tw

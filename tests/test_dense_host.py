@@ -82,9 +82,9 @@ def test_gated_bwd(kw, want):
 
 
 def test_workspaces():
-    """What the header says they hold: operands of the next product, and at most 256 MB of partial sums
-    (and the column sums' blocks)."""
-    L, rng, cap = tw.lib(), random.Random(3), (256 << 20) + 4096
+    """What the header says they hold: operands of the next product, at most 256 MB of partial sums, the planes
+    of one product's fp32 operands, the column sums' blocks."""
+    L, rng = tw.lib(), random.Random(3)
     assert L.linear_fwd_workspace_bytes(0, 64, 64, 1, 0) == 0 and L.linear_fwd_workspace_bytes(4, 60, 64, 1, 0) == 0
     assert L.linear_fwd_workspace_bytes(4, 64, 64, 1, 2) == 0 and L.linear_bwd_workspace_bytes(4, 64, 64, 1, 0, 9, 1, 1, 1) == 0
     assert L.ffn_gated_dense_fwd_workspace_bytes(4, 64, 64, 3) == 0 and L.ffn_gated_dense_bwd_workspace_bytes(-1, 64, 64, 1, 0) == 0
@@ -92,10 +92,12 @@ def test_workspaces():
         T, K, N = int(2 ** rng.uniform(0, 24)), 8 * int(2 ** rng.uniform(0, 17)), 8 * int(2 ** rng.uniform(0, 17))
         dt, lay, act = rng.randint(0, 1), rng.randint(0, 1), rng.randint(0, 4)
         n = T * N * (2 if dt else 4)
+        cap = (256 << 20) + 8192 + (0 if dt else 6 * (T * (K + N) + 2 * K * N))
         assert L.linear_fwd_workspace_bytes(T, K, N, dt, lay) <= cap
         assert L.linear_bwd_workspace_bytes(T, K, N, dt, lay, act, 1, 1, 0) <= n * (act > 0) + cap
         sums = (T // 16 + 1024) * N * 4
         assert L.linear_bwd_workspace_bytes(T, K, N, dt, lay, act, 0, 0, 1) <= sums
+        cap += 0 if dt else 6 * 3 * (T * (K + N) + K * N)
         assert n <= L.ffn_gated_dense_fwd_workspace_bytes(T, K, N, dt) <= n + cap
         assert 3 * n <= L.ffn_gated_dense_bwd_workspace_bytes(T, K, N, dt, 0) <= 3 * n + cap
         assert L.ffn_gated_dense_bwd_workspace_bytes(T, K, N, dt, 1) <= 3 * n + cap + 2 * sums
