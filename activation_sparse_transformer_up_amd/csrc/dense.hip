@@ -155,7 +155,7 @@ template <typename T, bool SUMS> struct EpiGluBack {
   T *dg, *du, *h;
   int64_t ldy;
   int act;
-  float *sums;
+  float *sums, *out[2];                     // out: the sums themselves, from a single strip
   struct Col {};
   struct Row {
     Raw8<T> g, u;
@@ -207,7 +207,7 @@ template <typename T> struct EpiDz {
   T *dz;
   int64_t ldy;
   int act;
-  float *sums;
+  float *sums, *out[2];                     // out: the sums themselves, from a single strip
   struct Col {};
   struct Row {
     Raw8<T> z;
@@ -412,11 +412,13 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
 
 // The epilogue over rows of partial sums, or of a matrix v (EpiDz): a workgroup takes 256 columns of a
 // strip of `strip` rows, thread t the 8 columns 8 (t % 32) of every eighth row. Its sums go to
-// sums[4 strip's number + t / 64], the two rows of a wave added.
+// sums[4 strip's number + t / 64], the two rows of a wave added; a single strip's sums are the result (one
+// launch less).
 template <typename T, class E>
 __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ part, int S, int batch, const T *__restrict__ v,
                                                     int64_t ldv, int N, int M, int strip, E e) {
   constexpr int DU = E::DUAL ? 2 : 1, UR = 4;             // rows in flight
+  __shared__ __attribute__((aligned(16))) float red[E::NSUM > 0 ? 4 : 1][256];
   const int m0 = blockIdx.x * 256, n0 = blockIdx.y * strip, b = blockIdx.z, c = (threadIdx.x & 31) * 8;
   const bool ok = c < M - m0;
   const int end = ok ? min(N - n0, strip) : 0;
@@ -469,14 +471,22 @@ __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ pa
       }
     }
     if constexpr (E::NSUM > 0) {
-      if (e.sums)
+      if (!e.sums) return;
 #pragma unroll
-        for (int j = 0; j < E::NSUM; ++j) {
+      for (int j = 0; j < E::NSUM; ++j) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], 32, 64);
-          if (ok && (threadIdx.x & 32) == 0)
-            keep8(e.sums + ((int64_t)(blockIdx.y * 4 + (threadIdx.x >> 6)) * E::NSUM + j) * M + m0 + c, sum[j]);
+        for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], 32, 64);
+        const bool mine = (threadIdx.x & 32) == 0;
+        if (gridDim.y > 1) {
+          if (ok && mine) keep8(e.sums + ((int64_t)(blockIdx.y * 4 + (threadIdx.x >> 6)) * E::NSUM + j) * M + m0 + c, sum[j]);
+        } else {
+          if (mine) keep8(&red[threadIdx.x >> 6][c], sum[j]);
+          __syncthreads();
+          const int t = threadIdx.x;
+          if (e.out[j] && t < M - m0) e.out[j][m0 + t] = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
+          __syncthreads();
         }
+      }
     }
   });
 }
@@ -645,8 +655,9 @@ Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batc
 
 int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 
-// Rows of a strip of k_dense_rows: for column sums few strips, whose sums are added afterwards.
+// Rows of a strip of k_dense_rows: for column sums few strips, whose sums are added afterwards, one up to 256 rows.
 int strip_of(int N, bool sums) {
+  if (sums && N <= 256) return (int)(ceil_div(N, 8) * 8);
   const int64_t r = ceil_div(N, sums ? 64 : 1024);
   return (int)(ceil_div(r, 8) * 8);
 }
@@ -843,8 +854,9 @@ template <typename T> hipError_t linear_bwd_run(const LinearBackArgs &a, hipStre
       lddz = a.N;
     }
     if (a.db) e.sums = (float *)(ws + p.sums);
+    e.out[0] = a.db;
     TW_TRY_HIP(launch_rows(prod_of(a.N, a.T, 0), (const T *)a.dy, a.lddy, e, s));
-    if (a.db) TW_TRY_HIP(add_sums(e.sums, 4 * row_strips(a.T, true), a.N, 1, a.db, nullptr, s));
+    if (a.db && row_strips(a.T, true) > 1) TW_TRY_HIP(add_sums(e.sums, 4 * row_strips(a.T, true), a.N, 1, a.db, nullptr, s));
   }
   if (a.dx) {
     Prod q = prod_of(a.K, a.T, a.N);
@@ -937,11 +949,14 @@ template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream
     e.dg = dg; e.du = du; e.h = h;
     e.ldy = a.f; e.act = a.act;
     if (bias) e.sums = (float *)(ws + p.sums);
+    e.out[0] = a.dbg;
+    e.out[1] = a.dbu;
     return product<T, kAlong>(q, p.dh, ws + p.part, e, s);
   };
   if (bias) {
     TW_TRY_HIP(back(std::true_type()));
-    TW_TRY_HIP(add_sums((const float *)(ws + p.sums), sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
+    if (p.dh.S == 1 || row_strips(a.T, true) > 1)
+      TW_TRY_HIP(add_sums((const float *)(ws + p.sums), sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
   } else {
     TW_TRY_HIP(back(std::false_type()));
   }
