@@ -884,8 +884,10 @@ int linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, const v
   if (T > 0 && ((dx && !w) || (dw && !x))) return TWELL_ERR_ARG;
   int st = dense_shape(T, d_in, d_out);
   if (st || (st = dense_ld(dy, lddy, T, d_out)) || (st = dense_ld(dw ? x : nullptr, ldx, T, d_in))) return st;
-  if (!al16(dy) || !al16(x) || !al16(w) || !al16(pre) || !al16(dx) || !al16(dw) || !al16(db)) return TWELL_ERR_ALIGN;
   if (!dx && !dw && !db) return TWELL_OK;
+  if (!al16(dy) || (dw && !al16(x)) || (dx && !al16(w)) || (act != TWELL_ACT_NONE && !al16(pre)) || !al16(dx) || !al16(dw) ||
+      !al16(db))
+    return TWELL_ERR_ALIGN;
   if (T > 0) {
     st = dense_ws(workspace, workspace_bytes,
                   linear_bwd_workspace_bytes(T, d_in, d_out, dtype, w_layout, act, dx != nullptr, dw != nullptr, db != nullptr));

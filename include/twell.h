@@ -571,11 +571,14 @@ int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
  *   dbg = sum_t dg, dbu = sum_t du [f] fp32 (may be NULL)
  *
  * Products are summed in fp32. bf16: h, dg, du and dz are rounded to bf16 once, as operands of the next
- * product; biases' gradients are sums of unrounded fp32 values. The same bits on every call. A NaN or
- * infinity in a row of x, dy, g, u or residual stays in that row of y and dx. The
+ * product; biases' gradients are sums of unrounded fp32 values. fp32: large products split their operands
+ * into three bf16 parts, which carry all 24 bits, others are fp32 matrix instructions. The same bits on every
+ * call. A NaN or infinity in a row of x, dy, g, u or residual stays in that row of y and dx (an infinity may
+ * come out as NaN where the formula still has a value: large fp32 products take it in parts). The
  * workspaces (..._workspace_bytes; may be 0, then NULL is allowed) need not be initialised; they hold h,
- * or dg, du and h, or dz, in dtype, and up to 256 MB of partial sums. T == 0: the forwards do nothing, the
- * backwards write zeros to the weights' and biases' gradients.
+ * or dg, du and h, or dz, in dtype, the column sums of blocks of rows, up to 256 MB of partial sums and, of
+ * large fp32 products, the parts of one product's operands (6 bytes per element). Calls that overlap on one
+ * workspace race. T == 0: the forwards do nothing, the backwards write zeros to the weights' and biases' gradients.
  * Errors: TWELL_ERR_ARG (null, dtype, act, w_layout, one of g and u), TWELL_ERR_SHAPE (T < 0, a size <= 0,
  * ld below the row), TWELL_ERR_ALIGN (d_in, d_out, d, f, ld % 8, pointers), TWELL_ERR_WORKSPACE,
  * TWELL_ERR_UNSUPPORTED (T > 2^24; d_in, d_out, d or f > 2^20; ld > 2^21).
@@ -634,7 +637,7 @@ int ffn_gated_dense_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx
  * A norm that is NaN or infinite skips the step: nothing is written. Without a norm, a NaN or infinite
  * gradient reaches its own element, with 8-bit states its block's states too.
  * Errors: TWELL_ERR_ARG (null, dtypes, state_bits, a copy of a bf16 param; lr, weight decay, max_norm
- * negative or NaN, betas outside [0, 1), eps <= 0, step < 1; an output that overlaps another, a gradient
+ * negative or NaN, betas outside [0, 1), eps below fp32's normal range, step < 1; an output that overlaps another, a gradient
  * or the scalars: a tensor stands in the list once), TWELL_ERR_SHAPE (negative n or size), TWELL_ERR_ALIGN,
  * TWELL_ERR_UNSUPPORTED (more than 2^40 elements in all).
  *

@@ -43,6 +43,8 @@ LIN_B = dict(dy=FAKE, lddy=128, x=FAKE, ldx=64, w=FAKE, lay=0, pre=FAKE, dt=1, T
     (dict(x=MIS), ALIGN), (dict(w=MIS), ALIGN), (dict(pre=MIS), ALIGN), (dict(dx=MIS), ALIGN), (dict(dw=MIS), ALIGN),
     (dict(db=MIS), ALIGN), (dict(ws=None), WS), (dict(wb=16), WS), (dict(ws=MIS), ALIGN), (dict(T=(1 << 24) + 1), UNSUP),
     (dict(K=(1 << 20) + 8, ldx=1 << 21), UNSUP), (dict(lddy=(1 << 21) + 8), UNSUP), (dict(ldx=(1 << 21) + 8), UNSUP),
+    # what is not needed is not looked at
+    (dict(dx=None, w=MIS, wb=0), WS), (dict(dw=None, x=MIS, wb=0), WS), (dict(act=0, pre=MIS, wb=0), WS),
     # nothing wanted: nothing is read or written
     (dict(dx=None, dw=None, db=None, ws=None, wb=0), 0), (dict(dx=None, dw=None, db=None, dy=None, x=None, w=None, pre=None), 0),
 ])

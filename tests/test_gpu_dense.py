@@ -173,6 +173,65 @@ def test_linear_large(T, K, N, layout):
     run_linear(T, T, K, N, BF16, layout, "gelu", bias=True, res=True)
 
 
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("T,K,N", [(65, 1032, 1032), (300, 8192, 1024), (520, 4104, 4104), (1100, 2056, 8200), (2050, 8200, 2056),
+                                   (61, 8200, 2056), (64, 4096, 14344)])
+def test_linear_between(T, K, N, layout):
+    """Every tile, and depths split in numbers of parts that are no powers of two."""
+    run_linear(T + 1, T, K, N, BF16, layout, "relu", bias=False, res=True, stride=8)
+
+
+PLANES = [(2048, 2048, 2048), (1500, 1992, 3000), (2055, 4104, 1032)]
+
+
+def in_planes(T, K, N, layout):
+    """Whether the product splits its fp32 operands, by its workspace: 6 bytes per element of both."""
+    return tw.linear_fwd_workspace_bytes(T, K, N, F32, layout) >= 6 * K * (T + N)
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("shape", PLANES)
+def test_linear_in_planes(shape, layout):
+    assert in_planes(*shape, layout)
+    run_linear(sum(shape), *shape, F32, layout, "gelu", stride=8)
+    run_linear_back(sum(shape), *shape, F32, layout, "silu", stride=8)
+
+
+def test_planes_of_one_operand_twice():
+    """x and dy one tensor, and one memory read with two strides: every operand keeps its own planes."""
+    T, d, f = 2048, 1024, 4096
+    g = gen(77)
+    both = torch.randn(2 * T, d, generator=g, device="cuda")
+    x, dy = both[:T], both[::2]                              # the same address, rows d and 2 d apart
+    wg, wu, w2 = (weight(g, f, d, d, F32) for _ in range(3))
+    G, U = rows(g, T, f, F32), rows(g, T, f, F32)
+    for a, b in ((x, dy), (x, x)):
+        got = tw.ffn_gated_dense_bwd(b, a, wg, wu, w2, G, U)
+        want = tw.ffn_gated_dense_bwd(b.clone(), a.clone(), wg, wu, w2, G, U)
+        for s, t in zip(got[:4], want[:4]):
+            assert torch.equal(s, t)
+
+
+def test_nonfinite_rows_in_planes():
+    T, K, N = 2048, 2048, 2048
+    g = gen(5)
+    x, w = rows(g, T, K, F32), weight(g, N, K, K, F32)
+    y = tw.linear_fwd(x, w)[0]
+    keep = torch.arange(T, device="cuda") != 13
+    for bad in (float("nan"), float("inf")):
+        xb = x.clone()
+        xb[13, 5] = bad
+        yb = tw.linear_fwd(xb, w)[0]
+        assert torch.equal(yb[keep], y[keep]) and not torch.isfinite(yb[13]).any()
+    big = x.clone()
+    big[7] = 0
+    big[7, 3] = 3.4e38                                       # near the largest: no infinity from rounding
+    want = big[7].double() @ w.double().t()
+    fits = want.abs() < 1e38
+    got = tw.linear_fwd(big, w)[0][7].double()
+    assert ((got - want).abs()[fits] <= 64 * E * want.abs()[fits] + 1e-30).all() and fits.any()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("layout", ["nk", "kn"])
 @pytest.mark.parametrize("shape", SHAPES)
@@ -267,6 +326,11 @@ GATED = [(1, 8, 8), (1, 64, 4104), (2, 72, 136), (17, 1032, 520), (64, 520, 2056
 @pytest.mark.parametrize("shape", GATED)
 def test_gated(shape, dtype):
     run_gated(sum(shape), *shape, dtype)
+
+
+def test_gated_in_planes():
+    run_gated(3, 2000, 1024, 4096, F32, stride=8)
+    run_gated_back(3, 2000, 1024, 4096, F32, stride=8)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -483,3 +547,50 @@ def test_python_refusals_on_gpu():
         tw.ffn_gated_dense_fwd(x, w, w[:64], w)
     with pytest.raises(tw.TwellError):
         tw.ffn_gated_dense_fwd(x, w, w, w, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------------------ beyond 2^31 elements
+
+
+@pytest.fixture
+def much_memory():
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of free GPU memory")
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("K,N", [(4104, 64), (64, 4104)])
+def test_far_rows(K, N, layout, much_memory):
+    """x or y of 530003 x 4104: the first, middle and last rows, and the weights' gradient in 64 bits over parts."""
+    T, dtype = 530003, BF16
+    say("linear far", T, K, N, layout)
+    g = gen(K)
+    x, dy = (torch.empty(T, n, dtype=dtype, device="cuda") for n in (K, N))
+    pre = torch.empty(T, N, dtype=dtype, device="cuda")
+    for at in range(0, T, 1 << 16):
+        for t in (x, dy, pre):
+            p = t[at:at + (1 << 16)]
+            p.copy_(torch.randn(p.shape, generator=g, device="cuda"))
+    w = weight(g, *((N, K) if layout == "nk" else (K, N)), K, dtype)
+    y, z = tw.linear_fwd(x, w, residual=dy, act="silu", w_layout=layout, want_pre=True)
+    dx, dw, db = tw.linear_bwd(dy, x, w, pre=pre, act="silu", w_layout=layout, want_bias=True)
+    for at in (0, (1 << 31) // 4104 - 3, T // 2, T - 9):
+        sel = slice(at, at + 9)
+        check_linear(x[sel], w, layout, None, dy[sel], "silu", y[sel], z[sel])
+        d = act64(pre[sel].double(), "silu")[1]
+        dz = dy[sel].double() * d
+        th = 32 * E * dy[sel].double().abs() + (2 * E + half(dtype)) * dz.abs()
+        near(dx[sel], *product(dz, (w if layout == "nk" else w.t()).double().t(), th), "dx", dtype)
+    ref, tol, one, sums = 0, 0, 0, 0
+    for at in range(0, T, 1 << 16):
+        sel = slice(at, at + (1 << 16))
+        dz = dy[sel].double() * act64(pre[sel].double(), "silu")[1]
+        e = 32 * E * dy[sel].double().abs() + 2 * E * dz.abs()
+        x64 = x[sel].double()
+        ref, tol = ref + dz.t() @ x64, tol + (e + half(dtype) * dz.abs() + (T + 4) * E * dz.abs()).t() @ x64.abs()
+        one, sums = one + dz.sum(0), sums + (e + (T + 4) * E * dz.abs()).sum(0)
+    near(dw if layout == "nk" else dw.t(), ref, tol, "dw", dtype)
+    near(db, one, sums, "db", F32)
