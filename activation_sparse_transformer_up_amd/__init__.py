@@ -714,41 +714,52 @@ def _choice(value, table, name):
     return code
 
 
-def _operand(t, name, dtype, shape, dev):
-    """Pointer of a contiguous operand, its dtype, shape and device checked (None: not given)."""
-    if t is None:
-        return None
+def _refuse(t, name, dtype, shape, dev):
+    """Raises what is wrong with an operand."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
     if t.device != dev:
         raise ValueError(f"{name} must live on {dev}")
-    return _ptr(t)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _operand(t, name, dtype, shape, dev):
+    """Pointer of a contiguous operand, its dtype, shape and device checked (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev.index or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
 def _row_operand(t, name, dtype, T, d, dev):
-    """(pointer, row stride) of a [T][d] operand, checked likewise."""
+    """(pointer, row stride) of a [T][d] operand, checked likewise; its rows may lie apart."""
     if t is None:
         return None, d
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != 2 or t.shape[0] != T:
-        raise ValueError(f"{name}: expected {[T, d]}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must live on {dev}")
-    return _rows(t, d)
+    if t.dtype != dtype or t.shape != (T, d) or t.get_device() != dev.index:
+        _refuse(t, name, dtype, (T, d), dev)
+    ld, one = t.stride()
+    if one != 1 and T > 0 and d > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), ld if T > 1 else d
 
 
 def _enqueue(name, dev, *args):
     """Calls the library on dev's current stream, with dev as the current device."""
-    if not dev.type == "cuda":
+    if dev.type != "cuda":
         raise ValueError("tensors must live on the GPU")
-    if dev.index is None or dev.index == torch._C._cuda_getDevice():
-        _check(getattr(lib(), name)(*args, _stream(dev)), name)
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        status = getattr(_LIB or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            _check(getattr(lib(), name)(*args, _stream(dev)), name)
+            status = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise TwellError(status, name)
 
 
 def _workspace(need, given, like):
@@ -892,18 +903,17 @@ def _pointers(tensors, dtypes, sizes, name, dev):
     """Host array of a list's pointers; every tensor contiguous, on dev, of one of the dtypes and its size."""
     if len(tensors) != len(sizes):
         raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(tensors)}")
-    ptrs = array.array("Q")
+    index = dev.index
     for t, n in zip(tensors, sizes):
         if t.dtype not in dtypes:
             raise TypeError(f"{name}: unsupported dtype {t.dtype}")
         if t.numel() != n:
             raise ValueError(f"{name}: expected {n} elements, got {list(t.shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name}: all tensors must live on {dev}")
+        if t.get_device() != index:
+            raise ValueError(f"{name}: all tensors must live on {dev}" if t.is_cuda else "tensors must live on the GPU")
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensors must be contiguous")
-        ptrs.append(t.data_ptr())
-    return ptrs
+    return array.array("Q", [t.data_ptr() for t in tensors])
 
 
 def _scalar(value, dtype, name, dev):
@@ -935,6 +945,8 @@ def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1
             raise ValueError("grads, m and v must match params")
         return
     dev = params[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
     sizes = array.array("q", [p.numel() for p in params])
     eight = m_scales is not None or v_scales is not None
     blocks = [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes] if eight else None
@@ -947,7 +959,8 @@ def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1
              _pointers(m_scales, f32, blocks, "m_scales", dev) if eight else None,
              _pointers(v_scales, f32, blocks, "v_scales", dev) if eight else None,
              _pointers(copies, (torch.bfloat16,), sizes, "copies", dev) if copies is not None else None,
-             sizes, array.array("i", [_dt(p.dtype) for p in params]), array.array("i", [_dt(g.dtype) for g in grads]),
+             sizes, array.array("i", [p.dtype is torch.bfloat16 for p in params]),
+             array.array("i", [g.dtype is torch.bfloat16 for g in grads]),
              array.array("d", weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n)]
     if len(lists[-1]) != n:
         raise ValueError("weight_decay: expected a number or one per tensor")
@@ -969,6 +982,8 @@ def adamw8_values(codes, scales, dtype: torch.dtype = torch.float32) -> list:
     if n == 0:
         return []
     dev = codes[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
     sizes = array.array("q", [c.numel() for c in codes])
     cp = _pointers(codes, (torch.int8, torch.uint8), sizes, "codes", dev)
     sp = _pointers(scales, (torch.float32,), [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes], "scales", dev)

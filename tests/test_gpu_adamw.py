@@ -327,7 +327,8 @@ def test_python_refusals_on_gpu():
     p, g, m, v = ([torch.ones(300, device="cuda") * k] for k in range(4))
     ok = dict(params=p, grads=g, m=m, v=v, lr=1e-3, step=1)
     st = tw.adamw8_states(p[0])
-    for kw, err in ((dict(grads=[g[0][:299]]), ValueError), (dict(grads=[g[0].half()]), TypeError), (dict(m=[m[0].bfloat16()]), TypeError),
+    for kw, err in ((dict(grads=[g[0][:299]]), ValueError), (dict(grads=[]), ValueError), (dict(weight_decay=[0.1, 0.1]), ValueError),
+                    (dict(v=[v[0].int()]), TypeError), (dict(m_scales=[st[1]]), ValueError), (dict(grads=[g[0].half()]), TypeError), (dict(m=[m[0].bfloat16()]), TypeError),
                     (dict(m=[m[0].cpu()]), ValueError), (dict(params=[torch.ones(20, 15, device="cuda").t()]), ValueError),
                     (dict(m=[st[0]], v=[st[2]], m_scales=[st[1]]), ValueError), (dict(m_scales=[st[1]], v_scales=[st[3]]), TypeError),
                     (dict(m=[st[0]], v=[st[2]], m_scales=[st[1]], v_scales=[st[3][:1]]), ValueError),
