@@ -916,6 +916,15 @@ def _pointers(tensors, dtypes, sizes, name, dev):
     return array.array("Q", [t.data_ptr() for t in tensors])
 
 
+def _copies(copies, sizes, dev):
+    """The same of the bf16 copies, some of which may be None."""
+    if len(copies) != len(sizes):
+        raise ValueError(f"copies: expected {len(sizes)} tensors, got {len(copies)}")
+    given = [(c, n) for c, n in zip(copies, sizes) if c is not None]
+    ptrs = iter(_pointers([c for c, _ in given], (torch.bfloat16,), [n for _, n in given], "copies", dev))
+    return array.array("Q", [0 if c is None else next(ptrs) for c in copies])
+
+
 def _scalar(value, dtype, name, dev):
     """(host value, device pointer) of a number or a one-element GPU tensor."""
     if not isinstance(value, torch.Tensor):
@@ -934,7 +943,7 @@ def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1
                max_norm: float = 1.0, copies=None, m_scales=None, v_scales=None) -> None:
     """One AdamW step over lists of tensors, in place. params and grads fp32 or bf16; the states m and v fp32,
     or 8-bit codes (int8 and uint8) with m_scales and v_scales (see adamw8_states); copies: bf16 tensors
-    that take the new values of fp32 params. step counts this step, from 1; weight_decay is a number or one
+    that take the new values of fp32 params (None: of none, or as an entry of that one). step counts this step, from 1; weight_decay is a number or one
     per tensor; lr and step may be GPU scalars (fp32, int64), which a captured step reads on every replay.
     norm: grad_norm's result over all gradients; they are then scaled by min(1, max_norm / (norm + 1e-6)), and a
     norm that is not finite skips the step. A tensor may be listed once only (TwellError)."""
@@ -958,7 +967,7 @@ def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1
              _pointers(v, (torch.uint8,) if eight else f32, sizes, "v", dev),
              _pointers(m_scales, f32, blocks, "m_scales", dev) if eight else None,
              _pointers(v_scales, f32, blocks, "v_scales", dev) if eight else None,
-             _pointers(copies, (torch.bfloat16,), sizes, "copies", dev) if copies is not None else None,
+             _copies(copies, sizes, dev) if copies is not None else None,
              sizes, array.array("i", [p.dtype is torch.bfloat16 for p in params]),
              array.array("i", [g.dtype is torch.bfloat16 for g in grads]),
              array.array("d", weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n)]

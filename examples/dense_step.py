@@ -92,14 +92,9 @@ class Adam:
         g = [grads[k] for k in self.names]
         norm = tw.grad_norm(g)
         bf16 = m.dtype == torch.bfloat16
-        order = [k for k in self.names if m.p[k].dim() == 2] if bf16 else []
-        pick = {k: i for i, k in enumerate(self.names)}
-        for part, copies in ((order, True), ([k for k in self.names if k not in order], False)):
-            at = [pick[k] for k in part]
-            tw.adamw_step([m.p[k] for k in part], [grads[k] for k in part], lr=self.lr, step=self.t, betas=(0.9, 0.95),
-                          weight_decay=[self.decay[i] for i in at], norm=norm, max_norm=self.max_norm,
-                          copies=[m.w[k] for k in part] if copies else None,
-                          **{name: [t[i] for i in at] for name, t in self.states.items()})
+        tw.adamw_step([m.p[k] for k in self.names], g, lr=self.lr, step=self.t, betas=(0.9, 0.95), weight_decay=self.decay, norm=norm,
+                      max_norm=self.max_norm, copies=[m.w[k] if m.w[k] is not m.p[k] else None for k in self.names] if bf16 else None,
+                      **self.states)
         if not bf16:
             m.refresh()
         return norm

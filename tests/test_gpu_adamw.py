@@ -169,6 +169,19 @@ def test_more_tensors_than_a_launch_takes(states):
     run(to_codes(t) if states == 8 else t, copies=True)
 
 
+def test_some_copies():
+    """A copy of every other param; the same step as without them."""
+    t = tensors(12, [300, 4097, 8, 2048])
+    e = {k: [x.clone() for x in v] for k, v in t.items()}
+    copies = [torch.zeros_like(p, dtype=BF16) if k % 2 else None for k, p in enumerate(t["params"])]
+    tw.adamw_step(**t, step=2, copies=copies, **HYPER)
+    tw.adamw_step(**e, step=2, **HYPER)
+    for a, b, c in zip(t["params"], e["params"], copies):
+        assert torch.equal(a, b) and (c is None or torch.equal(c, a.to(BF16)))
+    with pytest.raises(ValueError):
+        tw.adamw_step(**t, step=2, copies=copies[:2], **HYPER)
+
+
 @pytest.mark.parametrize("states", [32, 8])
 def test_chunks_per_workgroup(states):
     """More chunks than workgroups, of the largest size."""
