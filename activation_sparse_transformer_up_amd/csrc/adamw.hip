@@ -137,24 +137,35 @@ TW_DEV float block_scale(const float (&x)[8], float k) {
   return s < kTiny ? kTiny : s;
 }
 
-// rint(sqrt(t)), FOURTH: rint(sqrt(sqrt(t))), of correctly rounded roots (t up to 255^4). The hardware's root is
-// off by an ulp, 2^-16 of a code at most: only roots that close to a border between two codes are taken again.
-// The step of 366M elements, which spent its time on the four correct roots and the quotient of each: 1344 ->
-// 1262 us.
-template <bool FOURTH> TW_DEV float code_of(float t) {
-  float a = __builtin_amdgcn_sqrtf(t);
-  if constexpr (FOURTH) a = __builtin_amdgcn_sqrtf(a);
-  float q = rintf(a);
-  if (fabsf(a - q) > 0.4998f) q = rintf(FOURTH ? sqrtf(sqrtf(t)) : sqrtf(t));
-  return q;
+// q[i] = rint(sqrt(t[i])), FOURTH: rint(sqrt(sqrt(t[i]))), of correctly rounded roots (t up to 255^4). The
+// hardware's root is off by an ulp, 2^-14 of a code after two: only lanes with a root that close to a border between
+// two codes take their roots again. Correct roots throughout, and a quotient for the step, made the step of 366M
+// elements wait for its arithmetic: 1344 us, with hardware roots 1170.
+template <bool FOURTH> TW_DEV void codes_of(const float (&t)[8], float (&q)[8]) {
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a = __builtin_amdgcn_sqrtf(t[i]);
+    if constexpr (FOURTH) a = __builtin_amdgcn_sqrtf(a);
+    q[i] = rintf(a);
+    far = fmaxf(far, fabsf(a - q[i]));
+  }
+  if (far > 0.4999f)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = rintf(FOURTH ? sqrtf(sqrtf(t[i])) : sqrtf(t[i]));
 }
 
-// eps from which m / (sqrt(v) r + eps) is taken with the hardware's root and reciprocal, 8 2^-24 at most off
-// (below the root of a tiny v, which the hardware may flush, would count); 8-bit states only: with fp32 ones the
-// step waits for HBM either way.
-constexpr float kFastEps = 1e-12f;
+// The low bytes of four numbers.
+TW_DEV uint32_t bytes4(int a, int b, int c, int d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
+}
 
-template <typename PT, typename GT, bool EIGHT>
+// eps from which FAST takes m / (sqrt(v) r + eps) with the hardware's root and reciprocal, 8 2^-24 at most off
+// (below, the root of a tiny v, which the hardware may flush, would count); 8-bit states only: with fp32 ones
+// the step waits for HBM either way.
+constexpr double kFastEps = 1e-12;
+
+template <typename PT, typename GT, bool EIGHT, bool FAST>
 TW_DEV void step_chunk(const Table &t, int i, int64_t at, int n, float c, bool clip, const Hyper &h, float keep, float root2,
                        float rate) {
 #pragma clang fp contract(off)
@@ -184,35 +195,42 @@ TW_DEV void step_chunk(const Table &t, int i, int64_t at, int n, float c, bool c
       get8((const float *)t.m[i] + at, j, n, vec, m);
       get8((const float *)t.v[i] + at, j, n, vec, v);
     }
+    if (clip)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gv[e] *= c;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float x = gv[e];
-      if (clip) x *= c;
+      const float x = gv[e];
       m[e] = m[e] * b1 + x * a1;
       v[e] = v[e] * b2 + x * x * a2;
       float d;
-      if (EIGHT && eps >= kFastEps) d = m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * root2 + eps);
+      if constexpr (FAST) d = m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * root2 + eps);
       else d = m[e] / (sqrtf(v[e]) * root2 + eps);
       pv[e] = pv[e] * keep - d * rate;
-      if (j + e >= n) m[e] = v[e] = 0.f;    // not of the block
     }
+    if (j + 8 > n)                          // elements that are not the tensor's are not of the block
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e >= n) m[e] = v[e] = 0.f;
     put8(p, j, n, vec, pv);
     if (copy) put8(copy, j, n, vec, pv);
     if constexpr (EIGHT) {
       const float sm = block_scale(m, kStepM), sv = block_scale(v, kStepV);
       const float im = 1.f / sm, iv = 1.f / sv;
-      uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
+      float r[8], q[8];
+      int o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        int q = (int)fminf(code_of<false>(fabsf(m[e]) * im), 127.f);
-        q = m[e] < 0.f ? -q : q;
-        int r = (int)fminf(code_of<true>(v[e] * iv), 255.f);
-        r = v[e] > 0.f && r == 0 ? 1 : r;
-        (e < 4 ? qm.x : qm.y) |= (uint32_t)(q & 0xFF) << (8 * (e & 3));
-        (e < 4 ? qv.x : qv.y) |= (uint32_t)r << (8 * (e & 3));
-      }
-      put_codes((uint8_t *)t.m[i] + at, j, n, vec, qm);
-      put_codes((uint8_t *)t.v[i] + at, j, n, vec, qv);
+      for (int e = 0; e < 8; ++e) r[e] = fabsf(m[e]) * im;
+      codes_of<false>(r, q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (int)copysignf(fminf(q[e], 127.f), m[e]);
+      put_codes((uint8_t *)t.m[i] + at, j, n, vec, make_uint2(bytes4(o[0], o[1], o[2], o[3]), bytes4(o[4], o[5], o[6], o[7])));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = v[e] * iv;
+      codes_of<true>(r, q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (int)fminf(v[e] > 0.f ? fmaxf(q[e], 1.f) : q[e], 255.f);
+      put_codes((uint8_t *)t.v[i] + at, j, n, vec, make_uint2(bytes4(o[0], o[1], o[2], o[3]), bytes4(o[4], o[5], o[6], o[7])));
       if ((threadIdx.x & 31) == 0 && j < n) {
         t.ms[i][blk] = sm;
         t.vs[i][blk] = sv;
@@ -224,7 +242,7 @@ TW_DEV void step_chunk(const Table &t, int i, int64_t at, int n, float c, bool c
   }
 }
 
-template <bool EIGHT> __global__ __launch_bounds__(kNT) void k_adamw(Table t, Hyper h) {
+template <bool EIGHT, bool FAST> __global__ __launch_bounds__(kNT) void k_adamw(Table t, Hyper h) {
 #pragma clang fp contract(off)
   float c = 1.f;
   if (h.norm) {
@@ -249,11 +267,11 @@ template <bool EIGHT> __global__ __launch_bounds__(kNT) void k_adamw(Table t, Hy
     const float keep = (float)(1.0 - lr * t.decay[i]);
     const bool clip = h.norm != nullptr;
     if (t.p_bf16[i]) {
-      if (t.g_bf16[i]) step_chunk<uint16_t, uint16_t, EIGHT>(t, i, at, n, c, clip, h, keep, root2, rate);
-      else step_chunk<uint16_t, float, EIGHT>(t, i, at, n, c, clip, h, keep, root2, rate);
+      if (t.g_bf16[i]) step_chunk<uint16_t, uint16_t, EIGHT, FAST>(t, i, at, n, c, clip, h, keep, root2, rate);
+      else step_chunk<uint16_t, float, EIGHT, FAST>(t, i, at, n, c, clip, h, keep, root2, rate);
     } else {
-      if (t.g_bf16[i]) step_chunk<float, uint16_t, EIGHT>(t, i, at, n, c, clip, h, keep, root2, rate);
-      else step_chunk<float, float, EIGHT>(t, i, at, n, c, clip, h, keep, root2, rate);
+      if (t.g_bf16[i]) step_chunk<float, uint16_t, EIGHT, FAST>(t, i, at, n, c, clip, h, keep, root2, rate);
+      else step_chunk<float, float, EIGHT, FAST>(t, i, at, n, c, clip, h, keep, root2, rate);
     }
   }
 }
@@ -338,8 +356,9 @@ hipError_t launch_adamw(const AdamArgs &a, hipStream_t s) {
       t.vec[k] = (((uintptr_t)t.p[k] | (uintptr_t)t.g[k] | (uintptr_t)t.copy[k] | (uintptr_t)t.m[k] | (uintptr_t)t.v[k]) & 15) == 0;
     });
     if (!grid) continue;
-    if (a.eight) k_adamw<true><<<grid, kNT, 0, s>>>(t, h);
-    else k_adamw<false><<<grid, kNT, 0, s>>>(t, h);
+    if (!a.eight) k_adamw<false, false><<<grid, kNT, 0, s>>>(t, h);
+    else if (a.eps >= kFastEps) k_adamw<true, true><<<grid, kNT, 0, s>>>(t, h);
+    else k_adamw<true, false><<<grid, kNT, 0, s>>>(t, h);
     TW_TRY_HIP(hipGetLastError());
   }
   return hipSuccess;

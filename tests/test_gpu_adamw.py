@@ -157,7 +157,8 @@ def test_clipped(states, norm, max_norm):
 
 @pytest.mark.parametrize("states", [32, 8])
 @pytest.mark.parametrize("step,hyper", [(1, {}), (2, dict(betas=(0.0, 0.0))), (100000, dict(betas=(0.99, 0.9999))), (3, dict(lr=0.0)),
-                                        (5, dict(eps=1e-3)), (1 << 40, {})])
+                                        (5, dict(eps=1e-3)), (1 << 40, {}),
+                                        (4, dict(eps=1e-20)), (4, dict(eps=1.2e-38))])
 def test_hyper(states, step, hyper):
     t = tensors(3, [700, 4100])
     run(to_codes(t) if states == 8 else t, step=step, wd=0.0, **hyper)
