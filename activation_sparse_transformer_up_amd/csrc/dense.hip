@@ -19,7 +19,12 @@
 // the next product; sums, biases, activations and residuals are fp32.
 //
 // Products with fewer tiles than the CUs can hold split k; the fp32 partial sums are added in a fixed
-// order by k_dense_rows, which runs the same epilogue.
+// order by k_dense_rows, which runs the same epilogue. (Splits that meet in the product's kernel, the last to
+// arrive adding the others' tiles, save that launch but wait three times for memory behind the stream of
+// weights: 1 x 14336 by 4096 across k in 4 splits 25 us so, 30 met.)
+//
+// fp32 operands of large products are split into three bf16 planes first (six products, 24 bits); the
+// others run on the fp32 matrix instructions.
 #include "act.h"
 #include "launch.h"
 #include "mm.h"
@@ -572,7 +577,8 @@ Tile tile_of(bool wide, int kind, int c, bool dual) {      // wide: bf16 operand
 // large, one split): 1000 x 2048 by 8192: 54 / 34 / 42, 45 / 36 / 44; 4096 x 2048 by 8192: 202 / 128 / 109, 171 / 141 /
 // 106; 2048 x 4096 by 4096 across: 87 / 65 / 79; 1000 x 8192 by 2048 in four splits: 60 / 43 / 55, 60 / 46 / 57. Few rows
 // (small / narrow): 1 x 4096 by 14336 along k 26.2 / 23.3, 64 rows 28.4 / 40; across it, 64 x 14336 by 4096 in 256
-// workgroups: small 38, narrow 37, deep 31; one row small 34, narrow 25, deep 26.
+// workgroups: small 38, narrow 37, deep 31; one row small 34, narrow 25, deep 26. fp32 as it is / in planes: 2048 x
+// 2048 by 2048 146 / 116, 4096 x 2048 by 2048 276 / 193, 2255 x 1648 by 6120 388 / 275, 997 x 1000 by 5456 (dual) 122 / 142.
 struct Cost {
   int per_cu, stage, alone, start;
 };
