@@ -561,6 +561,7 @@ template <int KIND, bool DUAL> struct ShapeF {            // fp32 as it is
 template <bool DUAL> struct ShapeFew { typedef AsMMF<MMF<128, 32, false, false, DUAL>> G; };
 
 constexpr int kCUs = 256;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kPartBytes = (int64_t)256 << 20;        // partial sums of one product
 struct Tile { int m, n, wn; };              // columns, rows, rows of a wave
 Tile tile_of(bool wide, int kind, int c, bool dual) {      // wide: bf16 operands or planes
@@ -585,17 +586,19 @@ struct Cost {
 constexpr Cost kCostAlong[4] = {{2, 330, 210, 2000}, {2, 840, 460, 4000}, {1, 1400, 1080, 8000}, {2, 270, 160, 1500}};     // 64-k stages
 constexpr Cost kCostAcross[3] = {{2, 600, 590, 4500}, {1, 460, 390, 5000}, {1, 740, 530, 8000}};                        // 32-k stages
 constexpr Cost kCostBoth[3] = {{2, 680, 620, 3500}, {}, {1, 740, 540, 8000}};
-constexpr Cost kCostF = {1, 500, 550, 2000};                                        // fp32 as it is: 32-k stages
+constexpr Cost kCostF = {3, 540, 690, 2000};                                        // fp32 as it is: 32-k stages
 constexpr int kJoin = 6000;                 // the launch that adds partial sums, the host's part among it
 constexpr double kStream = 5500;            // bytes per nanosecond from HBM
 int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
+  // fp32 as it is, three per CU: the matrix instructions of a CU's workgroups take turns, whatever their rounds
+  // (1000 x 2728 by 1000, 256 tiles, in 1 / 2 / 3 splits: 65 / 60 / 58 us; 300 x 8192 by 1024, 80 tiles, in 1 / 3 / 6: 176 / 66 / 58)
+  if (c.per_cu == 3) return stages * (c.stage * ceil_div(tiles, kCUs) + c.alone - c.stage) + c.start;
   const int64_t slots = kCUs * c.per_cu, left = tiles % slots;
   double more = left * 2 > slots ? (double)(left * 2 - slots) / slots : 0.0;
   if (c.per_cu > 1 && more > 0.0) more = 0.75 + 0.25 * more;          // some CUs have two: the others wait for them
   return tiles / slots * (stages * c.stage + c.start) +
          (left ? (int64_t)(stages * (c.alone + (c.stage - c.alone) * more)) + c.start : 0);
 }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Split {
   int cls, S, ks;
