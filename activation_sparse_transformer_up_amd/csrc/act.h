@@ -1,6 +1,6 @@
 // The activations of the dense layers and their derivatives, in fp32. Two precisions: for fp32
-// operands the device library's functions (errors of a few 2^-24 of the value); for bf16 operands,
-// whose results are rounded to 2^-8, forms on the hardware's exp2 and reciprocal, 1 ulp each, which
+// operands or results the device library's functions (errors of a few 2^-24 of the value); for bf16 operands
+// with results that are rounded to 2^-8, forms on the hardware's exp2 and reciprocal, 1 ulp each, which
 // keep their errors near 2^-23 of the larger of 1 and |z| (column sums of gradients stay fp32).
 #pragma once
 #include "common.h"
