@@ -943,10 +943,12 @@ def adamw_step(params, grads, m, v, lr, step, betas=(0.9, 0.999), eps: float = 1
                max_norm: float = 1.0, copies=None, m_scales=None, v_scales=None) -> None:
     """One AdamW step over lists of tensors, in place. params and grads fp32 or bf16; the states m and v fp32,
     or 8-bit codes (int8 and uint8) with m_scales and v_scales (see adamw8_states); copies: bf16 tensors
-    that take the new values of fp32 params (None: of none, or as an entry of that one). step counts this step, from 1; weight_decay is a number or one
-    per tensor; lr and step may be GPU scalars (fp32, int64), which a captured step reads on every replay.
-    norm: grad_norm's result over all gradients; they are then scaled by min(1, max_norm / (norm + 1e-6)), and a
-    norm that is not finite skips the step. A tensor may be listed once only (TwellError)."""
+    that take the new values of fp32 params (None: of none, or as an entry of that one). step counts this step,
+    from 1; weight_decay is a number or one per tensor; lr and step may be GPU scalars (fp32, int64), which a captured
+    step reads on every replay; values there that would be refused as numbers (a step below 1, an lr that is negative
+    or not finite) skip the step. norm: grad_norm's result over all gradients; they are then scaled by min(1,
+    max_norm / (norm + 1e-6)), and a norm that is not finite skips the step. A tensor may be listed once only
+    (TwellError)."""
     params, grads = list(params), list(grads)
     n = len(params)
     if n == 0:

@@ -30,6 +30,7 @@ constexpr int kNT = 256;
 constexpr int kGridMax = 2048;              // workgroups of a launch (8 per CU)
 constexpr float kClipEps = 1e-6f;
 constexpr float kTiny = 0x1p-126f;
+constexpr double kMaxRate = 1e30;           // as the host's check of lr
 constexpr float kStepM = (float)(1.0 / 16129.0), kStepV = (float)(1.0 / 4228250625.0);    // 127^-2, 255^-4
 
 struct Table {
@@ -247,7 +248,7 @@ template <bool EIGHT, bool FAST> __global__ __launch_bounds__(kNT) void k_adamw(
   float c = 1.f;
   if (h.norm) {
     const float nv = *h.norm;
-    if (!(fabsf(nv) < INFINITY)) return;    // no step from gradients that overflowed
+    if (!(nv >= 0.f && nv < INFINITY)) return;      // no step from gradients that overflowed
     c = h.max_norm / (nv + kClipEps);
     c = c > 1.f ? 1.f : c;
   }
@@ -256,6 +257,7 @@ template <bool EIGHT, bool FAST> __global__ __launch_bounds__(kNT) void k_adamw(
   if (h.lr_dev || h.step_dev) {
     if (h.lr_dev) lr = (double)*h.lr_dev;
     const int64_t step = h.step_dev ? *h.step_dev : h.step;
+    if (!(lr >= 0.0 && lr <= kMaxRate) || step < 1) return;         // what the host refuses would spoil every parameter
     root2 = (float)(1.0 / sqrt(1.0 - pow_int(h.beta2, step)));
     rate = (float)(lr / (1.0 - pow_int(h.beta1, step)));
   }

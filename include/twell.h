@@ -634,7 +634,8 @@ int ffn_gated_dense_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx
  * m and v.
  * lr and step are host values, or, where lr_dev or step_dev is given, device scalars read by the
  * kernel (a captured step replays with the values that they then hold). step >= 1 counts this step.
- * A norm that is NaN or infinite skips the step: nothing is written. Without a norm, a NaN or infinite
+ * A norm that is NaN, infinite or negative skips the step: nothing is written; so do a step_dev below 1 and an lr_dev
+ * that is NaN, negative or above 1e30, as the host's values are refused. Without a norm, a NaN or infinite
  * gradient reaches its own element, with 8-bit states its block's states too.
  * Errors: TWELL_ERR_ARG (null, dtypes, state_bits, a copy of a bf16 param; lr, weight decay, max_norm
  * negative or NaN, betas outside [0, 1), eps below fp32's normal range, step < 1; an output that overlaps another, a gradient
