@@ -157,3 +157,38 @@ def test_whole_numbers(case, other):
         run_gated(T, K, N, TYPES[t], "relu" if other else "none")
     else:
         run_gated_back(T, K, N, TYPES[t], "relu" if other else "none")
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("K,N", [(4104, 64), (64, 4104)])
+def test_far_rows(K, N, layout):
+    """x or y, dz and dx of 530003 x 4104, beyond 2^31 elements: every output, the sums over all rows among them."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of free GPU memory")
+    T, step = 530003, 1 << 16
+    say("exact far", T, K, N, layout)
+    g = gen(K)
+    x, dy, pre = (torch.empty(T, n, dtype=BF16, device="cuda") for n in (K, N, N))
+    for at in range(0, T, step):
+        for t in (x, dy, pre):
+            p = t[at:at + step]
+            p.copy_(torch.randint(-3, 4, p.shape, generator=g, device="cuda"))
+    w = whole(g, *((N, K) if layout == "nk" else (K, N)), 3, 1, BF16)
+    w64 = (w if layout == "nk" else w.t()).double()
+    y, z = tw.linear_fwd(x, w, residual=dy, act="relu", w_layout=layout, want_pre=True)
+    dx, dw, db = tw.linear_bwd(dy, x, w, pre=pre, act="relu", w_layout=layout, want_bias=True)
+    assert 9.0 * T < LIMIT
+    sums, one = 0, 0
+    for at in range(0, T, step):
+        sel = slice(at, at + step)
+        x64 = x[sel].double()
+        want = product(x64, w64)
+        same(z[sel], want, ("pre", at))
+        same(y[sel], want.clamp(min=0) + dy[sel].double(), ("y", at))
+        dz = dy[sel].double() * (pre[sel] > 0)
+        same(dx[sel], product(dz, w64.t()), ("dx", at))
+        sums, one = sums + dz.t() @ x64, one + dz.sum(0)
+    assert bool((sums != 0).any()) and bool((one != 0).any())
+    same(dw if layout == "nk" else dw.t(), sums, "dw")
+    same(db, one, "db")
