@@ -36,17 +36,22 @@ Tile tile_of(bool wide, int kind, int c, bool dual) {      // wide: bf16 operand
 // 2048 by 2048 146 / 116, 4096 x 2048 by 2048 276 / 193, 2255 x 1648 by 6120 388 / 275, 997 x 1000 by 5456 (dual) 122 / 142.
 struct Cost {
   int per_cu, stage, alone, start;
+  bool turns = false;                       // by cost_of
 };
 constexpr Cost kCostAlong[4] = {{2, 330, 210, 2000}, {2, 840, 460, 4000}, {1, 1400, 1080, 8000}, {2, 270, 160, 1500}};     // 64-k stages
 constexpr Cost kCostAcross[3] = {{2, 600, 590, 4500}, {1, 460, 390, 5000}, {1, 740, 530, 8000}};                        // 32-k stages
 constexpr Cost kCostBoth[3] = {{2, 680, 620, 3500}, {}, {1, 740, 540, 8000}};
-constexpr Cost kCostF = {3, 540, 690, 2000};                                        // fp32 as it is: 32-k stages
+constexpr Cost kCostF = {3, 540, 690, 2000, true};                                  // fp32 as it is: 32-k stages
+// fp32, 128 x 32: two per CU. 32 x 13768 by 6720, 53 tiles in 4 / 6 / 8 / 12 / 24 splits: 88 / 113 / 94 / 102 / 94 us, the
+// 64 x 64 tile 102 / 110 / 118 / 101 / 105; 32 x 14336 by 4096 in 1 / 4 / 8 / 16: 295 / 82 / 50 / 51, 64 x 64 298 / 83 / 50 / 61; one
+// row, where both wait for w, 191 / 57 / 45 / 46 and 193 / 56 / 45 / 51.
+constexpr Cost kCostFew = {2, 1600, 720, 2000};
 constexpr int kJoin = 6000;                 // the launch that adds partial sums, the host's part among it
 constexpr double kStream = 5500;            // bytes per nanosecond from HBM
 int64_t cost_of(const Cost &c, int64_t tiles, int64_t stages) {
-  // fp32 as it is, three per CU: the matrix instructions of a CU's workgroups take turns, whatever their rounds
+  // turns: fp32 as it is, three 64 x 64 tiles per CU: the matrix instructions of a CU's workgroups take turns, whatever their rounds
   // (1000 x 2728 by 1000, 256 tiles, in 1 / 2 / 3 splits: 65 / 60 / 58 us; 300 x 8192 by 1024, 80 tiles, in 1 / 3 / 6: 176 / 66 / 58)
-  if (c.per_cu == 3) return stages * (c.stage * ceil_div(tiles, kCUs) + c.alone - c.stage) + c.start;
+  if (c.turns) return stages * (c.stage * ceil_div(tiles, kCUs) + c.alone - c.stage) + c.start;
   const int64_t slots = kCUs * c.per_cu, left = tiles % slots;
   double more = left * 2 > slots ? (double)(left * 2 - slots) / slots : 0.0;
   if (c.per_cu > 1 && more > 0.0) more = 0.75 + 0.25 * more;          // some CUs have two: the others wait for them
@@ -87,7 +92,7 @@ Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batc
   };
   if (!bf16) {
     consider(kSmall, kCostF);
-    if (kind == kAlong && N <= 32) consider(kNarrow, kCostF);
+    if (kind == kAlong && N <= 32) consider(kNarrow, kCostFew);
     // planes: six products of twice the bytes, 10 bytes moved per element before them
     if (N > 128) {
       const int64_t more = 16000 + elements * 10 / 5000;

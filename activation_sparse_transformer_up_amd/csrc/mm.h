@@ -405,7 +405,7 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
 // element is read once, as 4 bytes, where the planes take 10 to be made and 12 to be read): for few
 // rows and small products. A workgroup of four waves computes BM x BN (64 where an operand lies across
 // k), a wave 32 x 32, of which 16-column parts of B that do not exist are left out; a stage holds 32 k,
-// four stages in a ring. The k of the four lane groups g of an instruction may be any four, the same
+// NS stages in a ring (four, or three where three workgroups share a CU). The k of the four lane groups g of an instruction may be any four, the same
 // for both operands: instruction j of half h takes k = 16 h + 4 g + j, so that along k a lane reads its
 // four j in one load. In LDS, without bank conflicts:
 //   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
@@ -439,7 +439,7 @@ template <bool TR> TW_DEV f32x4_t mmf_frag(const char *st, int r0, int h, int la
   }
 }
 
-// acc += A B^T over k in [0, K), as mm_loop. A step waits for its stage, loads the one that is three
+// acc += A B^T over k in [0, K), as mm_loop. A step waits for its stage, loads the one that is NS - 1
 // ahead into the place of the last step's, and multiplies.
 template <class G> TW_DEV void mmf_loop(const MmfOperand &A, const MmfOperand &B, int K, f32x4_t (&acc)[2][2], char *smem) {
   constexpr uint32_t OOB = 0x80000000u;

@@ -93,3 +93,15 @@ def test_splits_cover_k(plan):
         assert ks % 64 == 0 and 1 <= S <= 64 and (S - 1) * ks < K <= S * ks
         assert S == 1 or S * batch * M * (1 + dual) * N * 4 <= 256 << 20
         assert not (b and planes) and blocks >= 1
+
+
+def test_few_fp32_rows_fit_their_places(plan):
+    """The 128 x 32 tile takes 80 KB of LDS, two per CU: its splits stay within the 512 places that there are."""
+    rng = random.Random(5)
+    rows = [(0, 0, dual, 8 * rng.randint(1, 1800), rng.randint(1, 32), 8 * rng.randint(8, 1800), 1) for _ in range(3000) for dual in (0, 1)]
+    seen = 0
+    for (_, _, dual, M, N, K, _), (cls, S, _, planes, _) in zip(rows, plan(rows)):
+        if CLASSES[cls] == "narrow" and S > 1:
+            seen += 1
+            assert -(-M * (1 + dual) // 128) * S <= 512, (M, N, K, S)
+    assert seen > 100
