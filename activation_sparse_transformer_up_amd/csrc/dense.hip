@@ -419,16 +419,17 @@ template <class G, class E, int GM> __global__ __launch_bounds__(G::NT) void k_d
   });
 }
 
-// The epilogue over rows of partial sums, or of a matrix v (EpiDz): a workgroup takes 256 columns of a
-// strip of `strip` rows, thread t the 8 columns 8 (t % 32) of every eighth row. Its sums go to
-// sums[4 strip's number + t / 64], the two rows of a wave added; a single strip's sums are the result (one
-// launch less).
-template <typename T, class E>
+// The epilogue over rows of partial sums, or of a matrix v (EpiDz): a workgroup takes 8 CG columns of a strip of
+// `strip` rows, thread t the 8 columns 8 (t % CG) of every RG-th row, RG = 256 / CG. Its sums go to sums[4 strip's
+// number + t / 64], the rows of a wave added; a single strip's sums are the result (one launch less), for which 64
+// columns a workgroup (CG = 8) leave a thread a quarter of the rows that 256 do.
+template <int CG, typename T, class E>
 __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ part, int S, int batch, const T *__restrict__ v,
                                                     int64_t ldv, int N, int M, int strip, E e) {
   constexpr int DU = E::DUAL ? 2 : 1, UR = 4;             // rows in flight
-  __shared__ __attribute__((aligned(16))) float red[E::NSUM > 0 ? 4 : 1][256];
-  const int m0 = blockIdx.x * 256, n0 = blockIdx.y * strip, b = blockIdx.z, c = (threadIdx.x & 31) * 8;
+  constexpr int RG = 256 / CG;
+  __shared__ __attribute__((aligned(16))) float red[E::NSUM > 0 ? 4 : 1][CG * 8];
+  const int m0 = blockIdx.x * (CG * 8), n0 = blockIdx.y * strip, b = blockIdx.z, c = threadIdx.x % CG * 8;
   const bool ok = c < M - m0;
   const int end = ok ? min(N - n0, strip) : 0;
   const int64_t plane = (int64_t)batch * N * M * DU;
@@ -439,9 +440,9 @@ __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ pa
     typename E::Col k;
     if (ok) e.col(c, k);
     float sum[2][8] = {};
-    int r = threadIdx.x >> 5;
+    int r = threadIdx.x / CG;
     if (part) {
-      for (; r < end; r += 8) {
+      for (; r < end; r += RG) {
         typename E::Row q;
         q.load(e, r, c);
         float x[8] = {}, x2[8] = {};
@@ -461,21 +462,21 @@ __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ pa
         e.template put<decltype(ACT)::value>(r, c, k, q, x, x2, sum);
       }
     } else {
-      for (; r < end; r += 8 * UR) {
+      for (; r < end; r += RG * UR) {
         typename E::Row q[UR];
         Raw8<T> raw[UR];
 #pragma unroll
         for (int i = 0; i < UR; ++i)
-          if (r + 8 * i < end) {
-            raw[i].load(v + (r + 8 * i) * ldv + c);
-            q[i].load(e, r + 8 * i, c);
+          if (r + RG * i < end) {
+            raw[i].load(v + (r + RG * i) * ldv + c);
+            q[i].load(e, r + RG * i, c);
           }
 #pragma unroll
         for (int i = 0; i < UR; ++i)
-          if (r + 8 * i < end) {
+          if (r + RG * i < end) {
             float x[8];
             raw[i].to(x);
-            e.template put<decltype(ACT)::value>(r + 8 * i, c, k, q[i], x, x, sum);
+            e.template put<decltype(ACT)::value>(r + RG * i, c, k, q[i], x, x, sum);
           }
       }
     }
@@ -484,15 +485,17 @@ __global__ __launch_bounds__(256) void k_dense_rows(const float *__restrict__ pa
 #pragma unroll
       for (int j = 0; j < E::NSUM; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], 32, 64);
-        const bool mine = (threadIdx.x & 32) == 0;
+        for (int o = CG; o < 64; o <<= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[j][i] += __shfl_xor(sum[j][i], o, 64);
+        const bool mine = (threadIdx.x & 63) < CG;
         if (gridDim.y > 1) {
           if (ok && mine) keep8(e.sums + ((int64_t)(blockIdx.y * 4 + (threadIdx.x >> 6)) * E::NSUM + j) * M + m0 + c, sum[j]);
         } else {
           if (mine) keep8(&red[threadIdx.x >> 6][c], sum[j]);
           __syncthreads();
           const int t = threadIdx.x;
-          if (e.out[j] && t < M - m0) e.out[j][m0 + t] = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
+          if (e.out[j] && t < CG * 8 && t < M - m0) e.out[j][m0 + t] = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
           __syncthreads();
         }
       }
@@ -564,9 +567,15 @@ int grid8(int64_t tiles) { return (int)((tiles + 7) / 8 * 8); }
 template <typename T, class E>
 hipError_t launch_rows(const Prod &a, const T *v, int64_t ldv, const E &e, hipStream_t s) {
   const bool sums = E::NSUM > 0 && e.sums;
-  const dim3 grid((unsigned)ceil_div(a.M, 256), row_strips(a.N, sums), a.batch);
-  k_dense_rows<T, E><<<grid, 256, 0, s>>>(v ? nullptr : a.part, a.S, a.batch, v, ldv, a.N, a.M, strip_of(a.N, sums), e);
-  return hipGetLastError();
+  auto go = [&](auto cg) {
+    constexpr int CG = decltype(cg)::value;
+    const dim3 grid((unsigned)ceil_div(a.M, CG * 8), row_strips(a.N, sums, !v), a.batch);
+    k_dense_rows<CG, T, E><<<grid, 256, 0, s>>>(v ? nullptr : a.part, a.S, a.batch, v, ldv, a.N, a.M, strip_of(a.N, sums, !v), e);
+    return hipGetLastError();
+  };
+  if constexpr (E::NSUM > 0)
+    if (sums && narrow_strip(a.N, a.M, !v)) return go(std::integral_constant<int, 8>());
+  return go(std::integral_constant<int, 32>());
 }
 
 // One product (a's shape and operands set) by plan p; ws: room for p.ws bytes.
@@ -703,7 +712,7 @@ LinearBackPlan linear_back_plan(int T, int K, int N, bool bf16, bool kn, int act
   LinearBackPlan p = {};
   Take take;
   if (act != kActNone && (want_dx || want_dw)) p.dz = take((size_t)T * N * (bf16 ? 2 : 4));
-  if (want_db) p.sums = take((size_t)4 * row_strips(T, true) * N * 4);
+  if (want_db) p.sums = take((size_t)4 * row_strips(T, true, false) * N * 4);
   size_t part = 0;
   if (want_dx) {
     p.dx = split_of(bf16, kn ? kAlong : kAcross, false, K, T, N, 1);
@@ -747,7 +756,7 @@ template <typename T> hipError_t linear_bwd_run(const LinearBackArgs &a, hipStre
     if (a.db) e.sums = (float *)(ws + p.sums);
     e.out[0] = a.db;
     TW_TRY_HIP(launch_rows(prod_of(a.N, a.T, 0), (const T *)a.dy, a.lddy, e, s));
-    if (a.db && row_strips(a.T, true) > 1) TW_TRY_HIP(add_sums(e.sums, 4 * row_strips(a.T, true), a.N, 1, a.db, nullptr, s));
+    if (a.db && row_strips(a.T, true, false) > 1) TW_TRY_HIP(add_sums(e.sums, 4 * row_strips(a.T, true, false), a.N, 1, a.db, nullptr, s));
   }
   if (a.dx) {
     Prod q = prod_of(a.K, a.T, a.N);
@@ -846,7 +855,7 @@ template <typename T> hipError_t gated_bwd_run(const GatedBackArgs &a, hipStream
   };
   if (bias) {
     TW_TRY_HIP(back(std::true_type()));
-    if (p.dh.S == 1 || row_strips(a.T, true) > 1)
+    if (p.dh.S == 1 || row_strips(a.T, true, true) > 1)
       TW_TRY_HIP(add_sums((const float *)(ws + p.sums), sum_blocks(bf16, kAlong, p.dh, a.T), a.f, 2, a.dbg, a.dbu, s));
   } else {
     TW_TRY_HIP(back(std::false_type()));

@@ -121,17 +121,25 @@ Split split_of(bool bf16, int kind, bool dual, int M, int N, int64_t K, int batc
   return best;
 }
 
-// Rows of a strip of k_dense_rows: for column sums few strips, whose sums are added afterwards, one up to 256 rows.
-int strip_of(int N, bool sums) {
-  if (sums && N <= 256) return (int)(ceil_div(N, 8) * 8);
+// Rows of a strip of k_dense_rows; join: over partial sums of k. For column sums few strips, whose sums a further
+// launch adds; one strip, without that launch, up to 256 rows (128 of a join, whose rows cost as many reads as there
+// are splits). One strip's workgroups take 64 columns, where those of 256 would not be one per CU. us on the GPU, one
+// strip of 256 columns a workgroup / of 64 / strips of 8 rows: db of 128 x 1024, bf16 gelu 8.5 / 4.0 / 5.7, fp32 gelu 21 / 7.1 /
+// 6.4, fp32 relu 6.7 / 3.6 / 5.6; 256 x 14336, bf16 gelu 15 / 6.1 / 11, fp32 40 / 13 / 14; 256 x 60000 20 / 18 / 24 and 47 / 33 /
+// 36; 16 rows 4.7 / 4.7 / 5.5. Gated backward with biases, joins of splits: fp32 64 x 1024 x 4096 70 / 63 / 64, 128 x 1000 x 2728
+// 104 / 83 / 80 (the host's part of a launch is 4), 200 x 4096 x 1024 173 / 142 / 135, 256 x 4096 x 2048 298 / 271 / 263.
+int strip_of(int N, bool sums, bool join) {
+  if (sums && N <= (join ? 128 : 256)) return (int)(ceil_div(N, 8) * 8);
   const int64_t r = ceil_div(N, sums ? 64 : 1024);
   return (int)(ceil_div(r, 8) * 8);
 }
-int row_strips(int N, bool sums) { return (int)ceil_div(N, strip_of(N, sums)); }
+int row_strips(int N, bool sums, bool join) { return (int)ceil_div(N, strip_of(N, sums, join)); }
+// Whether a single strip's workgroups take 64 columns of M.
+bool narrow_strip(int N, int M, bool join) { return row_strips(N, true, join) == 1 && N > 16 && ceil_div(M, 256) < kCUs; }
 
 // Blocks of column sums that a product's epilogue leaves.
 int sum_blocks(bool bf16, int kind, const Split &p, int N) {
-  if (p.S > 1) return 4 * row_strips(N, true);
+  if (p.S > 1) return 4 * row_strips(N, true, true);
   const Tile t = tile_of(bf16 || p.planes, kind, p.cls, false);
   return (int)(ceil_div(N, t.n) * (t.n / t.wn));
 }

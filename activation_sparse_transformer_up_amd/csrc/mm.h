@@ -405,9 +405,9 @@ TW_DEV void mm_loop64(const MmOperand &A, const MmOperand &B, int K, f32x4_t (&a
 // element is read once, as 4 bytes, where the planes take 10 to be made and 12 to be read): for few
 // rows and small products. A workgroup of four waves computes BM x BN (64 where an operand lies across
 // k), a wave 32 x 32, of which 16-column parts of B that do not exist are left out; a stage holds 32 k,
-// NS stages in a ring (four, or three where three workgroups share a CU). The k of the four lane groups g of an instruction may be any four, the same
-// for both operands: instruction j of half h takes k = 16 h + 4 g + j, so that along k a lane reads its
-// four j in one load. In LDS, without bank conflicts:
+// NS stages in a ring (four, or three where three workgroups share a CU). The k of the four lane groups
+// g of an instruction may be any four, the same for both operands: instruction j of half h takes k = 16 h
+// + 4 g + j, so that along k a lane reads its four j in one load. In LDS, without bank conflicts:
 //   along k:   row r at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7), as in mm_loop64
 //   across k:  k row j at 256 j, its 64-byte chunk c at c ^ ((j >> 2) & 3)
 template <int BM_, int BN_, bool ATR_, bool BTR_, bool DUAL_ = false, int NS_ = 4> struct MMF {

@@ -17,6 +17,10 @@ using namespace tw;
 int main() {
   int bf16, kind, dual, M, N, batch;
   long long K;
+  for (int T = 1; T <= 256; ++T)            // rows that a thread adds up for the column sums
+    for (int cols = 8; cols <= 1 << 20; cols *= 2)
+      for (int join = 0; join < 2; ++join)
+        printf("# %d %d %d %d\n", T, cols, join, (strip_of(T, true, join) + 7) / (narrow_strip(T, cols, join) ? 32 : 8));
   while (scanf("%d %d %d %d %d %lld %d", &bf16, &kind, &dual, &M, &N, &K, &batch) == 7) {
     const Split p = split_of(bf16, kind, dual, M, N, K, batch);
     printf("%d %d %d %d %d\n", p.cls, p.S, p.ks, (int)p.planes, sum_blocks(bf16, kind, p, N));
@@ -40,7 +44,9 @@ def plan(tmp_path_factory):
         """(class, S, ks, planes, blocks of column sums) of every (bf16, kind, dual, M, N, K, batch)."""
         text = "".join("%d %d %d %d %d %d %d\n" % r for r in rows)
         out = subprocess.run([str(d / "plan")], input=text, capture_output=True, text=True, check=True).stdout
-        return [tuple(map(int, line.split())) for line in out.splitlines()]
+        lines = out.splitlines()
+        ask.strips = [tuple(map(int, line[1:].split())) for line in lines if line[0] == "#"]
+        return [tuple(map(int, line.split())) for line in lines if line[0] != "#"]
     return ask
 
 
@@ -105,3 +111,13 @@ def test_few_fp32_rows_fit_their_places(plan):
             seen += 1
             assert -(-M * (1 + dual) // 128) * S <= 512, (M, N, K, S)
     assert seen > 100
+
+
+def test_column_sums_of_few_rows(plan):
+    """A thread adds up at most 8 rows of up to 256, 4 where each row is itself a sum over the splits of k, unless the
+    columns alone fill the CUs."""
+    plan([])
+    assert len(plan.strips) == 256 * 18 * 2
+    for T, cols, join, rows in plan.strips:
+        if cols < 65536:
+            assert rows <= (4 if join else 8), (T, cols, join, rows)
