@@ -16,7 +16,10 @@
 //   - dh is never written: the epilogue reads g and u and leaves dg, du and h, the next products' operands;
 //   - column sums (db) are taken from the fp32 values, per wave and then over the waves in a fixed order.
 // h, dg, du (and dz where there is an activation) are rounded to the operands' type once, as operands of
-// the next product; sums, biases, activations and residuals are fp32.
+// the next product; sums, biases, activations and residuals are fp32. In bf16 that rounding and the result's make
+// the error 0.0023 of the result in the root mean square where the result's alone makes 0.0017 (gated backward of
+// 16384 x 4096 x 14336 against 64 bits; 0.0019 behind a residual); parts of h that kept its digits would double the
+// products that read it.
 //
 // Products with fewer tiles than the CUs can hold split k; the fp32 partial sums are added in a fixed
 // order by k_dense_rows, which runs the same epilogue. (Splits that meet in the product's kernel, the last to

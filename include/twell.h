@@ -570,6 +570,10 @@ int grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
  *   dx = dg wg + du wu [T][d];  dwg = dg^T x, dwu = du^T x, dw2 = (act(g) u)^T dy [f][d]    in dtype
  *   dbg = sum_t dg, dbu = sum_t du [f] fp32 (may be NULL)
  *
+ * Activations are within 3 2^-24 of the larger of 1 and |z|, their derivatives within 4 2^-24, before a result's own
+ * rounding. An fp32 y has the same activation for bf16 as for fp32 operands; results in bf16, and the gradients of bf16
+ * operands, take shorter forms within the same bounds, of which gelu's tail loses digits of its own value (0.2% at
+ * -5, 1% at -8, where it is 5e-15).
  * Products are summed in fp32. bf16: h, dg, du and dz are rounded to bf16 once, as operands of the next
  * product; biases' gradients are sums of unrounded fp32 values. fp32: large products split their operands
  * into three bf16 parts, which carry all 24 bits, others are fp32 matrix instructions. The same bits on every
